@@ -1,4 +1,5 @@
-"""ctypes binding of libattn_gb300.so (include/attn_bwd.h, include/attn_diag.h).
+"""ctypes binding of libattn_gb300.so (include/attn_bwd.h, include/attn_diag.h; the serving
+operators of include/attn_cache.h are called from cache.py).
 
 Argument marshalling only: torch tensors are turned into pointers and element
 strides, outputs and workspace are allocated with torch (device memory), and
@@ -65,7 +66,9 @@ EXPORTS = ("attn_fwd", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main", "attn
            "attn_bwd_host_varlen_buffer_size", "attn_bwd_ex", "attn_fwd_ex",
            "attn_check_device_status",
            "attn_set_wait_timeout_ns", "attn_last_error", "attn_version", "attn_diag_mma",
-           "attn_diag_wait_timeout", "attn_diag_tanh")
+           "attn_diag_wait_timeout", "attn_diag_tanh", "attn_rope", "attn_cache_append",
+           "attn_decode", "attn_decode_workspace_size", "attn_cache_evict",
+           "attn_cache_evict_workspace_size")
 
 
 def lib() -> ctypes.CDLL:
@@ -127,6 +130,23 @@ def lib() -> ctypes.CDLL:
         L.attn_diag_tanh.restype = _I
         L.attn_diag_wait_timeout.argtypes = [ctypes.c_int64, _P]
         L.attn_diag_wait_timeout.restype = _I
+        # the serving operators (cache.py); structures are passed as packed bytes
+        q64, f32 = ctypes.c_int64, ctypes.c_float
+        L.attn_rope.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]
+        L.attn_rope.restype = _I
+        L.attn_cache_append.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
+                                        q64, _P, _P]
+        L.attn_cache_append.restype = _I
+        L.attn_decode.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, f32, _P, _P, _I, _P, _P, _P, q64,
+                                  _P, ctypes.c_size_t, _P]
+        L.attn_decode.restype = _I
+        L.attn_decode_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I]
+        L.attn_decode_workspace_size.restype = ctypes.c_size_t
+        L.attn_cache_evict.argtypes = [_P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P,
+                                       q64, _P, ctypes.c_size_t, _P]
+        L.attn_cache_evict.restype = _I
+        L.attn_cache_evict_workspace_size.argtypes = [_I, _I, _I, _I]
+        L.attn_cache_evict_workspace_size.restype = ctypes.c_size_t
         _lib = L
         return L
 

@@ -18,6 +18,7 @@
 #include <string>
 
 #include "../../include/attn_bwd.h"
+#include "cache.h"
 #include "internal.h"
 
 namespace attn {
@@ -46,8 +47,10 @@ int cuda_fail(cudaError_t e, const char* what) {
 }
 
 // Device status words: [0] = 0 or the site of a bounded wait that gave up;
-// [1] = 0 or the code of a failed cu_seqlens validation.
-__device__ unsigned int g_device_status[2] = {0u, 0u};
+// [1] = 0 or the code of a failed cu_seqlens validation;
+// [2] = 0 or the code of a bad length, page or offset met by a serving operator
+// (reported, but it stops no later call).
+__device__ unsigned int g_device_status[3] = {0u, 0u, 0u};
 
 namespace {
 constexpr int kMaxDevices = 64;
@@ -482,11 +485,11 @@ int attn_check_device_status(attn_stream_t stream) {
   g_err.clear();
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-  unsigned int v[2] = {0u, 0u};
+  unsigned int v[3] = {0u, 0u, 0u};
   e = cudaMemcpyFromSymbol(v, g_device_status, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e, "read device status");
-  if (v[0] != 0 || v[1] != 0) {
-    const unsigned int zero[2] = {0u, 0u};
+  if (v[0] != 0 || v[1] != 0 || v[2] != 0) {
+    const unsigned int zero[3] = {0u, 0u, 0u};
     e = cudaMemcpyToSymbol(g_device_status, zero, sizeof(zero));
     if (e != cudaSuccess) return cuda_fail(e, "clear device status");
     if (v[1] != 0) {
@@ -495,6 +498,12 @@ int attn_check_device_status(attn_stream_t stream) {
                          : v[1] == 0xB0000006u ? "seqused_k"
                                                : "cu_seqlens";
       return fail(ATTN_ERR_ARG, "%s failed device-side validation (code 0x%08x)", what, v[1]);
+    }
+    if (v[0] == 0) {
+      const char* what = v[2] == kBadPage     ? "a block_table entry names no page"
+                         : v[2] == kBadLength ? "seqlens: a length or slot out of range"
+                                              : "cu_seqlens of an append";
+      return fail(ATTN_ERR_ARG, "%s (device-side check, code 0x%08x)", what, v[2]);
     }
     return fail(ATTN_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (site 0x%08x)", v[0]);
   }
