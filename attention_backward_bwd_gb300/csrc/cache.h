@@ -75,7 +75,14 @@ struct DecodeParams {
   float* w_out;
   int64_t w_stride;
   float* lse2;     // workspace: [batch][h_q] base-2 log-sum-exp (+inf: no keys)
-  float* logits;   // workspace: [batch][h_q][max_seqlen] base-2 logits (weights only)
+  float* logits;   // workspace: [batch][h_q][logit_stride] base-2 logits from the first
+                   // key seen on (weights only, else nullptr)
+  int64_t logit_stride;
+  float* parts;    // workspace: two partials of each run of tiles
+  int64_t part_stride;  // floats of a partial
+  int part_rows;        // its rows of O (maxima and sums follow them)
+  int head_tiles;       // 16-row tiles of a group
+  FastDiv chunks;       // 16-byte chunks of a row
   unsigned int* status;
 };
 
@@ -109,7 +116,8 @@ inline int evict_move_cap(int budget, int max_seqlen) {
 }
 
 struct DecodeWs {
-  size_t off_lse2, off_logits, total;
+  size_t off_lse2, off_parts, off_logits, total;
+  int64_t logit_stride;
 };
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights);
 

@@ -286,7 +286,9 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
   p.w_out = weights_out;
   p.w_stride = weights_stride;
   p.lse2 = reinterpret_cast<float*>(ws + w.off_lse2);
-  p.logits = reinterpret_cast<float*>(ws + w.off_logits);
+  p.parts = reinterpret_cast<float*>(ws + w.off_parts);
+  p.logits = weights_in != nullptr ? reinterpret_cast<float*>(ws + w.off_logits) : nullptr;
+  p.logit_stride = w.logit_stride;
   if ((rc = status_of(&p.status))) return rc;
   const cudaError_t e = launch_decode(p, dtype, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "decode launch");
