@@ -84,6 +84,7 @@ struct DecodeParams {
   int head_tiles;       // 16-row tiles of a group
   FastDiv chunks;       // 16-byte chunks of a row
   unsigned int* status;
+  int whole;            // one block a segment, nothing to join
 };
 
 struct EvictParams {

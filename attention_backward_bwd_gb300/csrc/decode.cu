@@ -7,18 +7,22 @@
 // products are kept small and synchronous and the design goes into the loads.
 //
 // Split.  Keys come in tiles of 64.  All tiles of all (sequence, head) segments form one
-// line, cut into equal runs, one per resident block: ragged lengths balance by
-// themselves, and one long sequence uses every SM.  A segment that lies inside one block
-// is finished there; one that is cut leaves (O, maximum, sum) partials which a second
-// small kernel joins.  The cut depends on the lengths alone, so results do not depend on
-// timing.
+// line, cut into equal runs, one per resident block: ragged lengths balance by themselves,
+// and one long sequence uses every SM.  A segment that lies inside one run is finished
+// there; one that is cut leaves (O, maximum, sum) partials which a second small kernel
+// joins (it is launched early and waits for the first).  The cut depends on the lengths
+// alone, so results do not depend on timing.  (More and shorter runs, taken over by blocks
+// as they finish, were slower: 425 us with one run a block, 428 with two, 432 with four for
+// 64 sequences of 4096 to 16384 keys.)  Where every segment has at most kWholeTiles tiles
+// a block takes one segment and nothing is joined.
 //
-// Block.  Four warps; tiles pass through a ring of shared-memory stages filled by 16-byte
-// asynchronous copies, several tiles ahead.  Rows are padded by 16 bytes so that ldmatrix
-// meets no bank conflict.  In a tile each warp takes the logits of 16 keys; the warps
-// share the running maximum and P through shared memory; then each warp takes a quarter
-// of the head dimension of O over all 64 keys, so the warps never join their O.
-// Row addresses (page lookups) are worked out by two warps ahead of the copies.
+// Block.  Two warps look the pages up and keep a ring of shared-memory stages filled with
+// 16-byte asynchronous copies, several tiles ahead; eight warps compute.  Rows are padded
+// by 16 bytes so that ldmatrix meets no bank conflict.  Of a tile each compute warp takes
+// the logits of 8 keys; the warps share the running maximum and P through shared memory;
+// then each takes an eighth of the columns of O over all 64 keys, so they never join O.
+// (With four warps that also did the copies, the chain of dependent steps of a tile took
+// 3100 cycles against 2600 for its loads.)
 //
 // P is rounded to the inputs' type for the P V product (half a step of relative error
 // on each, averaged by the sum); the sum itself, maxima and logits stay fp32.
@@ -32,10 +36,21 @@ namespace attn {
 namespace {
 
 constexpr int kTile = 64;       // keys of a tile
-constexpr int kThreads = 128;
+constexpr int kWarps = 8;       // compute warps
+constexpr int kCompute = kWarps * 32;
+constexpr int kCopy = 64;       // copying threads, one for each key of a tile
+constexpr int kThreads = kCompute + kCopy;
+constexpr int kJoin = 128;      // threads of a join block
 constexpr int kMaxRows = 16;    // query heads of a block
-constexpr int kLens = 512;      // lengths kept in shared memory
+constexpr int kLens = 256;      // lengths kept in shared memory
 constexpr int kPPitch = 144;    // bytes of a P row (64 keys and 16 bytes)
+
+// Runs at most: sizes the partials without asking a device.
+constexpr int kMaxRuns = 320;
+
+// Segments of at most this many tiles are taken whole: one launch instead of two (6.2 us
+// against 8.2 for one sequence of 128 keys).
+constexpr int kWholeTiles = 4;
 
 // Stages: what fits twice on an SM up to 128 columns, once above (two blocks keep the
 // loads going while one of them synchronises; wider rows have fewer, larger tiles).
@@ -47,7 +62,7 @@ struct Cfg {
   static constexpr int kBlocks = DP <= 128 ? 2 : 1;
   static constexpr int kSlots = kStages + 2;
   static constexpr int kSmem = kStages * kStageBytes + kSlots * (kTile * 16 + 32) +
-                               kMaxRows * kPPitch + 2 * 4 * kMaxRows * 4 + kLens * 4;
+                               kMaxRows * kPPitch + 2 * kWarps * kMaxRows * 4 + kLens * 4;
 };
 
 struct TileDesc {
@@ -56,7 +71,7 @@ struct TileDesc {
   uint32_t valid[2];  // bit per key of the tile
   int pad[2];
 };
-enum { kBegin = 1, kEnd = 2, kWhole = 4, kSecond = 8 };
+enum { kBegin = 1, kEnd = 2, kFull = 4, kSecond = 8, kNone = 16 };
 
 // Keys that sequence length n leaves to attend: [first, n).
 __device__ __forceinline__ int first_key(const DecodeParams& p, int n) {
@@ -82,13 +97,13 @@ struct Cut {
 };
 
 // Block-wide exclusive prefix of the tiles of the sequences: every thread owns `per`
-// neighbouring ones.  Returns this thread's prefix; `mine` its own tiles.  Starts and
-// ends with a barrier.
-__device__ __forceinline__ long long scan_tiles(const DecodeParams& p, bool tell, int* lens,
-                                                long long* warp_sums, int per, long long& mine,
-                                                long long& total) {
+// neighbouring ones.  Returns this thread's prefix.  Ends with a barrier.  (The launch
+// checks that the sum stays below 2^31.)
+template <int N>
+__device__ __forceinline__ int scan_tiles(const DecodeParams& p, bool tell, int* lens,
+                                          int* warp_sums, int per, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  mine = 0;
+  int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
     if (b >= p.batch) break;
@@ -96,28 +111,36 @@ __device__ __forceinline__ long long scan_tiles(const DecodeParams& p, bool tell
     if (lens != nullptr && b < kLens) lens[b] = n;
     mine += tiles_of(p, n);
   }
-  long long x = mine;
+  int x = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, i);
+    const int y = __shfl_up_sync(0xffffffffu, x, i);
     if (lane >= i) x += y;
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  long long before = 0;
+  int before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < N / 32; ++w) {
     before += w < warp ? warp_sums[w] : 0;
     total += warp_sums[w];
   }
   return before + x - mine;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0), "l"(policy)
                : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -158,49 +181,82 @@ __device__ __forceinline__ float* partial(const DecodeParams& p, int c, int seco
   return p.parts + (static_cast<int64_t>(c) * 2 + second) * p.part_stride;
 }
 
+// The sequence that tile `r0` of the line lies in, and the tiles (of one head) before it.
+template <int N, typename Len>
+__device__ __forceinline__ int find_sequence(const DecodeParams& p, const int* pre, int per, int hv_n,
+                                             long long r0, Len len_of, int& before) {
+  int lo = 0, hi = N - 1;  // the last thread whose sequences start at or before r0
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<long long>(pre[mid]) * hv_n <= r0) lo = mid; else hi = mid - 1;
+  }
+  before = pre[lo];
+  for (int b = lo * per;; ++b) {
+    const int t = tiles_of(p, len_of(b));
+    if (r0 < static_cast<long long>(before + t) * hv_n) return b;
+    before += t;
+  }
+}
+
+// Rows of head tile hv of a sequence without keys.
+template <typename T>
+__device__ __forceinline__ void no_keys(const DecodeParams& p, int b, int hv) {
+  const int g = hv / p.head_tiles, ht = hv - g * p.head_tiles;
+  const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
+  T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h0 * p.o.sh;
+  const int chunks = p.head_dim / 8;
+  for (int i = threadIdx.x; i < hn * chunks; i += blockDim.x)
+    *reinterpret_cast<uint4*>(out + (i / chunks) * p.o.sh + (i % chunks) * 8) = make_uint4(0, 0, 0, 0);
+  if (p.lse != nullptr)
+    for (int i = threadIdx.x; i < hn; i += blockDim.x)
+      p.lse[static_cast<int64_t>(b) * p.h_q + h0 + i] = INFINITY;
+}
+
+// Barrier of the compute warps.
+__device__ __forceinline__ void compute_barrier() {
+  asm volatile("bar.sync 2, %0;" ::"n"(kCompute) : "memory");
+}
+
 template <typename T, int DP, bool EXACT>
 __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     decode_kernel(DecodeParams p) {
   using C = Cfg<DP>;
   constexpr int S = C::kStages, kPitch = C::kPitch, kSlots = C::kSlots;
-  constexpr int kSteps = DP / 16;      // k-steps of Q K^T
-  constexpr int kCols = DP / 4;        // columns of O of a warp
-  constexpr int kNt = kCols / 8;       // their n-tiles
+  constexpr int kSteps = DP / 16;       // k-steps of Q K^T
+  constexpr int kCols = DP / kWarps;    // columns of O of a warp
+  constexpr int kNt = kCols / 8;        // their n-tiles
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_sums[kThreads / 32];
-  __shared__ long long s_before;
-  __shared__ int s_b;
+  __shared__ int s_sums[kThreads / 32];
+  __shared__ int s_pre[kThreads];
   unsigned char* ring = smem;
   longlong2* rows = reinterpret_cast<longlong2*>(ring + S * C::kStageBytes);
   TileDesc* desc = reinterpret_cast<TileDesc*>(rows + kSlots * kTile);
   unsigned char* pbuf = reinterpret_cast<unsigned char*>(desc + kSlots);
-  float* smax = reinterpret_cast<float*>(pbuf + kMaxRows * kPPitch);
-  float* ssum = smax + 4 * kMaxRows;
-  int* lens = reinterpret_cast<int*>(ssum + 4 * kMaxRows);
+  float* smax = reinterpret_cast<float*>(pbuf + kMaxRows * kPPitch);  // [row][warp]
+  float* ssum = smax + kWarps * kMaxRows;
+  int* lens = reinterpret_cast<int*>(ssum + kWarps * kMaxRows);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
+  const uint32_t ring_u = smem_u32(ring);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this block's run of tiles
   const int per = (p.batch + kThreads - 1) / kThreads;
-  long long mine, total;
-  const long long before = scan_tiles(p, true, lens, s_sums, per, mine, total);
   Cut cut;
-  cut.total = total * hv_n;
-  cut.runs = static_cast<int>(min(static_cast<long long>(gridDim.x), cut.total));
-  if (static_cast<int>(blockIdx.x) >= cut.runs) return;
-  const long long r0 = cut.start(blockIdx.x), r1 = cut.start(blockIdx.x + 1);
-  if (r0 >= before * hv_n && r0 < (before + mine) * hv_n) {
-    long long at = before;
-    int b = tid * per;
-    for (;; ++b) {
-      const int t = tiles_of(p, clean_len(p, p.seqlens[b], false));
-      if (r0 < (at + t) * hv_n) break;
-      at += t;
+  if (p.whole) {
+    const int b = blockIdx.x / hv_n, n = clean_len(p, p.seqlens[b], true);
+    if (n == 0) {
+      no_keys<T>(p, b, blockIdx.x - b * hv_n);
+      return;
     }
-    s_b = b;
-    s_before = at;
+    if (tid == 0) lens[0] = n;
+  } else {
+    int total;
+    s_pre[tid] = scan_tiles<kThreads>(p, true, lens, s_sums, per, total);
+    cut.total = static_cast<long long>(total) * hv_n;
+    cut.runs = static_cast<int>(min(static_cast<long long>(gridDim.x), cut.total));
+    if (static_cast<int>(blockIdx.x) >= cut.runs) return;
   }
   // columns that no copy writes stay zero
   if (!EXACT) {
@@ -210,134 +266,168 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
   }
   __syncthreads();
 
-  // ---- the planner (warps 0 and 1, one key of a tile each): walks the run
-  int left = static_cast<int>(min(r1 - r0, 0x7fffffffLL));
-  const int n_tiles = left;
-  int cb = s_b, ch, ct, cn, cfirst, cnt;
-  bool seg_from_start;
-  int nth = 0;  // segment of the run: 0 first, then 1
-  auto load_seq = [&]() {
-    cn = cb < kLens ? lens[cb] : clean_len(p, p.seqlens[cb], false);
-    cfirst = first_key(p, cn);
-    cnt = (cn - cfirst + kTile - 1) / kTile;
-  };
-  load_seq();
-  {
-    const long long in = r0 - s_before * hv_n;
-    ch = static_cast<int>(in / cnt);
-    ct = static_cast<int>(in - static_cast<long long>(ch) * cnt);
-    seg_from_start = ct == 0;
-  }
-  int begin = 1;
-  // what plan() saw, for store_plan()
-  int pend_page = -1, pend_within = 0, pend_head = 0;
-  bool pend_live = false;
-  TileDesc pend;
-  auto plan = [&]() {  // looks one tile up and moves on
-    if (left == 0) return;
-    const int j = cfirst + ct * kTile + tid;
-    pend_live = j < cn;
-    pend_head = ch / p.head_tiles;
-    if (pend_live) {
-      const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
-      pend_within = j - n * static_cast<int>(p.cache.page.d);
-      pend_page = p.cache.table[cb * p.cache.table_stride + n];
-    }
-    const bool at_end = ct == cnt - 1;
-    pend.b = cb;
-    pend.hv = ch;
-    pend.rel = ct * kTile;
-    pend.flags = (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) |
-                 (at_end && seg_from_start ? kWhole : 0) | (nth ? kSecond : 0);
-    begin = 0;
-    --left;
-    if (left == 0) return;
-    if (!at_end) {
-      ++ct;
-      return;
-    }
-    ct = 0;
-    begin = 1;
-    nth = 1;
-    seg_from_start = true;
-    if (++ch == hv_n) {
-      ch = 0;
-      do {
-        ++cb;
-        load_seq();
-      } while (cnt == 0);
-    }
-  };
-  auto store_plan = [&](int slot) {
-    bool ok = pend_live;
-    if (ok && static_cast<unsigned>(pend_page) >= static_cast<unsigned>(p.cache.num_pages)) {
-      report(p.status, kBadPage);
-      ok = false;
-    }
-    longlong2 o = make_longlong2(-1, -1);
-    if (ok) {
-      o.x = pend_page * p.cache.k.sb + pend_within * p.cache.k.ss + pend_head * p.cache.k.sh;
-      o.y = pend_page * p.cache.v.sb + pend_within * p.cache.v.ss + pend_head * p.cache.v.sh;
-    }
-    rows[slot * kTile + tid] = o;
-    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) desc[slot].valid[warp] = bits;
-    if (tid == 0) {
-      desc[slot].b = pend.b;
-      desc[slot].hv = pend.hv;
-      desc[slot].rel = pend.rel;
-      desc[slot].flags = pend.flags;
-    }
-  };
-  const T* kbase = static_cast<const T*>(p.cache.k.ptr);
-  const T* vbase = static_cast<const T*>(p.cache.v.ptr);
-  const uint32_t ring_u = smem_u32(ring);
-  auto fetch = [&](int tile) {  // issues the copies of one tile
-    const longlong2* r = rows + (tile % kSlots) * kTile;
-    const uint32_t dst = ring_u + (tile % S) * C::kStageBytes;
-    if (EXACT) {
-      constexpr int kCh = DP / 8, kIter = kTile * kCh / kThreads;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int u = tid + i * kThreads, row = u / kCh, c = u % kCh;
-        const longlong2 o = r[row];
-        const bool ok = o.x >= 0;
-        cp_async16(dst + row * kPitch + c * 16, kbase + (ok ? o.x + c * 8 : 0), ok);
-        cp_async16(dst + (kTile + row) * kPitch + c * 16, vbase + (ok ? o.y + c * 8 : 0), ok);
-      }
+  if (warp >= kWarps) {
+    // ================================================== copies, one thread a key
+    const int key = tid - kCompute;
+    int left = 0;
+    int cb = 0, ch = 0, ct = 0, cn = 0, cfirst = 0, cnt = 0;
+    bool seg_from_start = true;
+    int nth = 0;  // segment of the run: 0 first, then 1
+    int begin = 1;
+    auto load_seq = [&](int n) {
+      cn = n;
+      cfirst = first_key(p, cn);
+      cnt = (cn - cfirst + kTile - 1) / kTile;
+    };
+    auto len_of = [&](int b) { return b < kLens ? lens[b] : clean_len(p, p.seqlens[b], false); };
+    if (p.whole) {
+      load_seq(lens[0]);
+      cb = blockIdx.x / hv_n;
+      ch = blockIdx.x - cb * hv_n;
+      left = cnt;
     } else {
-      const int total_u = kTile * static_cast<int>(p.chunks.d);
-      for (int u = tid; u < total_u; u += kThreads) {
-        const int row = static_cast<int>(p.chunks.div(u)), c = u - row * static_cast<int>(p.chunks.d);
-        const longlong2 o = r[row];
-        const bool ok = o.x >= 0;
-        cp_async16(dst + row * kPitch + c * 16, kbase + (ok ? o.x + c * 8 : 0), ok);
-        cp_async16(dst + (kTile + row) * kPitch + c * 16, vbase + (ok ? o.y + c * 8 : 0), ok);
-      }
+      const long long r0 = cut.start(blockIdx.x);
+      left = static_cast<int>(cut.start(blockIdx.x + 1) - r0);
+      int before;
+      cb = find_sequence<kThreads>(p, s_pre, per, hv_n, r0, len_of, before);
+      load_seq(len_of(cb));
+      const long long in = r0 - static_cast<long long>(before) * hv_n;
+      ch = static_cast<int>(in / cnt);
+      ct = static_cast<int>(in - static_cast<long long>(ch) * cnt);
+      seg_from_start = ct == 0;
     }
-  };
+    // what plan() saw, for store_plan()
+    int pend_page = -1, pend_within = 0, pend_head = 0;
+    bool pend_live = false;
+    TileDesc pend;
+    auto plan = [&]() {  // looks one tile up and moves on
+      if (left == 0) {
+        pend.flags = kNone;
+        pend_live = false;
+        return;
+      }
+      const int j = cfirst + ct * kTile + key;
+      pend_live = j < cn;
+      pend_head = ch / p.head_tiles;
+      if (begin) {  // the segment's queries are asked for a few tiles ahead
+        const int h = pend_head * p.group + (ch - pend_head * p.head_tiles) * kMaxRows + (key & 15);
+        if (h < (pend_head + 1) * p.group)
+          for (int i = (key >> 4) * 64; i < p.head_dim; i += 256)
+            prefetch_l2(static_cast<const T*>(p.q.ptr) + cb * p.q.sb + h * p.q.sh + i);
+      }
+      if (pend_live) {
+        const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
+        pend_within = j - n * static_cast<int>(p.cache.page.d);
+        pend_page = p.cache.table[cb * p.cache.table_stride + n];
+      }
+      const bool at_end = ct == cnt - 1;
+      pend.b = cb;
+      pend.hv = ch;
+      pend.rel = ct * kTile;
+      pend.flags = (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) |
+                   (at_end && seg_from_start ? kFull : 0) | (nth ? kSecond : 0);
+      begin = 0;
+      --left;
+      if (left == 0) return;
+      if (!at_end) {
+        ++ct;
+        return;
+      }
+      ct = 0;
+      begin = 1;
+      nth = 1;
+      seg_from_start = true;
+      if (++ch == hv_n) {
+        ch = 0;
+        do load_seq(len_of(++cb));
+        while (cnt == 0);
+      }
+    };
+    auto store_plan = [&](int slot) {
+      bool ok = pend_live;
+      if (ok && static_cast<unsigned>(pend_page) >= static_cast<unsigned>(p.cache.num_pages)) {
+        report(p.status, kBadPage);
+        ok = false;
+      }
+      longlong2 o = make_longlong2(-1, -1);
+      if (ok) {
+        o.x = pend_page * p.cache.k.sb + pend_within * p.cache.k.ss + pend_head * p.cache.k.sh;
+        o.y = pend_page * p.cache.v.sb + pend_within * p.cache.v.ss + pend_head * p.cache.v.sh;
+      }
+      rows[slot * kTile + key] = o;
+      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) desc[slot].valid[key >> 5] = bits;
+      if (key == 0) {
+        desc[slot].b = pend.b;
+        desc[slot].hv = pend.hv;
+        desc[slot].rel = pend.rel;
+        desc[slot].flags = pend.flags;
+      }
+    };
+    const T* kbase = static_cast<const T*>(p.cache.k.ptr);
+    const T* vbase = static_cast<const T*>(p.cache.v.ptr);
+    // keys and values are read once, unless a group has several head tiles: they leave
+    // the L2 first, so that logits and partials stay for the second kernel
+    const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+    auto fetch = [&](int tile) {  // issues the copies of one tile
+      const longlong2* r = rows + (tile % kSlots) * kTile;
+      const uint32_t dst = ring_u + (tile % S) * C::kStageBytes;
+      if (EXACT && kCopy % (DP / 8) == 0) {
+        constexpr int kCh = DP / 8, kStep = kCopy / kCh;
+        const int c = key % kCh, r0 = key / kCh;
+        const T *kc = kbase + c * 8, *vc = vbase + c * 8;
+        const uint32_t d0 = dst + r0 * kPitch + c * 16;
+#pragma unroll 8
+        for (int i = 0; i < kTile / kStep; ++i) {
+          const longlong2 o = r[r0 + i * kStep];
+          const bool ok = o.x >= 0;
+          cp_async16(d0 + i * kStep * kPitch, kc + (ok ? o.x : 0), ok, policy);
+          cp_async16(d0 + (kTile + i * kStep) * kPitch, vc + (ok ? o.y : 0), ok, policy);
+        }
+      } else {
+        const int total_u = kTile * static_cast<int>(p.chunks.d);
+#pragma unroll 4
+        for (int u = key; u < total_u; u += kCopy) {
+          const int row = static_cast<int>(p.chunks.div(u)), c = u - row * static_cast<int>(p.chunks.d);
+          const longlong2 o = r[row];
+          const bool ok = o.x >= 0;
+          cp_async16(dst + row * kPitch + c * 16, kbase + (ok ? o.x + c * 8 : 0), ok, policy);
+          cp_async16(dst + (kTile + row) * kPitch + c * 16, vbase + (ok ? o.y + c * 8 : 0), ok, policy);
+        }
+      }
+    };
 
-  // ---- prologue: plans for the first S tiles, copies for S - 1
-  if (warp < 2)
     for (int t = 0; t < S; ++t) {
       plan();
-      if (t < n_tiles) store_plan(t);
-      if (t == S - 1) plan();  // tile S waits in the registers
+      store_plan(t);
     }
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < S - 1; ++t) {
-    if (t < n_tiles) fetch(t);
-    cp_commit();
+    plan();  // tile S waits in the registers
+    __syncthreads();
+    for (int t = 0; t < S - 1; ++t) {
+      if (!(desc[t].flags & kNone)) fetch(t);
+      cp_commit();
+    }
+    for (int t = 0; !(desc[t % kSlots].flags & kNone); ++t) {
+      cp_wait<S - 2>();
+      __syncthreads();  // tile t is there for all; the stage of tile t - 1 is free
+      if (!(desc[(t + S - 1) % kSlots].flags & kNone)) fetch(t + S - 1);
+      cp_commit();
+      store_plan((t + S) % kSlots);
+      plan();
+    }
+    cp_wait<0>();
+    return;
   }
 
+  // ==================================================== attention
   uint32_t qf[kSteps][4];
   float o[kNt][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   const int row0 = lane >> 2, col2 = (lane & 3) * 2;
-
-  for (int t = 0; t < n_tiles; ++t) {
+  __syncthreads();
+  for (int t = 0;; ++t) {
     const TileDesc& d = desc[t % kSlots];
+    if (d.flags & kNone) break;
     if (d.flags & kBegin) {
       const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
       const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
@@ -358,87 +448,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
     }
-    cp_wait<S - 2>();
-    __syncthreads();  // tile t is there for all; stage of tile t - 1 is free
+    __syncthreads();  // tile t is there for all
 
-    if (t + S - 1 < n_tiles) fetch(t + S - 1);
-    cp_commit();
-    if (warp < 2 && t + S < n_tiles) {
-      store_plan((t + S) % kSlots);
-      plan();
-    }
-
-    // ---- logits of this warp's 16 keys
+    // ---- logits of this warp's 8 keys
     const uint32_t kst = ring_u + (t % S) * C::kStageBytes;
-    float s[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+    float s[4];
     {
-      const uint32_t a = kst + (warp * 16 + ((lane >> 4) << 3) + (lane & 7)) * kPitch + ((lane >> 3) & 1) * 16;
+      float s1[4];
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
+      for (int i = 0; i < 4; ++i) s[i] = s1[i] = 0.f;
+      const uint32_t a = kst + (warp * 8 + (lane & 7)) * kPitch + (lane >> 3) * 16;
+#pragma unroll
+      for (int k = 0; k < kSteps; k += 2) {
         uint32_t kf[4];
         ldsm4(a + k * 32, kf);
-        mma16816<T>(s[0], qf[k], kf[0], kf[1]);
-        mma16816<T>(s[1], qf[k], kf[2], kf[3]);
+        mma16816<T>(s, qf[k], kf[0], kf[1]);
+        mma16816<T>(s1, qf[k + 1], kf[2], kf[3]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += s1[i];
     }
-    const uint32_t valid = d.valid[warp >> 1] >> ((warp & 1) * 16);
-    float top[2] = {-INFINITY, -INFINITY};
+    const uint32_t valid = d.valid[warp >> 2] >> ((warp & 3) * 8 + col2);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool ok = (valid >> (n * 8 + col2 + (i & 1))) & 1u;
-        float x = p.softcap > 0.f ? p.cap_out * tanh_exp(s[n][i] * p.cap_in) : s[n][i] * p.scale_log2;
-        x = ok ? x : -INFINITY;
-        s[n][i] = x;
-        top[i >> 1] = fmaxf(top[i >> 1], x);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float x = p.softcap > 0.f ? p.cap_out * tanh_exp(s[i] * p.cap_in) : s[i] * p.scale_log2;
+      s[i] = (valid >> (i & 1)) & 1u ? x : -INFINITY;
+    }
     if (p.logits != nullptr) {
       const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
       const int hn = min(kMaxRows, p.group - ht * kMaxRows);
       const int64_t h0 = static_cast<int64_t>(d.b) * p.h_q + g * p.group + ht * kMaxRows;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (row0 + r * 8 < hn) {
-          float* out = p.logits + (h0 + row0 + r * 8) * p.logit_stride + d.rel + warp * 16 + col2;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            *reinterpret_cast<float2*>(out + n * 8) = make_float2(s[n][r * 2], s[n][r * 2 + 1]);
-        }
+        if (row0 + r * 8 < hn)
+          *reinterpret_cast<float2*>(p.logits + (h0 + row0 + r * 8) * p.logit_stride + d.rel + warp * 8 +
+                                     col2) = make_float2(s[r * 2], s[r * 2 + 1]);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      if ((lane & 3) == 0) smax[warp * kMaxRows + row0 + r * 8] = top[r];
+      float top = fmaxf(s[r * 2], s[r * 2 + 1]);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if ((lane & 3) == 0) smax[(row0 + r * 8) * kWarps + warp] = top;
     }
-    __syncthreads();
+    compute_barrier();
 
     // ---- P under the common maximum
     float scale_o[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float mx = m[r];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, smax[w * kMaxRows + row0 + r * 8]);
+      const float4 a = *reinterpret_cast<const float4*>(smax + (row0 + r * 8) * kWarps);
+      const float4 b = *reinterpret_cast<const float4*>(smax + (row0 + r * 8) * kWarps + 4);
+      const float mx = fmaxf(m[r], fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
+                                         fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w))));
       const float base = mx == -INFINITY ? 0.f : mx;
       scale_o[r] = ex2(m[r] - base);
       m[r] = mx;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float p0 = ex2(s[n][r * 2] - base), p1 = ex2(s[n][r * 2 + 1] - base);
-        sum += p0 + p1;
-        *reinterpret_cast<uint32_t*>(pbuf + (row0 + r * 8) * kPPitch +
-                                     (warp * 16 + n * 8 + col2) * 2) = Pack<T>::two(p0, p1);
-      }
-      l[r] = l[r] * scale_o[r] + sum;
+      const float p0 = ex2(s[r * 2] - base), p1 = ex2(s[r * 2 + 1] - base);
+      *reinterpret_cast<uint32_t*>(pbuf + (row0 + r * 8) * kPPitch + (warp * 8 + col2) * 2) =
+          Pack<T>::two(p0, p1);
+      l[r] = l[r] * scale_o[r] + (p0 + p1);
     }
-    __syncthreads();
+    compute_barrier();
 
     // ---- O += P V for this warp's columns
 #pragma unroll
@@ -449,19 +520,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       o[n][3] *= scale_o[1];
     }
     {
-      const uint32_t pa = smem_u32(pbuf) + ((lane & 7) + ((lane >> 3) & 1) * 8) * kPPitch + (lane >> 4) * 16;
-      const uint32_t va = kst + (kTile + (lane & 7) + ((lane >> 3) & 1) * 8) * kPitch +
-                          (warp * kCols + (lane >> 4) * 8) * 2;
+      const uint32_t pa = smem_u32(pbuf) + (lane & 15) * kPPitch + (lane >> 4) * 16;
+      const uint32_t va = kst + (kTile + lane) * kPitch + warp * kCols * 2;
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k) {
-        uint32_t pf[4];
-        ldsm4(pa + k * 32, pf);
+      for (int k = 0; k < kTile / 32; ++k) {
+        uint32_t p0[4], p1[4];
+        ldsm4(pa + k * 64, p0);
+        ldsm4(pa + k * 64 + 32, p1);
 #pragma unroll
-        for (int n = 0; n < kNt; n += 2) {
+        for (int n = 0; n < kNt; ++n) {
           uint32_t vf[4];
-          ldsm4_t(va + k * 16 * kPitch + n * 16, vf);
-          mma16816<T>(o[n], pf, vf[0], vf[1]);
-          mma16816<T>(o[n + 1], pf, vf[2], vf[3]);
+          ldsm4_t(va + k * 32 * kPitch + n * 16, vf);
+          mma16816<T>(o[n], p0, vf[0], vf[1]);
+          mma16816<T>(o[n], p1, vf[2], vf[3]);
         }
       }
     }
@@ -473,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
         float x = l[r];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if ((lane & 3) == 0) ssum[warp * kMaxRows + row0 + r * 8] = x;
+        if ((lane & 3) == 0) ssum[(row0 + r * 8) * kWarps + warp] = x;
       }
-      __syncthreads();
+      compute_barrier();
       const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
       const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
-      const bool whole = (d.flags & kWhole) != 0;
+      const bool whole = (d.flags & kFull) != 0;
       float* part = partial(p, blockIdx.x, (d.flags & kSecond) ? 1 : 0);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -486,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
         if (row >= hn) continue;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) sum += ssum[w * kMaxRows + row];
+        for (int w = 0; w < kWarps; ++w) sum += ssum[row * kWarps + w];
         const bool none = sum == 0.f;
         const float inv = none ? 0.f : 1.f / sum;
         if (whole) {
@@ -517,80 +588,83 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       }
     }
   }
-  cp_wait<0>();
 }
 
 // Joins the partials of cut segments, writes the rows of empty sequences, and adds the
-// attention weights.  Blocks [0, batch * h_q): one row of O each; then `chunks` blocks of
-// kKeys keys for every (sequence, key/value head) when weights are asked for.
+// attention weights.  The first `runs * part_rows` blocks take one row of the segment that
+// starts in their run and is cut at its end, if there is one; then come `chunks` blocks
+// of kKeys keys for every (sequence, key/value head) when weights are asked for.
 constexpr int kKeys = 1024;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) join_kernel(DecodeParams p, int runs, int dp, int chunks) {
-  __shared__ long long s_sums[kThreads / 32];
-  __shared__ long long s_before;
-  __shared__ float4 s_part[kThreads];
+__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, int row_blocks, int dp,
+                                                     int chunks) {
+  __shared__ int s_sums[kJoin / 32];
+  __shared__ int s_pre[kJoin];
+  __shared__ int s_before;
+  __shared__ float4 s_part[kJoin];
   __shared__ float s_lse[256];
+  __shared__ float s_w[kMaxRuns];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.h_q;
-  const bool is_row = blockIdx.x < rows;
-  int b, h, j0 = 0;
-  if (is_row) {
-    b = blockIdx.x / p.h_q;
-    h = blockIdx.x - b * p.h_q;
-  } else {
-    const int64_t u = blockIdx.x - rows;
-    const int bh = static_cast<int>(u / chunks);
-    j0 = static_cast<int>(u - static_cast<int64_t>(bh) * chunks) * kKeys;
-    b = bh / p.h_k;
-    h = (bh - b * p.h_k) * p.group;
-  }
-  const int n = clean_len(p, p.seqlens[b], false);
-  const int first = first_key(p, n), t_b = tiles_of(p, n);
   const int hv_n = p.h_k * p.head_tiles;
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  if (!is_row && j0 >= n) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // no block may end before the first kernel
-    return;
-  }
-  long long mine, total;
-  const long long before = scan_tiles(p, blockIdx.x == 0, nullptr, s_sums, per, mine, total);
-  if (b / per == tid) {
-    long long at = before;
-    for (int i = tid * per; i < b; ++i) at += tiles_of(p, clean_len(p, p.seqlens[i], false));
-    s_before = at;
-  }
-  __syncthreads();
-  Cut cut;
-  cut.total = total * hv_n;
-  cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
+  const int per = (p.batch + kJoin - 1) / kJoin;
   const int part_m = p.part_rows * dp;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto len_of = [&](int b) { return clean_len(p, p.seqlens[b], false); };
+  Cut cut;
 
-  if (is_row) {
-    T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
-    const int64_t at = static_cast<int64_t>(b) * p.h_q + h;
-    if (t_b == 0) {  // no keys
-      for (int d = tid; d < p.head_dim; d += kThreads) out[d] = static_cast<T>(0.f);
-      if (tid == 0 && p.lse != nullptr) p.lse[at] = INFINITY;
-      return;
+  if (static_cast<int>(blockIdx.x) < row_blocks) {
+    for (int b = blockIdx.x; b < p.batch; b += row_blocks)
+      if (clean_len(p, p.seqlens[b], runs == 0) == 0)
+        for (int hv = 0; hv < hv_n; ++hv) no_keys<T>(p, b, hv);
+    int total;
+    s_pre[tid] = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
+    cut.total = static_cast<long long>(total) * hv_n;
+    cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
+    __syncthreads();
+    const int run = blockIdx.x / p.part_rows, row = blockIdx.x - run * p.part_rows;
+    bool mine = run + 1 < cut.runs;  // a run with an end inside the line
+    int b = 0, hv = 0, nc = 0, lead = 0;
+    if (mine) {
+      const long long r0 = cut.start(run), e = cut.start(run + 1);
+      int before;
+      b = find_sequence<kJoin>(p, s_pre, per, hv_n, e - 1, len_of, before);
+      const int t_b = tiles_of(p, len_of(b));
+      const long long line0 = static_cast<long long>(before) * hv_n;
+      hv = static_cast<int>((e - 1 - line0) / t_b);
+      const long long s0 = line0 + static_cast<long long>(hv) * t_b;
+      mine = s0 >= r0 && s0 + t_b > e &&
+             row < p.group - (hv % p.head_tiles) * kMaxRows;  // starts here, goes on, has this row
+      if (mine) {
+        nc = cut.run_of(s0 + t_b - 1) - run + 1;
+        lead = r0 == s0 ? 0 : 1;  // only in its first run can the segment be the second
+      }
     }
-    const int g = h / p.group, hg = h - g * p.group, ht = hg / kMaxRows, row = hg - ht * kMaxRows;
-    const long long s0 = s_before * hv_n + static_cast<long long>(g * p.head_tiles + ht) * t_b;
-    const int c0 = cut.run_of(s0), c1 = cut.run_of(s0 + t_b - 1);
-    if (c0 == c1) return;  // finished by its run
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
+    const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
     float top = -INFINITY, sum = 0.f;
-    for (int c = c0; c <= c1; ++c)
-      top = fmaxf(top, partial(p, c, cut.start(c) >= s0 ? 0 : 1)[part_m + row]);
+    for (int i = tid; i < nc; i += kJoin) {
+      const float x = partial(p, run + i, i == 0 ? lead : 0)[part_m + row];
+      s_w[i] = x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (lane == 0) s_lse[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_lse[w]);
     const float base = top == -INFINITY ? 0.f : top;
+    __syncthreads();
     // threads: 16-byte column group, and every stripe-th run
-    const int groups = dp / 4, stripes = kThreads / groups > 0 ? kThreads / groups : 1;
+    const int groups = dp / 4, stripes = kJoin / groups;
     const int cg = tid % groups, st = tid / groups;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (st < stripes)
-      for (int c = c0 + st; c <= c1; c += stripes) {
-        const float* part = partial(p, c, cut.start(c) >= s0 ? 0 : 1);
-        const float w = ex2(part[part_m + row] - base);
+    if (st < stripes) {
+#pragma unroll 4
+      for (int i = st; i < nc; i += stripes) {
+        const float* part = partial(p, run + i, i == 0 ? lead : 0);
+        const float w = ex2(s_w[i] - base);
         const float4 x = *reinterpret_cast<const float4*>(part + row * dp + cg * 4);
         sum += w * part[part_m + kMaxRows + row];
         acc.x += w * x.x;
@@ -598,10 +672,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(DecodeParams p, int runs
         acc.z += w * x.z;
         acc.w += w * x.w;
       }
+    }
     s_part[tid] = acc;
     s_lse[tid] = sum;
     __syncthreads();
-    if (st == 0 && tid < groups) {
+    if (st == 0) {
       for (int i = 1; i < stripes; ++i) {
         const float4 x = s_part[tid + i * groups];
         acc.x += x.x;
@@ -612,6 +687,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(DecodeParams p, int runs
       }
       const bool none = sum == 0.f;
       const float inv = none ? 0.f : 1.f / sum;
+      T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
       if (cg * 4 < p.head_dim) {
         uint2 v;
         v.x = Pack<T>::two(none ? 0.f : acc.x * inv, none ? 0.f : acc.y * inv);
@@ -619,67 +695,116 @@ __global__ void __launch_bounds__(kThreads) join_kernel(DecodeParams p, int runs
         *reinterpret_cast<uint2*>(out + cg * 4) = v;
       }
       if (tid == 0 && p.lse != nullptr)
-        p.lse[at] = none ? INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+        p.lse[static_cast<int64_t>(b) * p.h_q + h] =
+            none ? INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
     }
     return;
   }
 
-  // ---- weights of keys [j0, j0 + kKeys) of one key/value head
-  const int g = h / p.group;
+  // ---- weights of keys [j0, j0 + kKeys), from the first one seen, of one key/value head
+  const int64_t u = blockIdx.x - row_blocks;
+  const int bg = static_cast<int>(u / chunks);
+  const int b = bg / p.h_k, g = bg - b * p.h_k, h = g * p.group;
+  const int n = len_of(b), first = first_key(p, n), t_b = tiles_of(p, n);
+  const int j0 = static_cast<int>(u - static_cast<int64_t>(bg) * chunks) * kKeys;
+  if (j0 >= n) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // no block may end before the first kernel
+    return;
+  }
+  int total;
+  const int before = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
+  if (b / per == tid) {
+    int at = before;
+    for (int i = tid * per; i < b; ++i) at += tiles_of(p, len_of(i));
+    s_before = at;
+  }
+  __syncthreads();
+  cut.total = static_cast<long long>(total) * hv_n;
+  cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // a thread's keys: 4 neighbours at rel, 4 at rel + kKeys / 2 (the logits' rows start at
+  // the first key seen and are whole tiles)
   const float* logits = p.logits + (static_cast<int64_t>(b) * p.h_q + h) * p.logit_stride;
-  float w[kKeys / kThreads];
+  const int rel0 = j0 + tid * 4, rel1 = rel0 + kKeys / 2, seen = n - first;
+  float w[8];
 #pragma unroll
-  for (int i = 0; i < kKeys / kThreads; ++i) w[i] = 0.f;
+  for (int i = 0; i < 8; ++i) w[i] = 0.f;
   for (int g0 = 0; g0 < p.group; g0 += 256) {
     const int gn = min(256, p.group - g0);
     __syncthreads();
-    if (t_b > 0)
-      for (int i = warp; i < gn; i += kThreads / 32) {  // the row's LSE, a warp each
-        const int hg = g0 + i, ht = hg / kMaxRows, row = hg - ht * kMaxRows;
-        const long long s0 = s_before * hv_n + static_cast<long long>(g * p.head_tiles + ht) * t_b;
-        const int c0 = cut.run_of(s0), c1 = cut.run_of(s0 + t_b - 1);
-        float lse2;
-        if (c0 == c1) {
-          lse2 = p.lse2[static_cast<int64_t>(b) * p.h_q + h + hg];
-        } else {
-          float top = -INFINITY, sum = 0.f;
-          for (int c = c0 + lane; c <= c1; c += 32)
-            top = fmaxf(top, partial(p, c, cut.start(c) >= s0 ? 0 : 1)[part_m + row]);
+    for (int i = warp; i < gn; i += kJoin / 32) {  // the row's LSE, a warp each
+      const int hg = g0 + i, ht = hg / kMaxRows, row = hg - ht * kMaxRows;
+      const long long s0 = static_cast<long long>(s_before) * hv_n +
+                           static_cast<long long>(g * p.head_tiles + ht) * t_b;
+      const int c0 = cut.run_of(s0), c1 = cut.run_of(s0 + t_b - 1);
+      float lse2;
+      if (c0 == c1) {
+        lse2 = p.lse2[static_cast<int64_t>(b) * p.h_q + h + hg];
+      } else {
+        const int lead = cut.start(c0) >= s0 ? 0 : 1;
+        float top = -INFINITY, sum = 0.f;
+        for (int c = c0 + lane; c <= c1; c += 32)
+          top = fmaxf(top, partial(p, c, c == c0 ? lead : 0)[part_m + row]);
 #pragma unroll
-          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          const float base = top == -INFINITY ? 0.f : top;
-          for (int c = c0 + lane; c <= c1; c += 32) {
-            const float* part = partial(p, c, cut.start(c) >= s0 ? 0 : 1);
-            sum += ex2(part[part_m + row] - base) * part[part_m + kMaxRows + row];
-          }
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-          lse2 = sum == 0.f ? INFINITY : base + log2f(sum);
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float base = top == -INFINITY ? 0.f : top;
+        for (int c = c0 + lane; c <= c1; c += 32) {
+          const float* part = partial(p, c, c == c0 ? lead : 0);
+          sum += ex2(part[part_m + row] - base) * part[part_m + kMaxRows + row];
         }
-        if (lane == 0) s_lse[i] = lse2;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        lse2 = sum == 0.f ? INFINITY : base + log2f(sum);
       }
+      if (lane == 0) s_lse[i] = lse2;
+    }
     __syncthreads();
+#pragma unroll 2
     for (int i = 0; i < gn; ++i) {
       const float lse2 = s_lse[i];
       const float* x = logits + (g0 + i) * p.logit_stride;
-#pragma unroll
-      for (int k = 0; k < kKeys / kThreads; ++k) {
-        const int j = j0 + k * kThreads + tid;
-        if (j >= first && j < n) w[k] += ex2(x[j - first] - lse2);
+      if (rel0 < seen) {
+        const float4 v = *reinterpret_cast<const float4*>(x + rel0);
+        w[0] += ex2(v.x - lse2);
+        w[1] += ex2(v.y - lse2);
+        w[2] += ex2(v.z - lse2);
+        w[3] += ex2(v.w - lse2);
+      }
+      if (rel1 < seen) {
+        const float4 v = *reinterpret_cast<const float4*>(x + rel1);
+        w[4] += ex2(v.x - lse2);
+        w[5] += ex2(v.y - lse2);
+        w[6] += ex2(v.z - lse2);
+        w[7] += ex2(v.w - lse2);
       }
     }
   }
   const int64_t at = (static_cast<int64_t>(b) * p.h_k + g) * p.w_stride;
+  const float* in = p.w_in + at;
+  float* out = p.w_out + at;
+  // keys before the window keep their weights
+  if (out != in)
+    for (int j = j0 + tid; j < min(first, j0 + kKeys); j += kJoin) out[j] = in[j];
 #pragma unroll
-  for (int k = 0; k < kKeys / kThreads; ++k) {
-    const int j = j0 + k * kThreads + tid;
-    if (j < n) p.w_out[at + j] = p.w_in[at + j] + w[k];
+  for (int half = 0; half < 2; ++half) {
+    const int rel = half ? rel1 : rel0, j = first + rel;
+    const float* v = w + half * 4;
+    if (rel + 3 < seen && ((reinterpret_cast<uintptr_t>(in + j) | reinterpret_cast<uintptr_t>(out + j)) & 15) == 0) {
+      float4 x = *reinterpret_cast<const float4*>(in + j);
+      x.x += v[0];
+      x.y += v[1];
+      x.z += v[2];
+      x.w += v[3];
+      *reinterpret_cast<float4*>(out + j) = x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (rel + i < seen) out[j + i] = in[j + i] + v[i];
+    }
   }
 }
 
 int pad_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
-// Resident blocks of the device at most: sizes the partials without asking a device.
-constexpr int kMaxRuns = 384;
 
 template <typename T, int DP, bool EXACT>
 cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
@@ -706,9 +831,13 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   p.part_stride = static_cast<int64_t>(p.part_rows) * dp + 2 * kMaxRows;
   p.chunks.set(static_cast<uint32_t>(p.head_dim / 8));
   const int64_t most = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles * ceil_div(p.max_seqlen, kTile);
+  if (static_cast<int64_t>(p.batch) * ceil_div(p.max_seqlen, kTile) > INT32_MAX) return cudaErrorInvalidValue;
   int64_t runs = static_cast<int64_t>(num_sms()) * (dp <= 128 ? 2 : 1);
   if (runs > kMaxRuns) runs = kMaxRuns;
   if (runs > most) runs = most;
+  p.whole = p.w_in == nullptr && p.max_seqlen <= kWholeTiles * kTile && runs > 0;
+  if (p.whole) runs = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles;
+  if (runs > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   const bool exact = dp == p.head_dim;
   if (runs > 0) {
@@ -719,19 +848,21 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     else e = exact ? launch_main<T, 256, true>(p, r, stream) : launch_main<T, 256, false>(p, r, stream);
     if (e != cudaSuccess) return e;
   }
+  if (p.whole) return cudaSuccess;
   const int chunks = p.w_in != nullptr ? ceil_div(p.max_seqlen, kKeys) : 0;
-  const int64_t blocks = static_cast<int64_t>(p.batch) * (p.h_q + static_cast<int64_t>(p.h_k) * chunks);
+  const int row_blocks = runs > 0 ? static_cast<int>(runs) * p.part_rows : 1;
+  const int64_t blocks = row_blocks + static_cast<int64_t>(p.batch) * p.h_k * chunks;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = runs > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), dp, chunks);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), row_blocks, dp, chunks);
 }
 
 }  // namespace
