@@ -47,6 +47,11 @@ int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out) {
   int rc;
   if ((rc = check_rows(&c->k, "k cache", c->num_pages, c->page_size, h_k))) return rc;
   if ((rc = check_rows(&c->v, "v cache", c->num_pages, c->page_size, h_k))) return rc;
+  // the kernels hold page and slot strides in 16-byte units of 32 bits (64 GiB a page)
+  for (const attn_tensor* t : {&c->k, &c->v})
+    if ((c->num_pages > 1 && t->stride_b / 8 > UINT32_MAX) ||
+        (c->page_size > 1 && t->stride_s / 8 > UINT32_MAX))
+      return fail(ATTN_ERR_STRIDE, "page and slot strides must stay below 2^35 elements");
   if (c->block_table == nullptr) return fail(ATTN_ERR_NULL, "block_table is NULL");
   if (!aligned(c->block_table, 4)) return fail(ATTN_ERR_ALIGN, "block_table must be 4-byte aligned");
   if (batch > 1 && c->table_stride < c->max_pages)

@@ -17,8 +17,9 @@
 // a block takes one segment and nothing is joined.
 //
 // Block.  Two warps look the pages up and keep a ring of shared-memory stages filled with
-// 16-byte asynchronous copies, several tiles ahead; eight warps compute.  Rows are padded
-// by 16 bytes so that ldmatrix meets no bank conflict.  Of a tile each compute warp takes
+// 16-byte asynchronous copies, several tiles ahead; eight warps compute.  The 16-byte chunks of
+// row r lie permuted by r % 8 inside each 128 bytes, so that neither the copies nor
+// ldmatrix meet a bank conflict (with padded rows the copies alone were 4 % slower).  Of a tile each compute warp takes
 // the logits of 8 keys; the warps share the running maximum and P through shared memory;
 // then each takes an eighth of the columns of O over all 64 keys, so they never join O.
 // (With four warps that also did the copies, the chain of dependent steps of a tile took
@@ -56,16 +57,16 @@ constexpr int kWholeTiles = 4;
 // loads going while one of them synchronises; wider rows have fewer, larger tiles).
 template <int DP>
 struct Cfg {
-  static constexpr int kPitch = DP * 2 + 16;
+  static constexpr int kPitch = DP * 2;
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = DP == 64 ? 5 : (DP == 128 ? 3 : (DP == 192 ? 4 : 3));
+  static constexpr int kStages = DP == 64 ? 6 : (DP == 128 ? 3 : (DP == 192 ? 4 : 3));
   static constexpr int kBlocks = DP <= 128 ? 2 : 1;
   static constexpr int kSlots = kStages + 2;
   static constexpr int kSmem = kStages * kStageBytes + kSlots * (kTile * 16 + 32) +
                                kMaxRows * kPPitch + 2 * kWarps * kMaxRows * 4 + kLens * 4;
 };
 
-struct TileDesc {
+struct __align__(16) TileDesc {
   int b, hv, rel;  // sequence, head tile, first key of the tile (from the first seen)
   int flags;
   uint32_t valid[2];  // bit per key of the tile
@@ -129,7 +130,13 @@ __device__ __forceinline__ int scan_tiles(const DecodeParams& p, bool tell, int*
   return before + x - mine;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real, uint64_t policy) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, long long src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "l"(policy)
+               : "memory");
+}
+// 16 bytes, or 16 zeros.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
                "r"(real ? 16 : 0), "l"(policy)
                : "memory");
@@ -179,6 +186,45 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // Partial of run c (its first or second cut segment): rows of O, then maxima and sums.
 __device__ __forceinline__ float* partial(const DecodeParams& p, int c, int second) {
   return p.parts + (static_cast<int64_t>(c) * 2 + second) * p.part_stride;
+}
+
+// Copies the rows of a tile, kLanes of the copying threads to a row.  `rows`: the addresses
+// of each key's rows of k and of v.
+// Addresses are read eight at a time before their copies are issued: a copy writes shared
+// memory, so a read behind it in program order waits until it has been issued.
+template <int DP, bool EXACT>
+__device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
+                                          int idx, const DecodeParams& p, uint64_t policy) {
+  constexpr int kLanes = DP == 64 ? 8 : (DP == 128 ? 16 : 32), kStep = kCopy / kLanes;
+  constexpr int kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
+  const int c = idx % kLanes, r0 = idx / kLanes;
+  if (c >= (EXACT ? DP / 8 : static_cast<int>(p.chunks.d))) return;
+  rows += r0;
+  dst += r0 * kPitch + ((c ^ r0) << 4);  // r0 < kStep, and kStep divides 8
+  auto at = [&](int i) { return (dst ^ (((i * kStep) & 7) << 4)) + i * kStep * kPitch; };
+  if ((valid[0] & valid[1]) == 0xffffffffu) {
+    static_assert(kIter % 8 == 0, "groups of eight rows");
+#pragma unroll
+    for (int i0 = 0; i0 < kIter; i0 += 8) {
+      longlong2 a[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = rows[(i0 + i) * kStep];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cp_async16(at(i0 + i), a[i].x + c * 16, policy);
+        cp_async16(at(i0 + i) + kTile * kPitch, a[i].y + c * 16, policy);
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < kIter; ++i) {
+      const longlong2 a = rows[i * kStep];
+      const bool ok = a.x != 0;
+      cp_async16_or_zero(at(i), ok ? a.x + c * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok, policy);
+      cp_async16_or_zero(at(i) + kTile * kPitch, ok ? a.y + c * 16 : reinterpret_cast<long long>(p.cache.v.ptr),
+                         ok, policy);
+    }
+  }
 }
 
 // The sequence that tile `r0` of the line lies in, and the tiles (of one head) before it.
@@ -262,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
   if (!EXACT) {
     const int c0 = p.head_dim / 8, nc = DP / 8 - c0;
     for (int i = tid; i < S * 2 * kTile * nc; i += kThreads)
-      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (c0 + i % nc) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ ((i / nc) & 7)) << 4)) = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
 
@@ -274,16 +320,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     bool seg_from_start = true;
     int nth = 0;  // segment of the run: 0 first, then 1
     int begin = 1;
+    // of the sequence: its keys and its table row; of the segment: the head's rows of slot 0
+    const int* table = nullptr;
+    const char *khead = nullptr, *vhead = nullptr;
     auto load_seq = [&](int n) {
       cn = n;
       cfirst = first_key(p, cn);
       cnt = (cn - cfirst + kTile - 1) / kTile;
+      table = p.cache.table + cb * p.cache.table_stride;
+    };
+    auto load_head = [&]() {
+      const int g = ch / p.head_tiles, ht = ch - g * p.head_tiles;
+      khead = reinterpret_cast<const char*>(static_cast<const T*>(p.cache.k.ptr) + g * p.cache.k.sh);
+      vhead = reinterpret_cast<const char*>(static_cast<const T*>(p.cache.v.ptr) + g * p.cache.v.sh);
+      // its queries are asked for a few tiles ahead
+      const int h = g * p.group + ht * kMaxRows + (key & 15);
+      if (h < (g + 1) * p.group)
+        for (int i = (key >> 4) * 64; i < p.head_dim; i += 256)
+          prefetch_l2(static_cast<const T*>(p.q.ptr) + cb * p.q.sb + h * p.q.sh + i);
     };
     auto len_of = [&](int b) { return b < kLens ? lens[b] : clean_len(p, p.seqlens[b], false); };
     if (p.whole) {
-      load_seq(lens[0]);
       cb = blockIdx.x / hv_n;
       ch = blockIdx.x - cb * hv_n;
+      load_seq(lens[0]);
       left = cnt;
     } else {
       const long long r0 = cut.start(blockIdx.x);
@@ -296,36 +356,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       ct = static_cast<int>(in - static_cast<long long>(ch) * cnt);
       seg_from_start = ct == 0;
     }
+    load_head();
+    // strides in 16-byte units: a page's offset is one 32 x 32 bit product
+    const uint32_t kp = static_cast<uint32_t>(p.cache.k.sb / 8), ks = static_cast<uint32_t>(p.cache.k.ss / 8);
+    const uint32_t vp = static_cast<uint32_t>(p.cache.v.sb / 8), vs = static_cast<uint32_t>(p.cache.v.ss / 8);
     // what plan() saw, for store_plan()
-    int pend_page = -1, pend_within = 0, pend_head = 0;
+    int pend_page = -1, pend_within = 0;
+    const char *pend_k = nullptr, *pend_v = nullptr;
     bool pend_live = false;
-    TileDesc pend;
+    int4 pend = make_int4(0, 0, 0, 0);
     auto plan = [&]() {  // looks one tile up and moves on
       if (left == 0) {
-        pend.flags = kNone;
+        pend.w = kNone;
         pend_live = false;
         return;
       }
       const int j = cfirst + ct * kTile + key;
       pend_live = j < cn;
-      pend_head = ch / p.head_tiles;
-      if (begin) {  // the segment's queries are asked for a few tiles ahead
-        const int h = pend_head * p.group + (ch - pend_head * p.head_tiles) * kMaxRows + (key & 15);
-        if (h < (pend_head + 1) * p.group)
-          for (int i = (key >> 4) * 64; i < p.head_dim; i += 256)
-            prefetch_l2(static_cast<const T*>(p.q.ptr) + cb * p.q.sb + h * p.q.sh + i);
-      }
+      pend_k = khead;
+      pend_v = vhead;
       if (pend_live) {
         const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
         pend_within = j - n * static_cast<int>(p.cache.page.d);
-        pend_page = p.cache.table[cb * p.cache.table_stride + n];
+        pend_page = table[n];
       }
       const bool at_end = ct == cnt - 1;
-      pend.b = cb;
-      pend.hv = ch;
-      pend.rel = ct * kTile;
-      pend.flags = (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) |
-                   (at_end && seg_from_start ? kFull : 0) | (nth ? kSecond : 0);
+      pend = make_int4(cb, ch, ct * kTile,
+                       (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) |
+                           (at_end && seg_from_start ? kFull : 0) | (nth ? kSecond : 0));
       begin = 0;
       --left;
       if (left == 0) return;
@@ -339,9 +397,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       seg_from_start = true;
       if (++ch == hv_n) {
         ch = 0;
-        do load_seq(len_of(++cb));
-        while (cnt == 0);
+        do {
+          ++cb;
+          load_seq(len_of(cb));
+        } while (cnt == 0);
       }
+      load_head();
     };
     auto store_plan = [&](int slot) {
       bool ok = pend_live;
@@ -349,54 +410,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
         report(p.status, kBadPage);
         ok = false;
       }
-      longlong2 o = make_longlong2(-1, -1);
+      longlong2 o = make_longlong2(0, 0);  // addresses of the key's row of k and of v
       if (ok) {
-        o.x = pend_page * p.cache.k.sb + pend_within * p.cache.k.ss + pend_head * p.cache.k.sh;
-        o.y = pend_page * p.cache.v.sb + pend_within * p.cache.v.ss + pend_head * p.cache.v.sh;
+        const uint32_t page = static_cast<uint32_t>(pend_page), in = static_cast<uint32_t>(pend_within);
+        o.x = reinterpret_cast<long long>(
+            pend_k + ((static_cast<uint64_t>(page) * kp + static_cast<uint64_t>(in) * ks) << 4));
+        o.y = reinterpret_cast<long long>(
+            pend_v + ((static_cast<uint64_t>(page) * vp + static_cast<uint64_t>(in) * vs) << 4));
       }
       rows[slot * kTile + key] = o;
       const uint32_t bits = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) desc[slot].valid[key >> 5] = bits;
-      if (key == 0) {
-        desc[slot].b = pend.b;
-        desc[slot].hv = pend.hv;
-        desc[slot].rel = pend.rel;
-        desc[slot].flags = pend.flags;
-      }
+      if (key == 0) *reinterpret_cast<int4*>(&desc[slot]) = pend;
     };
-    const T* kbase = static_cast<const T*>(p.cache.k.ptr);
-    const T* vbase = static_cast<const T*>(p.cache.v.ptr);
-    // keys and values are read once, unless a group has several head tiles: they leave
-    // the L2 first, so that logits and partials stay for the second kernel
+    // Keys and values are read once, unless a group has several head tiles: they leave the
+    // L2 first, so that logits and partials stay for the second kernel.
     const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-    auto fetch = [&](int tile) {  // issues the copies of one tile
-      const longlong2* r = rows + (tile % kSlots) * kTile;
-      const uint32_t dst = ring_u + (tile % S) * C::kStageBytes;
-      if (EXACT && kCopy % (DP / 8) == 0) {
-        constexpr int kCh = DP / 8, kStep = kCopy / kCh;
-        const int c = key % kCh, r0 = key / kCh;
-        const T *kc = kbase + c * 8, *vc = vbase + c * 8;
-        const uint32_t d0 = dst + r0 * kPitch + c * 16;
-#pragma unroll 8
-        for (int i = 0; i < kTile / kStep; ++i) {
-          const longlong2 o = r[r0 + i * kStep];
-          const bool ok = o.x >= 0;
-          cp_async16(d0 + i * kStep * kPitch, kc + (ok ? o.x : 0), ok, policy);
-          cp_async16(d0 + (kTile + i * kStep) * kPitch, vc + (ok ? o.y : 0), ok, policy);
-        }
-      } else {
-        const int total_u = kTile * static_cast<int>(p.chunks.d);
-#pragma unroll 4
-        for (int u = key; u < total_u; u += kCopy) {
-          const int row = static_cast<int>(p.chunks.div(u)), c = u - row * static_cast<int>(p.chunks.d);
-          const longlong2 o = r[row];
-          const bool ok = o.x >= 0;
-          cp_async16(dst + row * kPitch + c * 16, kbase + (ok ? o.x + c * 8 : 0), ok, policy);
-          cp_async16(dst + (kTile + row) * kPitch + c * 16, vbase + (ok ? o.y + c * 8 : 0), ok, policy);
-        }
-      }
-    };
-
     for (int t = 0; t < S; ++t) {
       plan();
       store_plan(t);
@@ -404,13 +433,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     plan();  // tile S waits in the registers
     __syncthreads();
     for (int t = 0; t < S - 1; ++t) {
-      if (!(desc[t].flags & kNone)) fetch(t);
+      if (!(desc[t].flags & kNone))
+        copy_rows<DP, EXACT>(rows + t * kTile, desc[t].valid, ring_u + t * C::kStageBytes, key, p, policy);
       cp_commit();
     }
     for (int t = 0; !(desc[t % kSlots].flags & kNone); ++t) {
       cp_wait<S - 2>();
       __syncthreads();  // tile t is there for all; the stage of tile t - 1 is free
-      if (!(desc[(t + S - 1) % kSlots].flags & kNone)) fetch(t + S - 1);
+      const int next = t + S - 1, slot = next % kSlots;
+      if (!(desc[slot].flags & kNone))
+        copy_rows<DP, EXACT>(rows + slot * kTile, desc[slot].valid,
+                                          ring_u + (next % S) * C::kStageBytes, key, p, policy);
       cp_commit();
       store_plan((t + S) % kSlots);
       plan();
@@ -457,11 +490,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       float s1[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = s1[i] = 0.f;
-      const uint32_t a = kst + (warp * 8 + (lane & 7)) * kPitch + (lane >> 3) * 16;
+      const uint32_t a = kst + (warp * 8 + (lane & 7)) * kPitch + (((lane >> 3) ^ (lane & 7)) << 4);
 #pragma unroll
       for (int k = 0; k < kSteps; k += 2) {
         uint32_t kf[4];
-        ldsm4(a + k * 32, kf);
+        ldsm4((a ^ ((k & 2) << 5)) + (k >> 2) * 128, kf);
         mma16816<T>(s, qf[k], kf[0], kf[1]);
         mma16816<T>(s1, qf[k + 1], kf[2], kf[3]);
       }
@@ -521,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     }
     {
       const uint32_t pa = smem_u32(pbuf) + (lane & 15) * kPPitch + (lane >> 4) * 16;
-      const uint32_t va = kst + (kTile + lane) * kPitch + warp * kCols * 2;
+      const uint32_t va = kst + (kTile + lane) * kPitch;
 #pragma unroll
       for (int k = 0; k < kTile / 32; ++k) {
         uint32_t p0[4], p1[4];
@@ -530,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
           uint32_t vf[4];
-          ldsm4_t(va + k * 32 * kPitch + n * 16, vf);
+          ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ (lane & 7)) << 4), vf);
           mma16816<T>(o[n], p0, vf[0], vf[1]);
           mma16816<T>(o[n], p1, vf[2], vf[3]);
         }
