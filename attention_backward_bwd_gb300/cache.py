@@ -11,6 +11,7 @@ current stream).
 """
 from __future__ import annotations
 
+import functools
 import struct
 from typing import Optional, Sequence, Tuple
 
@@ -24,122 +25,144 @@ _TENSOR = struct.Struct("@Pqqq")
 _PAGED = struct.Struct("@PqqqPqqqPqiii4x")
 _ROTARY = struct.Struct("@PqPii4iii")
 _OPTS = struct.Struct("@iif4xPP")
+_I32, _F32 = torch.int32, torch.float32
+# The current stream as an integer, without a Stream object around it (a call of a few
+# microseconds is mostly marshalling).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _fail(rc: int):
     raise AttnError(rc, lib().attn_last_error().decode())
 
 
-def _stream_of(stream, dev) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _call(fn, dev, stream, made, *args):
-    """Runs fn(*args, stream) with ``dev`` current.  ``made``: tensors allocated by
-    the caller; their memory is kept from reuse until ``stream`` has passed them."""
-    raw = _stream_of(stream, dev)
-    if torch.cuda.current_device() == dev.index:
+def _call(fn, index, stream, made, *args):
+    """Runs fn(*args, stream) with device ``index`` current.  ``made``: tensors
+    allocated by the caller; their memory is kept from reuse until ``stream`` has
+    passed them."""
+    raw = _raw_stream(index) if stream is None else \
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
         rc = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, raw)
     if rc != 0:
         _fail(rc)
     if stream is not None:
         other = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(raw, device=dev)
+            torch.cuda.ExternalStream(raw, device=index)
         for t in made:
             t.record_stream(other)
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
+def _first(t: torch.Tensor, name: str):
+    """(device index, dtype, dtype code) that the call's other tensors have to share."""
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise AttnError(-1, f"{name} must be float16 or bfloat16, got {t.dtype}")
-    return code
+    if not t.is_cuda:
+        raise AttnError(-9, f"{name} must be a CUDA tensor, got {t.device}")
+    return t.get_device(), t.dtype, code
 
 
-def _rows(name, t, like, dims) -> None:
-    """Device, dtype, rank and a unit stride over the head dimension."""
-    if not t.is_cuda or t.device != like.device:
-        raise AttnError(-9, f"{name} must be a CUDA tensor on {like.device}, got {t.device}")
-    if t.dtype != like.dtype:
-        raise AttnError(-1, f"{name} has dtype {t.dtype}, {like.dtype} was expected")
-    if t.dim() != dims:
-        raise AttnError(-2, f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.numel() > 0:
-        raise AttnError(-3, f"{name} must have unit stride over the head dimension")
+def _rows(name, t, index, dtype, dims):
+    """Strides of a tensor of head rows, after its device, dtype, rank and unit stride
+    over the head dimension were checked."""
+    s = t.stride()
+    if t.get_device() != index or t.dtype is not dtype or len(s) != dims or s[-1] != 1:
+        if t.get_device() != index:
+            raise AttnError(-9, f"{name} must be a CUDA tensor on cuda:{index}, got {t.device}")
+        if t.dtype is not dtype:
+            raise AttnError(-1, f"{name} has dtype {t.dtype}, {dtype} was expected")
+        if len(s) != dims:
+            raise AttnError(-2, f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+        if t.numel() > 0:
+            raise AttnError(-3, f"{name} must have unit stride over the head dimension")
+    return s
 
 
-def _ints(name, t, dev, shape) -> int:
-    """Pointer of a contiguous int32 tensor of the given shape (or None)."""
+def _ints(name, t, index, n):
+    """Pointer of a contiguous int32 tensor of n entries (None: none)."""
     if t is None:
-        return 0
-    if t.device != dev or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise AttnError(-9, f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}, "
-                            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return None
+    if t.get_device() != index or t.dtype is not _I32 or t.dim() != 1 or t.shape[0] != n or \
+            not t.is_contiguous():
+        raise AttnError(-9, f"{name} must be a contiguous int32 tensor [{n}] on cuda:{index}, got "
+                            f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _state(name, t, dev, dtype, batch, heads, width) -> int:
-    """Pointer of a contiguous [batch, H_k, >= width] tensor of per-slot state."""
+def _batch(seqlens) -> int:
+    if seqlens.dim() != 1:
+        raise AttnError(-9, f"seqlens must be a 1-D int32 tensor, got {tuple(seqlens.shape)}")
+    return seqlens.shape[0]
+
+
+def _state(name, t, index, dtype, batch, heads, width):
+    """(pointer, entries of a row) of a contiguous [batch, H_k, >= width] tensor of
+    per-slot state."""
     s = t.shape
-    if t.device != dev or t.dtype != dtype or len(s) != 3 or s[0] != batch or s[1] != heads or \
-            s[2] < width or not t.is_contiguous():
+    if t.get_device() != index or t.dtype is not dtype or len(s) != 3 or s[0] != batch or \
+            s[1] != heads or s[2] < width or not t.is_contiguous():
         raise AttnError(-9, f"{name} must be a contiguous {dtype} tensor [{batch}, {heads}, >= {width}] "
-                            f"on {dev}, got {t.dtype} {tuple(s)} on {t.device}")
-    return t.data_ptr()
+                            f"on cuda:{index}, got {t.dtype} {tuple(s)} on {t.device}")
+    return t.data_ptr(), s[2]
 
 
-def _cache(k_cache, v_cache, table, like, batch) -> Tuple[bytes, int, int]:
-    """(attn_paged_kv, H_k, slots of a sequence)."""
-    _rows("k_cache", k_cache, like, 4)
-    _rows("v_cache", v_cache, like, 4)
-    pages, size, heads, _ = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise AttnError(-2, f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(k_cache.shape)}")
-    if table.device != like.device or table.dtype != torch.int32 or table.dim() != 2 or \
+def _cache(k_cache, v_cache, table, index, dtype, batch):
+    """(attn_paged_kv, H_k, D, slots of a sequence)."""
+    ks = _rows("k_cache", k_cache, index, dtype, 4)
+    vs = _rows("v_cache", v_cache, index, dtype, 4)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise AttnError(-2, f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(shape)}")
+    pages, size, heads, dim = shape
+    if table.get_device() != index or table.dtype is not _I32 or table.dim() != 2 or \
             table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise AttnError(-9, f"block_table must be an int32 tensor [{batch}, pages] on {like.device} with "
+        raise AttnError(-9, f"block_table must be an int32 tensor [{batch}, pages] on cuda:{index} with "
                             f"contiguous rows, got {table.dtype} {tuple(table.shape)} on {table.device}")
-    ks, vs = k_cache.stride(), v_cache.stride()
     per = table.shape[1]
     return _PAGED.pack(k_cache.data_ptr(), ks[0], ks[1], ks[2], v_cache.data_ptr(), vs[0], vs[1], vs[2],
-                       table.data_ptr(), table.stride(0), pages, size, per), heads, per * size
+                       table.data_ptr(), table.stride(0), pages, size, per), heads, dim, per * size
 
 
-def _rotary(positions, inv_freq, sections, interleaved, inverse, dev, lead) -> bytes:
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.device != dev or \
-            inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise AttnError(-9, f"inv_freq must be a contiguous 1-D float32 tensor on {dev}")
+def _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, tokens) -> bytes:
+    if inv_freq.get_device() != index or inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous():
+        raise AttnError(-9, f"inv_freq must be a contiguous 1-D float32 tensor on cuda:{index}")
     n = inv_freq.shape[0]
-    sec = (n,) if sections is None else tuple(int(x) for x in sections)
-    if not 1 <= len(sec) <= 4:
-        raise AttnError(-2, f"sections must name 1 to 4 axes, got {len(sec)}")
-    shape = tuple(positions.shape)
-    if shape != (len(sec),) + lead and not (len(sec) == 1 and shape == lead):
-        raise AttnError(-2, f"positions must be {(len(sec),) + lead}, got {shape}")
-    if positions.device != dev or positions.dtype != torch.int32 or not positions.is_contiguous():
-        raise AttnError(-9, f"positions must be a contiguous int32 tensor on {dev}, got "
+    sec = (n,) if sections is None else tuple(sections)
+    axes = len(sec)
+    if not 1 <= axes <= 4:
+        raise AttnError(-2, f"sections must name 1 to 4 axes, got {axes}")
+    shape = positions.shape
+    if shape != (axes, *lead) and not (axes == 1 and shape == lead):
+        raise AttnError(-2, f"positions must be {(axes, *lead)}, got {tuple(shape)}")
+    if positions.get_device() != index or positions.dtype is not _I32 or not positions.is_contiguous():
+        raise AttnError(-9, f"positions must be a contiguous int32 tensor on cuda:{index}, got "
                             f"{positions.dtype} on {positions.device}")
-    tokens = 1
-    for x in lead:
-        tokens *= x
-    return _ROTARY.pack(positions.data_ptr(), tokens, inv_freq.data_ptr(), n, len(sec),
-                        *(sec + (0, 0, 0, 0))[:4], int(bool(interleaved)), int(bool(inverse)))
+    return _ROTARY.pack(positions.data_ptr(), tokens, inv_freq.data_ptr(), n, axes,
+                        *sec, *(0, 0, 0, 0)[axes:], 1 if interleaved else 0, 1 if inverse else 0)
 
 
-def _pack(t, packed: bool) -> bytes:
-    s = t.stride()
-    return _TENSOR.pack(t.data_ptr(), 0, s[0], s[1]) if packed else \
-        _TENSOR.pack(t.data_ptr(), s[0], s[1], s[2])
+def _stride3(s):
+    """Strides of batch, sequence and head of a padded or packed tensor."""
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
-def _same_place(name, out, x) -> None:
-    if out.data_ptr() == x.data_ptr() and out.numel() > 0 and out.stride() != x.stride():
+def _output(name, out, x, sx, index, dtype, made):
+    """(out, its strides): allocated like x, or checked against it."""
+    if out is None:
+        out = torch.empty_like(x)
+        made.append(out)
+        return out, out.stride()
+    so = _rows(name, out, index, dtype, len(sx))
+    if out.shape != x.shape:
+        raise AttnError(-2, f"{name} has shape {tuple(out.shape)}, its input {tuple(x.shape)}")
+    if out.data_ptr() == x.data_ptr() and so != sx and out.numel() > 0:
         raise AttnError(-9, f"{name} starts where its input does but has other strides")
+    return out, so
 
 
 def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = None,
@@ -154,39 +177,35 @@ def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = Non
     ``sections``: frequencies of each axis, at most four, in order (default: one axis).
     ``inverse=True`` turns back: on the gradients of the rotated q and k it is
     the backward pass.  ``k`` may be None.  ``out_q`` / ``out_k`` may be the inputs."""
-    L = lib()
-    if q.dim() not in (3, 4):
-        raise AttnError(-2, f"q must be [B, S, H, D] or packed [total, H, D], got {tuple(q.shape)}")
-    packed = q.dim() == 3
-    dt = _dtype(q, "q")
-    _rows("q", q, q, q.dim())
-    dev, lead = q.device, tuple(q.shape[:-2])
+    index, dtype, dt = _first(q, "q")
+    shape = q.shape
+    dims = len(shape)
+    if dims == 3:
+        tokens, hq, d = shape
+        batch, seqlen, lead = 1, tokens, (tokens,)
+    elif dims == 4:
+        batch, seqlen, hq, d = shape
+        tokens, lead = batch * seqlen, (batch, seqlen)
+    else:
+        raise AttnError(-2, f"q must be [B, S, H, D] or packed [total, H, D], got {tuple(shape)}")
     made = []
-    if out_q is None:
-        out_q = torch.empty_like(q)
-        made.append(out_q)
+    sq = _rows("q", q, index, dtype, dims)
+    out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
+    hk, pk, pok = hq, None, None
     if k is not None:
-        _rows("k", k, q, q.dim())
-        if tuple(k.shape[:-2]) != lead or k.shape[-1] != q.shape[-1]:
-            raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
-        if out_k is None:
-            out_k = torch.empty_like(k)
-            made.append(out_k)
+        sk = _rows("k", k, index, dtype, dims)
+        hk = k.shape[-2]
+        if k.shape != (*lead, hk, d):
+            raise AttnError(-2, f"q {tuple(shape)} and k {tuple(k.shape)} disagree on tokens or D")
+        out_k, sok = _output("out_k", out_k, k, sk, index, dtype, made)
+        pk, pok = _TENSOR.pack(k.data_ptr(), *_stride3(sk)), _TENSOR.pack(out_k.data_ptr(), *_stride3(sok))
     elif out_k is not None:
         raise AttnError(-9, "out_k without k")
-    for name, out, x in (("out_q", out_q, q), ("out_k", out_k, k)):
-        if x is not None and not (made and out is made[0]):
-            _rows(name, out, q, q.dim())
-            if out.shape != x.shape:
-                raise AttnError(-2, f"{name} has shape {tuple(out.shape)}, its input {tuple(x.shape)}")
-            _same_place(name, out, x)
-    rot = _rotary(positions, inv_freq, sections, interleaved, inverse, dev, lead)
-    batch, seqlen = (1, lead[0]) if packed else lead
-    if batch == 0 or seqlen == 0:
+    rot = _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, tokens)
+    if tokens == 0:
         return out_q, out_k
-    _call(L.attn_rope, dev, stream, made, _pack(q, packed), None if k is None else _pack(k, packed),
-          _pack(out_q, packed), None if k is None else _pack(out_k, packed), dt, batch, seqlen,
-          q.shape[-2], q.shape[-2] if k is None else k.shape[-2], q.shape[-1], rot)
+    _call(lib().attn_rope, index, stream, made, _TENSOR.pack(q.data_ptr(), *_stride3(sq)), pk,
+          _TENSOR.pack(out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
     return out_q, out_k
 
 
@@ -206,80 +225,75 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
     [B, H_k, slots], with ``seen`` int32 [B]) receives each new slot's token
     number ``seen[b] + i`` for attn_cache_evict.  ``seqlens`` is not advanced.
     """
-    L = lib()
-    dt = _dtype(k, "k")
-    _rows("k", k, k, 3)
-    _rows("v", v, k, 3)
-    dev = k.device
+    index, dtype, dt = _first(k, "k")
+    sk, sv = _rows("k", k, index, dtype, 3), _rows("v", v, index, dtype, 3)
     tokens, hk, d = k.shape
     if v.shape != k.shape:
         raise AttnError(-2, f"v has shape {tuple(v.shape)}, k {tuple(k.shape)}")
-    batch = seqlens.shape[0] if seqlens.dim() == 1 else -1
-    lens = _ints("seqlens", seqlens, dev, (batch,))
-    cache, heads, slots = _cache(k_cache, v_cache, block_table, k, batch)
-    if heads != hk or k_cache.shape[3] != d:
+    batch = _batch(seqlens)
+    lens = _ints("seqlens", seqlens, index, batch)
+    cache, heads, dim, _ = _cache(k_cache, v_cache, block_table, index, dtype, batch)
+    if heads != hk or dim != d:
         raise AttnError(-2, f"k {tuple(k.shape)} does not fit a cache {tuple(k_cache.shape)}")
-    cu = _ints("cu_seqlens", cu_seqlens, dev, (batch + 1,))
-    if cu_seqlens is None and tokens != batch:
+    cu = _ints("cu_seqlens", cu_seqlens, index, batch + 1)
+    if cu is None and tokens != batch:
         raise AttnError(-9, f"without cu_seqlens there is one token a sequence: {tokens} tokens, "
                             f"{batch} sequences")
     if (positions is None) != (inv_freq is None):
         raise AttnError(-9, "positions and inv_freq go together")
     rot = None if positions is None else \
-        _rotary(positions, inv_freq, sections, interleaved, False, dev, (tokens,))
+        _rotary(positions, inv_freq, sections, interleaved, False, index, (tokens,), tokens)
     made = []
     q_arg = oq_arg = None
     hq = hk
     if q is not None:
         if rot is None:
             raise AttnError(-9, "q is only taken to be rotated: give positions and inv_freq, or no q")
-        _rows("q", q, k, 3)
-        if q.shape[0] != tokens or q.shape[2] != d:
-            raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
-        if out_q is None:
-            out_q = torch.empty_like(q)
-            made.append(out_q)
-        else:
-            _rows("out_q", out_q, k, 3)
-            if out_q.shape != q.shape:
-                raise AttnError(-2, f"out_q has shape {tuple(out_q.shape)}, q {tuple(q.shape)}")
-            _same_place("out_q", out_q, q)
+        sq = _rows("q", q, index, dtype, 3)
         hq = q.shape[1]
-        q_arg, oq_arg = _pack(q, True), _pack(out_q, True)
+        if q.shape != (tokens, hq, d):
+            raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
+        out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
+        q_arg = _TENSOR.pack(q.data_ptr(), 0, sq[0], sq[1])
+        oq_arg = _TENSOR.pack(out_q.data_ptr(), 0, so[0], so[1])
     elif out_q is not None:
         raise AttnError(-9, "out_q without q")
-    sp, width = 0, 0
+    sp, width = None, 0
     if slot_positions is not None:
         if seen is None:
             raise AttnError(-9, "slot_positions needs seen")
-        sp = _state("slot_positions", slot_positions, dev, torch.int32, batch, hk, 1)
-        width = slot_positions.shape[2]
+        sp, width = _state("slot_positions", slot_positions, index, _I32, batch, hk, 1)
     if tokens == 0:
         return out_q
-    _call(L.attn_cache_append, dev, stream, made, q_arg, oq_arg, _pack(k, True), _pack(v, True), dt,
-          tokens, batch, hq, hk, d, cache, lens, cu or None, rot, sp or None, width,
-          _ints("seen", seen, dev, (batch,)) or None)
+    _call(lib().attn_cache_append, index, stream, made, q_arg, oq_arg,
+          _TENSOR.pack(k.data_ptr(), 0, sk[0], sk[1]), _TENSOR.pack(v.data_ptr(), 0, sv[0], sv[1]), dt,
+          tokens, batch, hq, hk, d, cache, lens, cu, rot, sp, width, _ints("seen", seen, index, batch))
     return out_q
 
 
+@functools.lru_cache(maxsize=256)
 def decode_workspace_size(batch: int, h_q: int, h_k: int, head_dim: int, max_seqlen: int,
                           weights: bool = False) -> int:
     return int(lib().attn_decode_workspace_size(batch, h_q, h_k, head_dim, max_seqlen, int(weights)))
 
 
 def alloc_decode_workspace(q, k_cache, max_seqlen: int, weights: bool = False) -> torch.Tensor:
-    """Workspace of attn_decode for queries like ``q`` [B, H_q, D] over ``k_cache``."""
+    """Workspace (at least 256 bytes) of attn_decode for queries like ``q`` [B, H_q, D] over ``k_cache``."""
     n = decode_workspace_size(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], max_seqlen, weights)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
-def _workspace(workspace, need, dev, made) -> torch.Tensor:
+def _workspace(workspace, need, like, index, made):
+    """(pointer, bytes) of the caller's workspace or of a new one (none if none is needed)."""
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         made.append(workspace)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise AttnError(-9, f"workspace must be a contiguous uint8 tensor on {dev}")
-    return workspace
+    elif workspace.get_device() != index or workspace.dtype is not torch.uint8 or \
+            not workspace.is_contiguous():
+        raise AttnError(-9, f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[int] = None,
@@ -296,57 +310,49 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
     softmax weight, summed over the query heads that share it, is added to it, in
     place or into ``weights_out``.  ``workspace``: uint8 of at least
     ``decode_workspace_size(...)`` bytes, not shared by calls that may overlap."""
-    L = lib()
-    dt = _dtype(q, "q")
-    _rows("q", q, q, 3)
-    dev = q.device
+    index, dtype, dt = _first(q, "q")
+    sq = _rows("q", q, index, dtype, 3)
     batch, hq, d = q.shape
-    cache, hk, slots = _cache(k_cache, v_cache, block_table, q, batch)
-    if k_cache.shape[3] != d or hq % max(hk, 1) != 0:
+    cache, hk, dim, slots = _cache(k_cache, v_cache, block_table, index, dtype, batch)
+    if dim != d or hk == 0 or hq % hk != 0:
         raise AttnError(-2, f"q {tuple(q.shape)} does not fit a cache {tuple(k_cache.shape)}")
-    lens = _ints("seqlens", seqlens, dev, (batch,))
+    lens = _ints("seqlens", seqlens, index, batch)
     max_seqlen = slots if max_seqlen is None else int(max_seqlen)
     made = []
-    if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
-    else:
-        _rows("out", out, q, 3)
-        if out.shape != q.shape:
-            raise AttnError(-2, f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
+    out, so = _output("out", out, q, sq, index, dtype, made)
     if lse is None:
-        lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((batch, hq), dtype=_F32, device=q.device)
         made.append(lse)
-    elif lse.device != dev or lse.dtype != torch.float32 or tuple(lse.shape) != (batch, hq) or \
+    elif lse.get_device() != index or lse.dtype is not _F32 or lse.shape != (batch, hq) or \
             not lse.is_contiguous():
-        raise AttnError(-2, f"lse must be a contiguous float32 tensor {(batch, hq)} on {dev}")
-    if batch == 0:
-        return out, lse
+        raise AttnError(-2, f"lse must be a contiguous float32 tensor {(batch, hq)} on cuda:{index}")
     w_in = w_out = None
     width = 0
     if weights is not None:
-        weights_out = weights if weights_out is None else weights_out
-        w_in = _state("weights", weights, dev, torch.float32, batch, hk, max_seqlen)
-        w_out = _state("weights_out", weights_out, dev, torch.float32, batch, hk, max_seqlen)
-        width = weights.shape[2]
-        if weights_out.shape[2] != width:
-            raise AttnError(-2, "weights and weights_out must have the same shape")
+        w_in, width = _state("weights", weights, index, _F32, batch, hk, max_seqlen)
+        w_out = w_in
+        if weights_out is not None:
+            w_out, other = _state("weights_out", weights_out, index, _F32, batch, hk, max_seqlen)
+            if other != width:
+                raise AttnError(-2, "weights and weights_out must have the same shape")
     elif weights_out is not None:
         raise AttnError(-9, "weights_out without weights")
-    need = L.attn_decode_workspace_size(batch, hq, hk, d, max_seqlen, weights is not None)
-    workspace = _workspace(workspace, need, dev, made)
+    if batch == 0:
+        return out, lse
+    ws, size = _workspace(workspace, decode_workspace_size(batch, hq, hk, d, max_seqlen, w_in is not None),
+                          q, index, made)
     opts = None
     if window is not None or softcap:
         left, right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
         opts = _OPTS.pack(left, right, float(softcap or 0.0), 0, 0)
-    qs, os = q.stride(), out.stride()
-    _call(L.attn_decode, dev, stream, made, _TENSOR.pack(q.data_ptr(), qs[0], 0, qs[1]),
-          _TENSOR.pack(out.data_ptr(), os[0], 0, os[1]), lse.data_ptr(), dt, batch, hq, hk, d,
+    _call(lib().attn_decode, index, stream, made, _TENSOR.pack(q.data_ptr(), sq[0], 0, sq[1]),
+          _TENSOR.pack(out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
           d ** -0.5 if scale is None else float(scale), cache, lens, max_seqlen, opts, w_in, w_out,
-          width, workspace.data_ptr(), workspace.numel())
+          width, ws, size)
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
 def evict_workspace_size(batch: int, h_k: int, budget: int, max_seqlen: int) -> int:
     return int(lib().attn_cache_evict_workspace_size(batch, h_k, budget, max_seqlen))
 
@@ -372,38 +378,38 @@ def attn_cache_evict(k_cache, v_cache, block_table, seqlens, weights, budget: in
     are changed in place; ``weights_out`` and ``positions_out`` default to the
     inputs; slots [budget, seqlens[b]) get 0 and -1 there.  ``seqlens_out`` must
     not be ``seqlens``."""
-    L = lib()
-    dt = _dtype(k_cache, "k_cache")
-    dev = k_cache.device
-    batch = seqlens.shape[0] if seqlens.dim() == 1 else -1
-    cache, hk, slots = _cache(k_cache, v_cache, block_table, k_cache, batch)
-    lens = _ints("seqlens", seqlens, dev, (batch,))
+    index, dtype, dt = _first(k_cache, "k_cache")
+    batch = _batch(seqlens)
+    cache, hk, d, slots = _cache(k_cache, v_cache, block_table, index, dtype, batch)
+    lens = _ints("seqlens", seqlens, index, batch)
     max_seqlen = slots if max_seqlen is None else int(max_seqlen)
-    weights_out = weights if weights_out is None else weights_out
-    w_in = _state("weights", weights, dev, torch.float32, batch, hk, max_seqlen)
-    w_out = _state("weights_out", weights_out, dev, torch.float32, batch, hk, max_seqlen)
-    width = weights.shape[2]
+    budget = int(budget)
+    if weights_out is None:
+        weights_out = weights
+    w_in, width = _state("weights", weights, index, _F32, batch, hk, max_seqlen)
+    w_out, same = _state("weights_out", weights_out, index, _F32, batch, hk, max_seqlen)
     p_in = p_out = None
-    same = weights_out.shape[2] == width
+    widths = {width, same}
     if slot_positions is not None:
-        positions_out = slot_positions if positions_out is None else positions_out
-        p_in = _state("slot_positions", slot_positions, dev, torch.int32, batch, hk, max_seqlen)
-        p_out = _state("positions_out", positions_out, dev, torch.int32, batch, hk, max_seqlen)
-        same = same and slot_positions.shape[2] == width and positions_out.shape[2] == width
+        if positions_out is None:
+            positions_out = slot_positions
+        p_in, same = _state("slot_positions", slot_positions, index, _I32, batch, hk, max_seqlen)
+        widths.add(same)
+        p_out, same = _state("positions_out", positions_out, index, _I32, batch, hk, max_seqlen)
+        widths.add(same)
     elif positions_out is not None:
         raise AttnError(-9, "positions_out without slot_positions")
-    if not same:
+    if len(widths) != 1:
         raise AttnError(-2, "weights, slot_positions and their outputs must have the same shape")
     made = []
     if seqlens_out is None:
         seqlens_out = torch.empty_like(seqlens)
         made.append(seqlens_out)
-    out = _ints("seqlens_out", seqlens_out, dev, (batch,))
+    out = _ints("seqlens_out", seqlens_out, index, batch)
     if batch == 0:
         return seqlens_out, weights_out, positions_out
-    need = L.attn_cache_evict_workspace_size(batch, hk, int(budget), max_seqlen)
-    workspace = _workspace(workspace, need, dev, made)
-    _call(L.attn_cache_evict, dev, stream, made, cache, dt, batch, hk, k_cache.shape[3], lens, out,
-          max_seqlen, int(budget), int(recent), _ints("seen", seen, dev, (batch,)) or None, w_in, w_out,
-          p_in, p_out, width, workspace.data_ptr(), workspace.numel())
+    ws, size = _workspace(workspace, evict_workspace_size(batch, hk, budget, max_seqlen), k_cache,
+                          index, made)
+    _call(lib().attn_cache_evict, index, stream, made, cache, dt, batch, hk, d, lens, out, max_seqlen,
+          budget, int(recent), _ints("seen", seen, index, batch), w_in, w_out, p_in, p_out, width, ws, size)
     return seqlens_out, weights_out, positions_out

@@ -290,7 +290,7 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
   p.w_in = weights_in;
   p.w_out = weights_out;
   p.w_stride = weights_stride;
-  p.lse2 = reinterpret_cast<float*>(ws + w.off_lse2);
+  p.lse2 = weights_in != nullptr ? reinterpret_cast<float*>(ws + w.off_lse2) : nullptr;
   p.parts = reinterpret_cast<float*>(ws + w.off_parts);
   p.logits = weights_in != nullptr ? reinterpret_cast<float*>(ws + w.off_logits) : nullptr;
   p.logit_stride = w.logit_stride;

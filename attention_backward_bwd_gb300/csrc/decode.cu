@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
             const float lse2 = none ? INFINITY : m[r] + log2f(sum);
             const int64_t at = static_cast<int64_t>(d.b) * p.h_q + h0 + row;
             if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
-            p.lse2[at] = lse2;
+            if (p.lse2 != nullptr) p.lse2[at] = lse2;
           }
         } else {
 #pragma unroll
@@ -901,12 +901,13 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
 }  // namespace
 
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights) {
-  DecodeWs w;
+  DecodeWs w = {};
+  if (!weights && max_seqlen <= kWholeTiles * kTile) return w;  // nothing is joined
   const size_t rows = static_cast<size_t>(batch) * h_q;
   const int group = h_q / h_k, part_rows = group < kMaxRows ? group : kMaxRows;
   w.logit_stride = round_up(max_seqlen, kTile);
-  w.off_lse2 = 0;
-  w.off_parts = align256(rows * 4);
+  w.off_lse2 = 0;  // with weights only
+  w.off_parts = weights ? align256(rows * 4) : 0;
   w.off_logits = w.off_parts + align256(static_cast<size_t>(kMaxRuns) * 2 *
                                         (static_cast<size_t>(part_rows) * pad_dim(head_dim) + 2 * kMaxRows) * 4);
   w.total = w.off_logits + (weights ? align256(rows * static_cast<size_t>(w.logit_stride) * 4) : 0);

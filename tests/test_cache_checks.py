@@ -140,7 +140,10 @@ def test_append_refuses(lib, kw, code):
     (dict(dt=2), DTYPE), (dict(hq=5), SHAPE), (dict(d=4), SHAPE), (dict(scale=float("nan")), ARG),
     (dict(most=-1), ARG), (dict(most=129), ARG), (dict(q=T(0)), NULL), (dict(o=T(P + 8)), ALIGN),
     (dict(o=T(h=0)), STRIDE), (dict(n=None), NULL), (dict(lse=P + 2), ALIGN), (dict(wi=P, width=100), ARG),
-    (dict(wi=P, wo=P, width=99), STRIDE), (dict(ws=None), WS), (dict(ws=P + 64), WS), (dict(size=3), WS),
+    (dict(wi=P, wo=P, width=99), STRIDE),
+    # (up to 256 keys need no workspace)
+    (dict(ws=None, most=300, c=paged(per=20, ts=20)), WS), (dict(ws=P + 64, most=300, c=paged(per=20, ts=20)), WS),
+    (dict(size=3, most=300, c=paged(per=20, ts=20)), WS), (dict(ws=None, wi=P, wo=P, width=100), WS),
     (dict(opts=binding_cache._OPTS.pack(-2, -1, 0.0, 0, 0)), ARG),
     (dict(opts=binding_cache._OPTS.pack(-1, -1, -1.0, 0, 0)), ARG),
     (dict(opts=binding_cache._OPTS.pack(-1, -1, 0.0, 0, P)), ARG),
@@ -165,6 +168,8 @@ def test_workspace_sizes(lib):
     b = ab.decode_workspace_size(4, 32, 8, 128, 1000, weights=True)
     assert a > 0 and a % 256 == 0 and b >= a + 4 * 32 * 1000 * 4
     assert ab.decode_workspace_size(4, 5, 2, 128, 10) == 0
+    assert ab.decode_workspace_size(4, 32, 8, 128, 256) == 0
+    assert ab.decode_workspace_size(4, 32, 8, 128, 100, weights=True) > 0
     assert ab.evict_workspace_size(4, 8, 100, 1000) >= 4 * 8 * (4 + 2 * 400)
     assert ab.evict_workspace_size(4, 8, 100, 50) >= 4 * 8 * 4
     assert ab.evict_workspace_size(0, 8, 100, 50) == 0
