@@ -120,16 +120,15 @@ int check_workspace(const void* ws, size_t given, size_t need) {
 }
 
 struct EvictWs {
-  size_t off_from, off_to, total;
+  size_t off_to, total;
 };
 
 EvictWs evict_ws(int batch, int h_k, int budget, int max_seqlen) {
   const size_t heads = static_cast<size_t>(batch) * h_k;
-  const size_t list = heads * evict_move_cap(budget, max_seqlen) * 4;
+  const size_t list = heads * evict_move_cap(budget, max_seqlen) * sizeof(int2);
   EvictWs w;
-  w.off_from = align256(heads * 4);
-  w.off_to = w.off_from + align256(list);
-  w.total = w.off_to + align256(list);
+  w.off_to = align256(list);
+  w.total = w.off_to + align256(list > 0 ? list : 1);
   return w;
 }
 
@@ -353,9 +352,8 @@ int attn_cache_evict(const attn_paged_kv* cache, int dtype, int batch, int h_k, 
   p.pos_in = positions_in;
   p.pos_out = positions_out;
   p.stride = state_stride;
-  p.count = reinterpret_cast<int*>(ws);
-  p.from = reinterpret_cast<int*>(ws + w.off_from);
-  p.to = reinterpret_cast<int*>(ws + w.off_to);
+  p.from = reinterpret_cast<int2*>(ws);
+  p.to = reinterpret_cast<int2*>(ws + w.off_to);
   p.move_cap = evict_move_cap(budget, max_seqlen);
   if ((rc = status_of(&p.status))) return rc;
   const cudaError_t e = launch_evict(p, dtype, reinterpret_cast<cudaStream_t>(stream));

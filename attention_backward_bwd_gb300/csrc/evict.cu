@@ -1,23 +1,35 @@
 // Eviction from the paged cache by accumulated attention weight
-// (attn_cache_evict), in two launches.
+// (attn_cache_evict), in one launch.
 //
-// Selection, one block per (sequence, head): the rank of a slot is a 32-bit key
-// that orders as the floats do; four passes of 8 bits with a histogram in shared
-// memory find the key of the budget-th largest and how many of its equals stay.
-// Each thread then owns a run of neighbouring slots, and block-wide prefix sums
-// over the threads turn "kept" into places: the i-th kept slot above the budget
-// moves into the i-th freed slot below it.  Sources and targets are disjoint
-// ranges of slots, so the moves need no order among each other.
+// A cluster of blocks takes one (sequence, head); every block owns a run of its slots.
+// Selection: the rank of a slot is a 32-bit key that orders as the floats do.  Four
+// passes over its 8-bit digits find the key of the budget-th largest and how many of its
+// equals stay: each block counts digits in its shared memory, and all blocks of the
+// cluster read each other's counts (one bin a thread; with three passes of 2048 bins those
+// reads took 200 us).  Up to 8 keys a thread stay in
+// registers; further ones are read again from the L2 in each pass.
+// Places: warp ballots and prefix sums over them, in slot order, turn "kept" into indices;
+// the i-th kept slot at or above the budget moves into the i-th freed slot below it.
+// Sources and targets are disjoint ranges of slots, so the moves need no order.
+// Copy: the cluster's threads move state and rows of k and v, 16 bytes a thread.
 //
-// Copy: the listed rows of k and v, 16 bytes a thread.
+// The bytes are few (n weights and positions a head, and the rows that move); what
+// bounds it is the chain of passes, so a head is spread over up to eight blocks while the
+// device has room for them.
+#include <cooperative_groups.h>
+
 #include "cache.h"
 #include "common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace attn {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kBins = 256;
+constexpr int kKeep = 8;  // keys of a thread in registers
+constexpr int kMaxCluster = 8;
 
 // Unsigned key in the order of the ranks: NaN lowest, then the floats (-0 = +0).
 __device__ __forceinline__ uint32_t rank_key(float w) {
@@ -27,45 +39,28 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 }
 constexpr uint32_t kInfKey = 0xFF800000u;  // rank_key(+inf): the rank of a recent slot
 
-// Exclusive prefix sum of v over the block; total in `sum`.
-__device__ int block_scan(int v, int* warp_sums, int& sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, i);
-    if (lane >= i) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, i);
-      if (lane >= i) s += y;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  sum = warp_sums[31];
-  return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
-}
+struct Totals {
+  int ties, holes, movers;
+};
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int tid = threadIdx.x;
-  const int bh = blockIdx.x, b = bh / p.h_k;
+template <int T>
+__global__ void __launch_bounds__(T) evict_kernel(EvictParams p, int cs, FastDiv per_move) {
+  constexpr int W = T / 32;
+  __shared__ int hist[4][kBins];
+  __shared__ int s_sums[W];
+  __shared__ int s_cnt[kKeep * W];   // of a batch: per round and warp, then their prefixes
+  __shared__ int s_cnt2[kKeep * W];
+  __shared__ int s_digit, s_left, s_equal;
+  __shared__ Totals s_tot;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bh = blockIdx.x / cs, rank = blockIdx.x - bh * cs;
+  const int b = bh / p.h_k, h = bh - b * p.h_k;
   const int n = p.seqlens[b];
   if (n < 0 || n > p.max_seqlen) {
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       report(p.status, kBadLength);
-      p.count[bh] = 0;
-      if (bh == b * p.h_k) p.seqlens_out[b] = 0;
+      if (h == 0) p.seqlens_out[b] = 0;
     }
     return;
   }
@@ -74,134 +69,324 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictParams p) {
   float* w_out = p.w_out + base;
   const int* pos = p.pos_in != nullptr ? p.pos_in + base : nullptr;
   int* pos_out = p.pos_out != nullptr ? p.pos_out + base : nullptr;
-  const int m = min(n, p.budget);
-  if (tid == 0 && bh == b * p.h_k) p.seqlens_out[b] = m;
+  const bool copy_w = w_out != w, copy_pos = pos != nullptr && pos_out != pos;
+  if (tid == 0 && rank == 0 && h == 0) p.seqlens_out[b] = min(n, p.budget);
   if (n <= p.budget) {
-    if (tid == 0) p.count[bh] = 0;
-    for (int j = tid; j < n; j += kSelThreads) {
-      if (w_out != w) w_out[j] = w[j];
-      if (pos != nullptr && pos_out != pos) pos_out[j] = pos[j];
+    for (int j = rank * T + tid; j < n; j += cs * T) {
+      if (copy_w) w_out[j] = w[j];
+      if (copy_pos) pos_out[j] = pos[j];
     }
     return;
   }
-  const long long recent_from =
-      p.recent > 0 ? static_cast<long long>(p.seen[b]) - p.recent : 0;
-  auto key_of = [&](int j) -> uint32_t {
-    if (p.recent > 0 && pos[j] >= recent_from) return kInfKey;
-    return rank_key(w[j]);
+
+  // ---- keys: this block's slots are [first, last), round i of a batch T of them
+  const int per = ((n + cs - 1) / cs + T - 1) / T * T;
+  const int first = min(n, rank * per), last = min(n, first + per);
+  const int batches = (last - first + kKeep * T - 1) / (kKeep * T);
+  const long long recent_from = p.recent > 0 ? static_cast<long long>(p.seen[b]) - p.recent : 0;
+  auto slot = [&](int batch, int i) { return first + (batch * kKeep + i) * T + tid; };
+  auto load = [&](int batch, uint32_t (&key)[kKeep]) {
+    float x[kKeep];
+    int q[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int j = slot(batch, i);
+      x[i] = j < last ? w[j] : 0.f;
+      q[i] = p.recent > 0 && j < last ? pos[j] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) key[i] = p.recent > 0 && q[i] >= recent_from ? kInfKey : rank_key(x[i]);
+  };
+  for (int i = tid; i < 4 * kBins; i += T) (&hist[0][0])[i] = 0;
+  if (tid == 0) s_tot = Totals{0, 0, 0};
+  uint32_t key[kKeep];
+  load(0, key);
+  __syncthreads();
+
+  // ---- key of the budget-th largest, digit by digit
+  uint32_t prefix = 0;
+  int need = p.budget, equal = 0;  // still to be found among the `equal` keys that share `prefix`
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + 8);
+    for (int bt = 0; bt < batches; ++bt) {
+      if (bt > 0) load(bt, key);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (slot(bt, i) < last && (key[i] & mask) == prefix)
+          atomicAdd(&hist[pass][(key[i] >> shift) & 255u], 1);
+    }
+    if (batches > 1) load(0, key);
+    cluster.sync();
+    // thread t: bin 255 - t, the highest first
+    int mine = 0;
+    if (tid < kBins)
+      for (int r = 0; r < cs; ++r) mine += cluster.map_shared_rank(&hist[pass][0], r)[kBins - 1 - tid];
+    int x = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, i);
+      if (lane >= i) x += y;
+    }
+    if (lane == 31) s_sums[warp] = x;
+    __syncthreads();
+    int above = x - mine;
+#pragma unroll
+    for (int v = 0; v < kBins / 32 - 1; ++v) above += v < warp ? s_sums[v] : 0;
+    if (above < need && above + mine >= need) {
+      s_digit = kBins - 1 - tid;
+      s_left = need - above;
+      s_equal = mine;
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
+    need = s_left;
+    equal = s_equal;
+  }
+
+  // Exclusive prefixes of the counts of a batch, in slot order (round by round, warp by
+  // warp); returns the batch's total.  Starts and ends with a barrier.
+  auto scan_counts = [&](int* cnt) -> int {
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int kPer = kKeep * W / 32;
+      int v[kPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v[i] = cnt[lane * kPer + i];
+        sum += v[i];
+      }
+      int x = sum;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, i);
+        if (lane >= i) x += y;
+      }
+      int at = x - sum;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        cnt[lane * kPer + i] = at;
+        at += v[i];
+      }
+      if (lane == 31) s_sums[0] = x;
+    }
+    __syncthreads();
+    const int total = s_sums[0];
+    return total;
+  };
+  // The block totals of the blocks before this one, and of all.
+  auto exchange = [&](Totals& all) {
+    cluster.sync();
+    Totals before{0, 0, 0};
+    all = Totals{0, 0, 0};
+    for (int r = 0; r < cs; ++r) {
+      const Totals t = *cluster.map_shared_rank(&s_tot, r);
+      if (r < rank) {
+        before.ties += t.ties;
+        before.holes += t.holes;
+        before.movers += t.movers;
+      }
+      all.ties += t.ties;
+      all.holes += t.holes;
+      all.movers += t.movers;
+    }
+    return before;
+  };
+  const uint32_t below = (1u << lane) - 1;
+
+  // ---- which of the equal keys stay: the lower slots
+  const bool all_ties = equal == need;
+  Totals all;
+  int tie_base = 0;
+  if (!all_ties) {
+    int mine = 0;
+    for (int bt = 0; bt < batches; ++bt) {
+      if (bt > 0) load(bt, key);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        mine += __popc(__ballot_sync(0xffffffffu, slot(bt, i) < last && key[i] == prefix));
+    }
+    if (batches > 1) load(0, key);
+    if (lane == 0) atomicAdd(&s_tot.ties, mine);
+    tie_base = exchange(all).ties;
+  }
+  // Bit i: the batch's key i stays.  `ties`: equal keys before the batch; advanced.
+  auto kept = [&](int bt, int& ties) -> uint32_t {
+    uint32_t keep = 0;
+    if (all_ties) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) keep |= (slot(bt, i) < last && key[i] >= prefix ? 1u : 0u) << i;
+      return keep;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const uint32_t t = __ballot_sync(0xffffffffu, slot(bt, i) < last && key[i] == prefix);
+      if (lane == 0) s_cnt[i * W + warp] = __popc(t);
+    }
+    const int total = scan_counts(s_cnt);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const bool in = slot(bt, i) < last, tie = in && key[i] == prefix;
+      const uint32_t t = __ballot_sync(0xffffffffu, tie);
+      const int place = ties + s_cnt[i * W + warp] + __popc(t & below);
+      keep |= ((in && key[i] > prefix) || (tie && place < need) ? 1u : 0u) << i;
+    }
+    __syncthreads();
+    ties += total;
+    return keep;
   };
 
-  // ---- key of the budget-th largest
-  uint32_t prefix = 0;
-  int need = p.budget;  // still to be found among keys that share `prefix`
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int j = tid; j < n; j += kSelThreads) {
-      const uint32_t k = key_of(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+  // ---- freed slots below the budget and kept ones above it, over the blocks
+  {
+    int holes = 0, movers = 0, ties = tie_base;
+    for (int bt = 0; bt < batches; ++bt) {
+      if (bt > 0) load(bt, key);
+      const uint32_t keep = kept(bt, ties);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int j = slot(bt, i);
+        const bool k = (keep >> i) & 1u;
+        holes += __popc(__ballot_sync(0xffffffffu, j < last && j < p.budget && !k));
+        movers += __popc(__ballot_sync(0xffffffffu, j < last && j >= p.budget && k));
+      }
     }
-    __syncthreads();
-    if (tid == 0) {
-      int left = need, bin = 255;
-      for (; bin > 0 && hist[bin] < left; --bin) left -= hist[bin];
-      s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-      s_need = left;
+    if (batches > 1) load(0, key);
+    if (lane == 0) {
+      atomicAdd(&s_tot.holes, holes);
+      atomicAdd(&s_tot.movers, movers);
     }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    __syncthreads();
   }
+  const Totals before = exchange(all);
+  const int moves = all.movers;  // as many as there are holes
+  int2* from = p.from + static_cast<int64_t>(bh) * p.move_cap;
+  int2* to = p.to + static_cast<int64_t>(bh) * p.move_cap;
+  const int* row = p.cache.table + b * p.cache.table_stride;
+  auto place = [&](int j) {  // slot and its page, -1 for a bad one
+    const int page = row[p.cache.page.div(static_cast<uint32_t>(j))];
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(p.cache.num_pages)) return make_int2(j, page);
+    report(p.status, kBadPage);
+    return make_int2(j, -1);
+  };
+  {
+    int hole = before.holes, mover = before.movers, ties = tie_base;
+    for (int bt = 0; bt < batches; ++bt) {
+      if (bt > 0) load(bt, key);
+      const uint32_t keep = kept(bt, ties);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int j = slot(bt, i);
+        const bool k = (keep >> i) & 1u;
+        const uint32_t hb = __ballot_sync(0xffffffffu, j < last && j < p.budget && !k);
+        const uint32_t mb = __ballot_sync(0xffffffffu, j < last && j >= p.budget && k);
+        if (lane == 0) {
+          s_cnt[i * W + warp] = __popc(hb);
+          s_cnt2[i * W + warp] = __popc(mb);
+        }
+      }
+      const int all_holes = scan_counts(s_cnt), all_movers = scan_counts(s_cnt2);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int j = slot(bt, i);
+        const bool k = (keep >> i) & 1u;
+        const bool is_hole = j < last && j < p.budget && !k, is_mover = j < last && j >= p.budget && k;
+        const uint32_t hb = __ballot_sync(0xffffffffu, is_hole), mb = __ballot_sync(0xffffffffu, is_mover);
+        if (is_hole) to[hole + s_cnt[i * W + warp] + __popc(hb & below)] = place(j);
+        if (is_mover) from[mover + s_cnt2[i * W + warp] + __popc(mb & below)] = place(j);
+        // state of slots that stay, and of those that go
+        if (j < last && j < p.budget && k) {
+          if (copy_w) w_out[j] = w[j];
+          if (copy_pos) pos_out[j] = pos[j];
+        } else if (j < last && j >= p.budget && !k) {
+          w_out[j] = 0.f;
+          if (pos != nullptr) pos_out[j] = -1;
+        }
+      }
+      __syncthreads();
+      hole += all_holes;
+      mover += all_movers;
+    }
+  }
+  cluster.sync();  // the lists are complete
 
-  // ---- places: thread t owns slots [j0, j1)
-  const int per = (n + kSelThreads - 1) / kSelThreads;
-  const int j0 = min(n, tid * per), j1 = min(n, j0 + per);
-  int ties = 0;
-  for (int j = j0; j < j1; ++j) ties += key_of(j) == prefix ? 1 : 0;
-  int sum;
-  const int ties_before = block_scan(ties, warp_sums, sum);
-  int seen_ties = ties_before, holes = 0, movers = 0;
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t k = key_of(j);
-    const bool keep = k > prefix || (k == prefix && seen_ties++ < need);
-    if (j < p.budget) holes += keep ? 0 : 1;
-    else movers += keep ? 1 : 0;
-  }
-  int n_holes, n_movers;
-  int hole = block_scan(holes, warp_sums, n_holes);
-  int mover = block_scan(movers, warp_sums, n_movers);
-  int* from = p.from + static_cast<int64_t>(bh) * p.move_cap;
-  int* to = p.to + static_cast<int64_t>(bh) * p.move_cap;
-  seen_ties = ties_before;
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t k = key_of(j);
-    const bool keep = k > prefix || (k == prefix && seen_ties++ < need);
-    if (j < p.budget) {
-      if (!keep) to[hole++] = j;
-    } else if (keep) {
-      from[mover++] = j;
+  // ---- moves: state, then rows: unit c of a move is a chunk of k, then of v
+  for (int i = rank * T + tid; i < moves; i += cs * T) {
+    const int s = from[i].x, t = to[i].x;
+    const float x = w[s];
+    w_out[t] = x;
+    w_out[s] = 0.f;
+    if (pos != nullptr) {
+      const int y = pos[s];
+      pos_out[t] = y;
+      pos_out[s] = -1;
     }
   }
-  if (tid == 0) p.count[bh] = n_movers;
-  __syncthreads();
-
-  // ---- state: kept slots stay, moved ones follow, the rest is cleared
-  if (w_out != w)
-    for (int j = tid; j < p.budget; j += kSelThreads) w_out[j] = w[j];
-  if (pos != nullptr && pos_out != pos)
-    for (int j = tid; j < p.budget; j += kSelThreads) pos_out[j] = pos[j];
-  __syncthreads();
-  for (int i = tid; i < n_movers; i += kSelThreads) {
-    w_out[to[i]] = w[from[i]];
-    if (pos != nullptr) pos_out[to[i]] = pos[from[i]];
-  }
-  __syncthreads();
-  for (int j = p.budget + tid; j < n; j += kSelThreads) {
-    w_out[j] = 0.f;
-    if (pos != nullptr) pos_out[j] = -1;
+  const int chunks = p.head_dim / 8;
+  uint4* kp = static_cast<uint4*>(const_cast<void*>(p.cache.k.ptr));
+  uint4* vp = static_cast<uint4*>(const_cast<void*>(p.cache.v.ptr));
+  const int64_t units = static_cast<int64_t>(moves) * per_move.d, stride = static_cast<int64_t>(cs) * T;
+  auto address = [&](int2 at, int c) -> uint4* {  // nullptr for a bad page
+    if (at.y < 0) return nullptr;
+    const int within = at.x - static_cast<int>(p.cache.page.div(static_cast<uint32_t>(at.x)) * p.cache.page.d);
+    const TensorArg& t = c < chunks ? p.cache.k : p.cache.v;
+    return (c < chunks ? kp + c : vp + (c - chunks)) + (at.y * t.sb + within * t.ss + h * t.sh) / 8;
+  };
+  constexpr int kUnroll = 4;  // units in flight of a thread
+  for (int64_t u0 = rank * T + tid; u0 < units; u0 += kUnroll * stride) {
+    uint4* src[kUnroll];
+    uint4* dst[kUnroll];
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t u = u0 + k * stride;
+      src[k] = dst[k] = nullptr;
+      if (u < units) {
+        const int i = units <= INT32_MAX ? static_cast<int>(per_move.div(static_cast<uint32_t>(u)))
+                                         : static_cast<int>(u / per_move.d);
+        const int c = static_cast<int>(u - static_cast<int64_t>(i) * per_move.d);
+        src[k] = address(from[i], c);
+        dst[k] = address(to[i], c);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (src[k] != nullptr && dst[k] != nullptr) x[k] = *src[k];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (src[k] != nullptr && dst[k] != nullptr) *dst[k] = x[k];
   }
 }
 
-// Rows of k and v from their old slots into the freed ones.
-__global__ void __launch_bounds__(256) move_kernel(EvictParams p, int chunks) {
-  const int bh = blockIdx.x, b = bh / p.h_k, h = bh - b * p.h_k;
-  const int moves = p.count[bh];
-  const int* row = p.cache.table + b * p.cache.table_stride;
-  const int* from = p.from + static_cast<int64_t>(bh) * p.move_cap;
-  const int* to = p.to + static_cast<int64_t>(bh) * p.move_cap;
-  const uint4* k = static_cast<const uint4*>(p.cache.k.ptr);
-  const uint4* v = static_cast<const uint4*>(p.cache.v.ptr);
-  const int64_t total = static_cast<int64_t>(moves) * chunks;
-  for (int64_t u = blockIdx.y * 256 + threadIdx.x; u < total; u += gridDim.y * 256) {
-    const int i = static_cast<int>(u / chunks), c = static_cast<int>(u - static_cast<int64_t>(i) * chunks);
-    int p0, w0, p1, w1;
-    const bool good = page_of(p.cache, row, from[i], p0, w0, p.status) &
-                      page_of(p.cache, row, to[i], p1, w1, p.status);
-    if (!good) continue;
-    const TensorArg &ka = p.cache.k, &va = p.cache.v;
-    const uint4 x = k[(p0 * ka.sb + w0 * ka.ss + h * ka.sh) / 8 + c];
-    const uint4 y = v[(p0 * va.sb + w0 * va.ss + h * va.sh) / 8 + c];
-    const_cast<uint4*>(k)[(p1 * ka.sb + w1 * ka.ss + h * ka.sh) / 8 + c] = x;
-    const_cast<uint4*>(v)[(p1 * va.sb + w1 * va.ss + h * va.sh) / 8 + c] = y;
-  }
+template <int T>
+cudaError_t launch_t(const EvictParams& p, int cs, cudaStream_t stream) {
+  FastDiv per_move;
+  per_move.set(static_cast<uint32_t>(p.head_dim / 8 * 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.h_k * cs);
+  cfg.blockDim = dim3(T);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<T>, p, cs, per_move);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream) {
   (void)dtype;  // rows are moved as 16-byte chunks
-  const unsigned heads = static_cast<unsigned>(p.batch) * p.h_k;
-  select_kernel<<<heads, kSelThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.move_cap == 0) return e;
-  const int chunks = p.head_dim / 8;
-  const int64_t most = (static_cast<int64_t>(p.move_cap) * chunks + 255) / 256;
-  int64_t y = (8 * static_cast<int64_t>(num_sms()) + heads - 1) / heads;
-  if (y > most) y = most;
-  move_kernel<<<dim3(heads, static_cast<unsigned>(y < 1 ? 1 : y)), 256, 0, stream>>>(p, chunks);
-  return cudaGetLastError();
+  const int64_t heads = static_cast<int64_t>(p.batch) * p.h_k;
+  if (heads * kMaxCluster > INT32_MAX) return cudaErrorInvalidValue;
+  // blocks of a head: while all of them fit the device at once and each has 512 slots
+  int cs = 1;
+  while (cs < kMaxCluster && heads * cs * 2 <= 4 * static_cast<int64_t>(num_sms()) &&
+         p.max_seqlen / (cs * 2) >= 512)
+    cs *= 2;
+  return ceil_div(p.max_seqlen, cs) <= 256 * kKeep ? launch_t<256>(p, cs, stream)
+                                                   : launch_t<1024>(p, cs, stream);
 }
 
 }  // namespace attn
