@@ -99,8 +99,8 @@ struct EvictParams {
   const int* pos_in;
   int* pos_out;
   int64_t stride;
-  int2* from;   // workspace: [batch * h_k][move_cap] source slots and their pages
-  int2* to;     // workspace: the slots they move to
+  int* from;    // workspace: [batch * h_k][move_cap] source slots
+  int* to;      // workspace: the slots they move to
   int move_cap;
   unsigned int* status;
 };

@@ -125,7 +125,7 @@ struct EvictWs {
 
 EvictWs evict_ws(int batch, int h_k, int budget, int max_seqlen) {
   const size_t heads = static_cast<size_t>(batch) * h_k;
-  const size_t list = heads * evict_move_cap(budget, max_seqlen) * sizeof(int2);
+  const size_t list = heads * evict_move_cap(budget, max_seqlen) * sizeof(int);
   EvictWs w;
   w.off_to = align256(list);
   w.total = w.off_to + align256(list > 0 ? list : 1);
@@ -352,8 +352,8 @@ int attn_cache_evict(const attn_paged_kv* cache, int dtype, int batch, int h_k, 
   p.pos_in = positions_in;
   p.pos_out = positions_out;
   p.stride = state_stride;
-  p.from = reinterpret_cast<int2*>(ws);
-  p.to = reinterpret_cast<int2*>(ws + w.off_to);
+  p.from = reinterpret_cast<int*>(ws);
+  p.to = reinterpret_cast<int*>(ws + w.off_to);
   p.move_cap = evict_move_cap(budget, max_seqlen);
   if ((rc = status_of(&p.status))) return rc;
   const cudaError_t e = launch_evict(p, dtype, reinterpret_cast<cudaStream_t>(stream));
