@@ -26,6 +26,8 @@ int check_rows(const attn_tensor* t, const char* name, int64_t nb, int64_t ns, i
                   "%s: strides must be positive multiples of 8 elements (got b=%lld s=%lld h=%lld)",
                   name, static_cast<long long>(t->stride_b), static_cast<long long>(t->stride_s),
                   static_cast<long long>(t->stride_h));
+  if (nh > 1 && t->stride_h > INT32_MAX)
+    return fail(ATTN_ERR_STRIDE, "%s: the head stride must stay below 2^31 elements", name);
   return ATTN_OK;
 }
 

@@ -4,11 +4,11 @@
 //
 // Pair i of a token's head row is turned by angle = position * inv_freq[i]:
 //   (x, y) -> (x cos - y sin, x sin + y cos);
-// the gradient is the same with -sin.  A block takes a few tokens with all their
-// heads and computes each token's n_freq sines and cosines once, into shared
-// memory, so the heads cost two FMAs and a rounding an element and the kernel is
-// bound by the memory it streams: every row is read once and written once, 16
-// bytes a thread.
+// the gradient is the same with -sin.  A warp takes a token (or a part of its heads, when
+// there are few tokens): it computes the token's n_freq sines and cosines once, and its
+// lanes hold those of their chunk in registers while they pass over the heads, so a head
+// costs two FMAs and a rounding an element and the kernel is bound by the memory it
+// streams: every row is read once and written once, 16 bytes a lane, four rows in flight.
 //
 // The angle is reduced before it is rounded: inv_freq / 2 pi is held as a 64-bit
 // fraction of a turn F, and position * F modulo 2^64 is exactly the fraction of
@@ -22,195 +22,258 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 16;  // tokens of a block
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;   // row groups of a warp in flight
+// Blocks resident on an SM: halves hold two chunks a row group and eight turns, 128
+// registers; pairs and copies less (16384 tokens of 40 heads of 128, halves: 54.6 us with
+// two blocks, 60.1 with three; pairs, 17400 appended tokens of 32 heads: 84.1 and 79.1).
+template <int MODE>
+constexpr int kBlocks = MODE == 0 ? 2 : 3;
 
 enum RopeMode { kHalves = 0, kPairs = 1, kScalar = 2 };
 
+// How a warp's lanes share the rows: 1 << lanes_log2 lanes take one rotated row (its
+// units: chunk pairs that turn, then chunks that are copied; kScalar: pairs of elements,
+// the lanes looping over them), 1 << v_lanes_log2 lanes one row of v (its chunks).
 struct RopeGrid {
-  int tile;          // tokens of a block
-  FastDiv per_token; // units of a token: (h_q + h_k) * per_row + (append) h_k * chunks
-  FastDiv per_row;   // units of a rotated row
-  FastDiv chunks;    // 16-byte chunks of a row
-  int rot_units;     // units of a row that turn pairs (the rest copies)
-  FastDiv seq;       // seqlen (padded tensors)
+  int lanes_log2, v_lanes_log2;
+  int units, rot_units, chunks;
+  int q_groups, k_groups, v_groups;  // groups of rows that a warp takes at once
+  int parts;             // warps that share a token's groups
+  FastDiv part, seq;
 };
 
 template <typename T>
-__device__ __forceinline__ void turn8(uint4& lo, uint4& hi, const float2* cs, float sign) {
+__device__ __forceinline__ void turn8(uint4& lo, uint4& hi, const float2* cs) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
   uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = Pack<T>::unpack(a[i]), y = Pack<T>::unpack(b[i]);
     const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
-    const float s0 = c0.y * sign, s1 = c1.y * sign;
+    const float s0 = c0.y, s1 = c1.y;
     a[i] = Pack<T>::two(x.x * c0.x - y.x * s0, x.y * c1.x - y.y * s1);
     b[i] = Pack<T>::two(x.x * s0 + y.x * c0.x, x.y * s1 + y.y * c1.x);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void turn_pairs(uint4& v, const float2* cs, float sign) {
+__device__ __forceinline__ void turn_pairs(uint4& v, const float2* cs) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = Pack<T>::unpack(a[i]);
     const float2 c = cs[i];
-    const float s = c.y * sign;
+    const float s = c.y;
     a[i] = Pack<T>::two(x.x * c.x - x.y * s, x.x * s + x.y * c.x);
   }
 }
 
 struct TokenInfo {
   int64_t k_off, v_off;  // element offsets of the token's slot (head 0) in the cache
-  int seq, slot;         // slot < 0: not stored
-  int live;              // belongs to a sequence
+  int slot;              // < 0: not stored
+  bool live;             // belongs to a sequence
 };
 
-// Sequence and slot of new token t, with every device-side check.
-__device__ void locate(const RopeParams& p, int64_t t, TokenInfo& out) {
-  out.live = 0;
-  out.slot = -1;
-  int b = static_cast<int>(t), i = 0;
+// Sequence and slot of new token t, with every device-side check, by a whole warp; its
+// first part also writes the token's number into slot_positions.
+__device__ __forceinline__ TokenInfo locate(const RopeParams& p, int t, bool first_part) {
+  const int lane = lane_id();
+  TokenInfo info{0, 0, -1, false};
+  int b = t, i = 0;
   if (p.cu != nullptr) {
-    b = seq_of_row(p.cu, p.batch, static_cast<int>(t));
-    const int c0 = p.cu[b], c1 = p.cu[b + 1];
-    if (t >= p.cu[p.batch]) return;  // behind the last sequence
-    if (t < c0 || t >= c1) {
-      report(p.status, kBadOffsets);
-      return;
+    int lo = 0, hi = p.batch;  // the last sequence that starts at or before t, 32 probes a step
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi - 1);
+      const int n = __popc(__ballot_sync(0xffffffffu, p.cu[at] <= t));
+      lo = min(lo + max(n - 1, 0) * step, hi - 1);
+      hi = min(lo + step, hi);
     }
-    i = static_cast<int>(t) - c0;
+    b = lo;
+    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+    if (t >= p.cu[p.batch]) return info;  // behind the last sequence
+    if (t < c0 || t >= c1) {
+      if (lane == 0) report(p.status, kBadOffsets);
+      return info;
+    }
+    i = t - c0;
   }
-  out.live = 1;
-  out.seq = b;
+  info.live = true;
   const int n = p.seqlens[b];
   const int64_t slot = static_cast<int64_t>(n) + i;
   const int64_t cap = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d;
   if (n < 0 || slot >= cap || (p.slot_positions != nullptr && slot >= p.slots_stride)) {
-    report(p.status, kBadLength);
-    return;
+    if (lane == 0) report(p.status, kBadLength);
+    return info;
   }
   int page, within;
   if (!page_of(p.cache, p.cache.table + b * p.cache.table_stride, static_cast<int>(slot), page,
                within, p.status))
-    return;
-  out.slot = static_cast<int>(slot);
-  out.k_off = page * p.cache.k.sb + within * p.cache.k.ss;
-  out.v_off = page * p.cache.v.sb + within * p.cache.v.ss;
-  if (p.slot_positions != nullptr) {
+    return info;
+  info.slot = static_cast<int>(slot);
+  info.k_off = page * p.cache.k.sb + within * p.cache.k.ss;
+  info.v_off = page * p.cache.v.sb + within * p.cache.v.ss;
+  if (first_part && p.slot_positions != nullptr) {
     const int number = p.seen[b] + i;
-    for (int h = 0; h < p.h_k; ++h)
+    for (int h = lane; h < p.h_k; h += 32)
       p.slot_positions[(static_cast<int64_t>(b) * p.h_k + h) * p.slots_stride + slot] = number;
   }
+  return info;
 }
 
 template <typename T, int MODE, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, RopeGrid g) {
-  extern __shared__ float2 cs_all[];  // [tile][n_freq] (cos, sin)
+__global__ void __launch_bounds__(kThreads, kBlocks<MODE>) rope_kernel(RopeParams p, RopeGrid g) {
+  extern __shared__ float2 cs_all[];  // [warp][n_freq] (cos, sin)
   __shared__ unsigned long long turns[128];
-  __shared__ TokenInfo info[kMaxTile];
-  const int nf = p.rot.n_freq;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * g.tile;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(g.tile), p.tokens - t0));
+  const int nf = p.rot.n_freq, lane = lane_id(), warp = threadIdx.x >> 5;
+  float2* cs = cs_all + warp * nf;
 
   // fraction of a turn that one position adds at each frequency, times 2^64
   for (int i = threadIdx.x; i < nf; i += kThreads) {
     const double x = static_cast<double>(p.rot.inv_freq[i]) * 0.15915494309189535;
     turns[i] = static_cast<unsigned long long>((x - floor(x)) * 18446744073709551616.0);
   }
-  if (APPEND) {
-    for (int i = threadIdx.x; i < nt; i += kThreads) locate(p, t0 + i, info[i]);
-    if (blockIdx.x == 0 && p.cu != nullptr)
-      for (int i = threadIdx.x; i < p.batch; i += kThreads)
-        if (p.cu[i] < 0 || p.cu[i] > p.cu[i + 1]) report(p.status, kBadOffsets);
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < nt * nf; u += kThreads) {
-    const int t = u / nf, i = u - t * nf;
-    int axis = 0;
-#pragma unroll
-    for (int a = 0; a < 3; ++a) axis += i >= p.rot.end[a] ? 1 : 0;
-    const long long pos = p.rot.positions[axis * p.rot.axis_stride + t0 + t];
-    const unsigned long long phase = static_cast<unsigned long long>(pos) * turns[i];
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);
-    cs_all[u] = make_float2(c, s);
-  }
+  if (APPEND && blockIdx.x == 0 && p.cu != nullptr)
+    for (int i = threadIdx.x; i < p.batch; i += kThreads)
+      if (p.cu[i] < 0 || p.cu[i] > p.cu[i + 1]) report(p.status, kBadOffsets);
   __syncthreads();
 
-  const int total = nt * static_cast<int>(g.per_token.d);
-  const int rotated = (p.h_q + p.h_k) * static_cast<int>(g.per_row.d);
-  for (int w = threadIdx.x; w < total; w += kThreads) {
-    const int t = static_cast<int>(g.per_token.div(w));
-    int u = w - t * static_cast<int>(g.per_token.d);
-    const int64_t token = t0 + t;
-    if (APPEND && u >= rotated) {  // v: copied into its slot
-      u -= rotated;
-      const int h = static_cast<int>(g.chunks.div(u));
-      const int c = u - h * static_cast<int>(g.chunks.d);
-      if (info[t].slot < 0) continue;
-      const T* src = static_cast<const T*>(p.v.ptr) + token * p.v.ss + h * p.v.sh;
-      T* dst = static_cast<T*>(const_cast<void*>(p.cache.v.ptr)) + info[t].v_off + h * p.cache.v.sh;
-      *reinterpret_cast<uint4*>(dst + 8 * c) = *reinterpret_cast<const uint4*>(src + 8 * c);
-      continue;
+  const int c = lane & ((1 << g.lanes_log2) - 1), rl = lane >> g.lanes_log2;
+  const bool turns_here = c < g.rot_units;
+  const int total = g.q_groups + g.k_groups + g.v_groups;
+  const int64_t items = p.tokens * g.parts, step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += step) {
+    int64_t token = item;
+    int begin = 0, end = total;
+    bool first_part = true;
+    if (g.parts > 1) {
+      token = item / g.parts;
+      const int part = static_cast<int>(item - token * g.parts);
+      first_part = part == 0;
+      begin = static_cast<int>(g.part.div(part * total));
+      end = static_cast<int>(g.part.div((part + 1) * total));
     }
-    int h = static_cast<int>(g.per_row.div(u));
-    u -= h * static_cast<int>(g.per_row.d);
-    const T* src;
-    T* dst;
     int64_t b = 0, s = token;
     if (!APPEND) {
       b = g.seq.div(static_cast<uint32_t>(token));
       s = token - b * g.seq.d;
     }
-    if (h < p.h_q) {
-      if (APPEND && !info[t].live) continue;
-      src = static_cast<const T*>(p.q.ptr) + b * p.q.sb + s * p.q.ss + h * p.q.sh;
-      dst = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + b * p.oq.sb + s * p.oq.ss + h * p.oq.sh;
-    } else {
-      h -= p.h_q;
-      src = static_cast<const T*>(p.k.ptr) + b * p.k.sb + s * p.k.ss + h * p.k.sh;
-      if (APPEND) {
-        if (info[t].slot < 0) continue;
-        dst = static_cast<T*>(const_cast<void*>(p.cache.k.ptr)) + info[t].k_off + h * p.cache.k.sh;
-      } else {
-        dst = static_cast<T*>(const_cast<void*>(p.ok.ptr)) + b * p.ok.sb + s * p.ok.ss + h * p.ok.sh;
+    TokenInfo info{0, 0, -1, false};
+    bool ready = false;
+    // what the stores need, worked out while the first rows are on their way
+    auto prepare = [&]() {
+      if (APPEND) info = locate(p, static_cast<int>(token), first_part);
+      __syncwarp();  // the last token's values have been read
+      for (int i = lane; i < nf; i += 32) {
+        int axis = 0;
+#pragma unroll
+        for (int a = 0; a < 3; ++a) axis += i >= p.rot.end[a] ? 1 : 0;
+        const long long pos = p.rot.positions[axis * p.rot.axis_stride + token];
+        const unsigned long long phase = static_cast<unsigned long long>(pos) * turns[i];
+        float sn, cn;
+        sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &sn, &cn);
+        cs[i] = make_float2(cn, sn * p.rot.sign);
       }
-    }
-    const float2* cs = cs_all + t * nf;
-    if (MODE == kScalar) {  // sizes that are not whole chunks: one pair of elements
-      int i0 = 2 * u, i1 = 2 * u + 1;
-      if (u < nf && !p.rot.interleaved) {
-        i0 = u;
-        i1 = u + nf;
+      __syncwarp();
+      ready = true;
+    };
+    // The rows of q, of k, and of v (copied).  Head strides stay below 2^31 elements.
+    int g0 = 0;
+#pragma unroll 1
+    for (int kind = 0; kind < (APPEND ? 3 : 2); ++kind) {
+      const int n = kind == 0 ? p.h_q : p.h_k;
+      const int groups = kind == 0 ? g.q_groups : (kind == 1 ? g.k_groups : g.v_groups);
+      const int lanes_log2 = kind == 2 ? g.v_lanes_log2 : g.lanes_log2, rpw = 32 >> lanes_log2;
+      const int it_begin = max(begin - g0, 0), it_end = min(end - g0, groups);
+      g0 += groups;
+      if (it_begin >= it_end) continue;
+      const TensorArg& in = kind == 0 ? p.q : (kind == 1 ? p.k : p.v);
+      const uint32_t ss = static_cast<uint32_t>(in.sh);
+      const T* src = static_cast<const T*>(in.ptr) + b * in.sb + s * in.ss;
+      auto target = [&](uint32_t& ds) -> T* {  // nullptr: not stored
+        if (!APPEND || kind == 0) {
+          const TensorArg& out = kind == 0 ? p.oq : p.ok;
+          ds = static_cast<uint32_t>(out.sh);
+          if (APPEND && !info.live) return nullptr;
+          return static_cast<T*>(const_cast<void*>(out.ptr)) + b * out.sb + s * out.ss;
+        }
+        const TensorArg& out = kind == 1 ? p.cache.k : p.cache.v;
+        ds = static_cast<uint32_t>(out.sh);
+        if (info.slot < 0) return nullptr;
+        return static_cast<T*>(const_cast<void*>(out.ptr)) + (kind == 1 ? info.k_off : info.v_off);
+      };
+
+      if (MODE == kScalar && kind < 2) {  // sizes that are not whole chunks: pairs of elements
+        if (!ready) prepare();
+        uint32_t ds;
+        T* dst = target(ds);
+        if (dst == nullptr) continue;
+        for (int r = it_begin * rpw + rl; r < min(n, it_end * rpw); r += rpw)
+          for (int u = c; u < g.units; u += 1 << lanes_log2) {
+            const bool turn = u < nf;
+            const int i0 = turn && !p.rot.interleaved ? u : 2 * u;
+            const int i1 = turn && !p.rot.interleaved ? u + nf : 2 * u + 1;
+            const T* x = src + static_cast<uint64_t>(ss) * r;
+            T* y = dst + static_cast<uint64_t>(ds) * r;
+            const float x0 = static_cast<float>(x[i0]), x1 = static_cast<float>(x[i1]);
+            const float2 a = turn ? cs[u] : make_float2(1.f, 0.f);
+            y[i0] = static_cast<T>(x0 * a.x - x1 * a.y);
+            y[i1] = static_cast<T>(x0 * a.y + x1 * a.x);
+          }
+        continue;
       }
-      float x = static_cast<float>(src[i0]), y = static_cast<float>(src[i1]);
-      if (u < nf) {
-        const float c = cs[u].x, sn = cs[u].y * p.rot.sign;
-        const float a = x * c - y * sn;
-        y = x * sn + y * c;
-        x = a;
+      const int cc = kind == 2 ? lane & ((1 << lanes_log2) - 1) : c, r0 = kind == 2 ? lane >> lanes_log2 : rl;
+      const bool lane_on = cc < (kind == 2 ? g.chunks : g.units), turn = kind < 2 && turns_here;
+      // elements of this lane's chunk in a row (halves: the pairs' second chunk is nf behind)
+      const int at = MODE == kPairs || turn || kind == 2 ? 8 * cc : 2 * nf + 8 * (cc - g.rot_units);
+      constexpr int kTurns = MODE == kHalves ? 8 : 4;
+      float2 mine[kTurns];
+      bool have = false;
+#pragma unroll 1
+      for (int it = it_begin; it < it_end; it += kBatch) {
+        uint4 lo[kBatch], hi[kBatch];
+        const int row = it * rpw + r0;
+        const int rows_on = lane_on ? min(n, it_end * rpw) - row : 0;  // of this lane, from `row` on
+        const T* x = src + static_cast<uint64_t>(ss) * static_cast<uint32_t>(row) + at;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i * rpw < rows_on) {
+            const T* xi = x + static_cast<uint64_t>(ss) * static_cast<uint32_t>(i * rpw);
+            lo[i] = *reinterpret_cast<const uint4*>(xi);
+            if (MODE == kHalves && turn) hi[i] = *reinterpret_cast<const uint4*>(xi + nf);
+          }
+        if (!ready) prepare();
+        if (!have && turn)
+#pragma unroll
+          for (int i = 0; i < kTurns; ++i) mine[i] = cs[kTurns * cc + i];
+        have = true;
+        uint32_t ds;
+        T* y = target(ds);
+        if (y == nullptr) break;
+        y += static_cast<uint64_t>(ds) * static_cast<uint32_t>(row) + at;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i * rpw < rows_on) {
+            T* yi = y + static_cast<uint64_t>(ds) * static_cast<uint32_t>(i * rpw);
+            if (turn) {
+              if (MODE == kHalves) {
+                turn8<T>(lo[i], hi[i], mine);
+                *reinterpret_cast<uint4*>(yi + nf) = hi[i];
+              } else {
+                turn_pairs<T>(lo[i], mine);
+              }
+            }
+            *reinterpret_cast<uint4*>(yi) = lo[i];
+          }
       }
-      dst[i0] = static_cast<T>(x);
-      dst[i1] = static_cast<T>(y);
-    } else if (u < g.rot_units) {
-      if (MODE == kHalves) {
-        uint4 lo = *reinterpret_cast<const uint4*>(src + 8 * u);
-        uint4 hi = *reinterpret_cast<const uint4*>(src + nf + 8 * u);
-        turn8<T>(lo, hi, cs + 8 * u, p.rot.sign);
-        *reinterpret_cast<uint4*>(dst + 8 * u) = lo;
-        *reinterpret_cast<uint4*>(dst + nf + 8 * u) = hi;
-      } else {
-        uint4 v = *reinterpret_cast<const uint4*>(src + 8 * u);
-        turn_pairs<T>(v, cs + 4 * u, p.rot.sign);
-        *reinterpret_cast<uint4*>(dst + 8 * u) = v;
-      }
-    } else if (src != dst) {
-      const int at = 2 * nf + 8 * (u - g.rot_units);
-      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
     }
   }
+}
+
+int log2_at_least(int n) {  // of the power of two that is at least n, at most 32
+  int l = 0;
+  while (l < 5 && (1 << l) < n) ++l;
+  return l;
 }
 
 template <typename T, bool APPEND>
@@ -220,19 +283,28 @@ cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   const int mode = p.rot.interleaved ? (nf % 4 == 0 ? kPairs : kScalar)
                                      : (nf % 8 == 0 ? kHalves : kScalar);
   RopeGrid g;
+  g.chunks = d / 8;
   g.rot_units = mode == kHalves ? nf / 8 : (mode == kPairs ? nf / 4 : nf);
-  const int copies = mode == kScalar ? (d - 2 * nf) / 2 : (d - 2 * nf) / 8;
-  g.per_row.set(static_cast<uint32_t>(g.rot_units + copies));
-  g.chunks.set(static_cast<uint32_t>(d / 8));
-  const int64_t units = static_cast<int64_t>(p.h_q + p.h_k) * g.per_row.d +
-                        (APPEND ? static_cast<int64_t>(p.h_k) * g.chunks.d : 0);
-  if (units * kMaxTile > INT32_MAX) return cudaErrorInvalidValue;
-  g.per_token.set(static_cast<uint32_t>(units));
+  g.units = g.rot_units + (mode == kScalar ? (d - 2 * nf) / 2 : (d - 2 * nf) / 8);
+  g.lanes_log2 = log2_at_least(g.units);
+  g.v_lanes_log2 = log2_at_least(g.chunks);
+  g.q_groups = ceil_div(p.h_q, 32 >> g.lanes_log2);
+  g.k_groups = ceil_div(p.h_k, 32 >> g.lanes_log2);
+  g.v_groups = APPEND ? ceil_div(p.h_k, 32 >> g.v_lanes_log2) : 0;
+  // few tokens: a token's groups are shared by several warps, down to a batch each, so
+  // that every resident warp has about four items and none waits long for the others
+  const int64_t most = static_cast<int64_t>(num_sms()) * (mode == kHalves ? kBlocks<kHalves> : kBlocks<kPairs>);
+  const int64_t groups = static_cast<int64_t>(g.q_groups) + g.k_groups + g.v_groups;
+  const int64_t batches = (groups + kBatch - 1) / kBatch;
+  int64_t parts = 4 * most * kWarps / p.tokens;
+  parts = parts < 1 ? 1 : (parts > batches ? batches : parts);
+  g.parts = static_cast<int>(parts);
+  if (groups * (parts + 1) > INT32_MAX) return cudaErrorInvalidValue;
+  g.part.set(static_cast<uint32_t>(parts));
   g.seq.set(static_cast<uint32_t>(p.seqlen));
-  const int64_t tile = p.tokens / (4 * static_cast<int64_t>(num_sms()));
-  g.tile = static_cast<int>(tile < 1 ? 1 : (tile > kMaxTile ? kMaxTile : tile));
-  const unsigned blocks = static_cast<unsigned>((p.tokens + g.tile - 1) / g.tile);
-  const size_t smem = static_cast<size_t>(g.tile) * nf * sizeof(float2);
+  int64_t grid = (p.tokens * parts + kWarps - 1) / kWarps;
+  const unsigned blocks = static_cast<unsigned>(grid < most ? grid : most);
+  const size_t smem = static_cast<size_t>(kWarps) * nf * sizeof(float2);
   if (mode == kHalves)
     rope_kernel<T, kHalves, APPEND><<<blocks, kThreads, smem, stream>>>(p, g);
   else if (mode == kPairs)
