@@ -28,13 +28,17 @@ constexpr int kBatch = 4;   // row groups of a warp in flight
 // registers; pairs and copies less (16384 tokens of 40 heads of 128, halves: 54.6 us with
 // two blocks, 60.1 with three; pairs, 17400 appended tokens of 32 heads: 84.1 and 79.1).
 template <int MODE>
-constexpr int kBlocks = MODE == 0 ? 2 : 3;
+constexpr int kBlocks = MODE == 1 ? 3 : 2;
 
-enum RopeMode { kHalves = 0, kPairs = 1, kScalar = 2 };
+// kHalves: a lane takes a chunk of 8 first elements and the chunk of their second ones
+// (n_freq a multiple of 8).  kPairs: neighbouring elements, any n_freq.  kMixed: halves
+// whose second elements start inside a chunk; a lane takes one chunk and reads the other
+// elements of its pairs beside it, all of a row before the row is written.
+enum RopeMode { kHalves = 0, kPairs = 1, kMixed = 2 };
 
 // How a warp's lanes share the rows: 1 << lanes_log2 lanes take one rotated row (its
-// units: chunk pairs that turn, then chunks that are copied; kScalar: pairs of elements,
-// the lanes looping over them), 1 << v_lanes_log2 lanes one row of v (its chunks).
+// units: chunks or chunk pairs that turn, then chunks that are copied), 1 << v_lanes_log2
+// lanes one row of v (its chunks).
 struct RopeGrid {
   int lanes_log2, v_lanes_log2;
   int units, rot_units, chunks;
@@ -57,15 +61,32 @@ __device__ __forceinline__ void turn8(uint4& lo, uint4& hi, const float2* cs) {
   }
 }
 
+// The first `n` of a chunk's four pairs turn.
 template <typename T>
-__device__ __forceinline__ void turn_pairs(uint4& v, const float2* cs) {
+__device__ __forceinline__ void turn_pairs(uint4& v, const float2* cs, int n) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (i >= n) break;
     const float2 x = Pack<T>::unpack(a[i]);
     const float2 c = cs[i];
     const float s = c.y;
     a[i] = Pack<T>::two(x.x * c.x - x.y * s, x.x * s + x.y * c.x);
+  }
+}
+
+// Element i of a chunk becomes x cs.x + y cs.y with its pair's other element y (cs.y is
+// -sin in the first half of the pairs, sin in the second); the first `n` (even) turn.
+template <typename T>
+__device__ __forceinline__ void turn_mixed(uint4& v, const uint32_t (&other)[4], const float2* cs, int n) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = Pack<T>::unpack(a[i]);
+    const float2 y = Pack<T>::unpack(other[i]);
+    if (2 * i < n)
+      a[i] = Pack<T>::two(x.x * cs[2 * i].x + y.x * cs[2 * i].y,
+                          x.y * cs[2 * i + 1].x + y.y * cs[2 * i + 1].y);
   }
 }
 
@@ -203,35 +224,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks<MODE>) rope_kernel(RopeParam
         return static_cast<T*>(const_cast<void*>(out.ptr)) + (kind == 1 ? info.k_off : info.v_off);
       };
 
-      if (MODE == kScalar && kind < 2) {  // sizes that are not whole chunks: pairs of elements
-        if (!ready) prepare();
-        uint32_t ds;
-        T* dst = target(ds);
-        if (dst == nullptr) continue;
-        for (int r = it_begin * rpw + rl; r < min(n, it_end * rpw); r += rpw)
-          for (int u = c; u < g.units; u += 1 << lanes_log2) {
-            const bool turn = u < nf;
-            const int i0 = turn && !p.rot.interleaved ? u : 2 * u;
-            const int i1 = turn && !p.rot.interleaved ? u + nf : 2 * u + 1;
-            const T* x = src + static_cast<uint64_t>(ss) * r;
-            T* y = dst + static_cast<uint64_t>(ds) * r;
-            const float x0 = static_cast<float>(x[i0]), x1 = static_cast<float>(x[i1]);
-            const float2 a = turn ? cs[u] : make_float2(1.f, 0.f);
-            y[i0] = static_cast<T>(x0 * a.x - x1 * a.y);
-            y[i1] = static_cast<T>(x0 * a.y + x1 * a.x);
-          }
-        continue;
-      }
       const int cc = kind == 2 ? lane & ((1 << lanes_log2) - 1) : c, r0 = kind == 2 ? lane >> lanes_log2 : rl;
       const bool lane_on = cc < (kind == 2 ? g.chunks : g.units), turn = kind < 2 && turns_here;
       // elements of this lane's chunk in a row (halves: the pairs' second chunk is nf behind)
-      const int at = MODE == kPairs || turn || kind == 2 ? 8 * cc : 2 * nf + 8 * (cc - g.rot_units);
-      constexpr int kTurns = MODE == kHalves ? 8 : 4;
+      const int at = MODE != kHalves || turn || kind == 2 ? 8 * cc : 2 * nf + 8 * (cc - g.rot_units);
+      constexpr int kTurns = MODE == kPairs ? 4 : 8;
+      // of this lane's pairs (or elements, kMixed) the first ones that turn
+      const int n_turn = min(kTurns, MODE == kPairs ? nf - 4 * cc : (MODE == kMixed ? 2 * nf - 8 * cc : 8));
       float2 mine[kTurns];
       bool have = false;
 #pragma unroll 1
       for (int it = it_begin; it < it_end; it += kBatch) {
         uint4 lo[kBatch], hi[kBatch];
+        uint32_t other[MODE == kMixed ? kBatch : 1][4];
         const int row = it * rpw + r0;
         const int rows_on = lane_on ? min(n, it_end * rpw) - row : 0;  // of this lane, from `row` on
         const T* x = src + static_cast<uint64_t>(ss) * static_cast<uint32_t>(row) + at;
@@ -241,12 +246,37 @@ __global__ void __launch_bounds__(kThreads, kBlocks<MODE>) rope_kernel(RopeParam
             const T* xi = x + static_cast<uint64_t>(ss) * static_cast<uint32_t>(i * rpw);
             lo[i] = *reinterpret_cast<const uint4*>(xi);
             if (MODE == kHalves && turn) hi[i] = *reinterpret_cast<const uint4*>(xi + nf);
+            if (MODE == kMixed && turn) {
+              if (nf % 2 == 0) {  // two elements at a time: both lie in one half
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = at + 2 * k;
+                  other[i][k] = e < 2 * nf ? *reinterpret_cast<const uint32_t*>(xi + 2 * k + (e < nf ? nf : -nf)) : 0u;
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int e = at + k;
+                  const uint32_t y =
+                      e < 2 * nf ? *reinterpret_cast<const unsigned short*>(xi + k + (e < nf ? nf : -nf)) : 0u;
+                  other[i][k / 2] = k % 2 == 0 ? y : other[i][k / 2] | (y << 16);
+                }
+              }
+            }
           }
         if (!ready) prepare();
         if (!have && turn)
 #pragma unroll
-          for (int i = 0; i < kTurns; ++i) mine[i] = cs[kTurns * cc + i];
+          for (int i = 0; i < kTurns; ++i)
+            if (i < n_turn) {
+              const int f = kTurns * cc + i;
+              mine[i] = cs[MODE == kMixed && f >= nf ? f - nf : f];
+              if (MODE == kMixed && f < nf) mine[i].y = -mine[i].y;
+            } else {
+              mine[i] = make_float2(0.f, 0.f);  // not used
+            }
         have = true;
+        if (MODE == kMixed) __syncwarp();  // every lane has read its pairs' other elements
         uint32_t ds;
         T* y = target(ds);
         if (y == nullptr) break;
@@ -259,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<MODE>) rope_kernel(RopeParam
               if (MODE == kHalves) {
                 turn8<T>(lo[i], hi[i], mine);
                 *reinterpret_cast<uint4*>(yi + nf) = hi[i];
+              } else if (MODE == kPairs) {
+                turn_pairs<T>(lo[i], mine, n_turn);
               } else {
-                turn_pairs<T>(lo[i], mine);
+                turn_mixed<T>(lo[i], other[i], mine, n_turn);
               }
             }
             *reinterpret_cast<uint4*>(yi) = lo[i];
@@ -279,13 +311,11 @@ int log2_at_least(int n) {  // of the power of two that is at least n, at most 3
 template <typename T, bool APPEND>
 cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   const int nf = p.rot.n_freq, d = p.head_dim;
-  // 16-byte chunks need whole chunks of pairs: 8 frequencies (halves) or 4 (pairs)
-  const int mode = p.rot.interleaved ? (nf % 4 == 0 ? kPairs : kScalar)
-                                     : (nf % 8 == 0 ? kHalves : kScalar);
+  const int mode = p.rot.interleaved ? kPairs : (nf % 8 == 0 ? kHalves : kMixed);
   RopeGrid g;
   g.chunks = d / 8;
-  g.rot_units = mode == kHalves ? nf / 8 : (mode == kPairs ? nf / 4 : nf);
-  g.units = g.rot_units + (mode == kScalar ? (d - 2 * nf) / 2 : (d - 2 * nf) / 8);
+  g.rot_units = mode == kHalves ? nf / 8 : (2 * nf + 7) / 8;
+  g.units = mode == kHalves ? g.rot_units + (d - 2 * nf) / 8 : d / 8;
   g.lanes_log2 = log2_at_least(g.units);
   g.v_lanes_log2 = log2_at_least(g.chunks);
   g.q_groups = ceil_div(p.h_q, 32 >> g.lanes_log2);
@@ -293,7 +323,7 @@ cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   g.v_groups = APPEND ? ceil_div(p.h_k, 32 >> g.v_lanes_log2) : 0;
   // few tokens: a token's groups are shared by several warps, down to a batch each, so
   // that every resident warp has about four items and none waits long for the others
-  const int64_t most = static_cast<int64_t>(num_sms()) * (mode == kHalves ? kBlocks<kHalves> : kBlocks<kPairs>);
+  const int64_t most = static_cast<int64_t>(num_sms()) * (mode == kPairs ? kBlocks<kPairs> : kBlocks<kHalves>);
   const int64_t groups = static_cast<int64_t>(g.q_groups) + g.k_groups + g.v_groups;
   const int64_t batches = (groups + kBatch - 1) / kBatch;
   int64_t parts = 4 * most * kWarps / p.tokens;
@@ -310,7 +340,7 @@ cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   else if (mode == kPairs)
     rope_kernel<T, kPairs, APPEND><<<blocks, kThreads, smem, stream>>>(p, g);
   else
-    rope_kernel<T, kScalar, APPEND><<<blocks, kThreads, smem, stream>>>(p, g);
+    rope_kernel<T, kMixed, APPEND><<<blocks, kThreads, smem, stream>>>(p, g);
   return cudaGetLastError();
 }
 
