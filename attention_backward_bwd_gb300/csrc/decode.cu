@@ -623,20 +623,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
   }
 }
 
-// Joins the partials of cut segments, writes the rows of empty sequences, and adds the
-// attention weights.  The first `runs * part_rows` blocks take one row of the segment that
-// starts in their run and is cut at its end, if there is one; then come `chunks` blocks
-// of kKeys keys for every (sequence, key/value head) when weights are asked for.
-constexpr int kKeys = 1024;
-
+// Joins the partials of cut segments and writes the rows of empty sequences: a block takes
+// one row of the segment that starts in its run and is cut at its end, if there is one.
 template <typename T>
-__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, int row_blocks, int dp,
-                                                     int chunks) {
+__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, int dp) {
   __shared__ int s_sums[kJoin / 32];
   __shared__ int s_pre[kJoin];
-  __shared__ int s_before;
   __shared__ float4 s_part[kJoin];
-  __shared__ float s_lse[256];
+  __shared__ float s_lse[kJoin];
   __shared__ float s_w[kMaxRuns];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
@@ -644,196 +638,139 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, i
   const int part_m = p.part_rows * dp;
   auto len_of = [&](int b) { return clean_len(p, p.seqlens[b], false); };
   Cut cut;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (static_cast<int>(blockIdx.x) < row_blocks) {
-    for (int b = blockIdx.x; b < p.batch; b += row_blocks)
-      if (clean_len(p, p.seqlens[b], runs == 0) == 0)
-        for (int hv = 0; hv < hv_n; ++hv) no_keys<T>(p, b, hv);
-    int total;
-    s_pre[tid] = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
-    cut.total = static_cast<long long>(total) * hv_n;
-    cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
-    __syncthreads();
-    const int run = blockIdx.x / p.part_rows, row = blockIdx.x - run * p.part_rows;
-    bool mine = run + 1 < cut.runs;  // a run with an end inside the line
-    int b = 0, hv = 0, nc = 0, lead = 0;
-    if (mine) {
-      const long long r0 = cut.start(run), e = cut.start(run + 1);
-      int before;
-      b = find_sequence<kJoin>(p, s_pre, per, hv_n, e - 1, len_of, before);
-      const int t_b = tiles_of(p, len_of(b));
-      const long long line0 = static_cast<long long>(before) * hv_n;
-      hv = static_cast<int>((e - 1 - line0) / t_b);
-      const long long s0 = line0 + static_cast<long long>(hv) * t_b;
-      mine = s0 >= r0 && s0 + t_b > e &&
-             row < p.group - (hv % p.head_tiles) * kMaxRows;  // starts here, goes on, has this row
-      if (mine) {
-        nc = cut.run_of(s0 + t_b - 1) - run + 1;
-        lead = r0 == s0 ? 0 : 1;  // only in its first run can the segment be the second
-      }
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
-    const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
-    float top = -INFINITY, sum = 0.f;
-    for (int i = tid; i < nc; i += kJoin) {
-      const float x = partial(p, run + i, i == 0 ? lead : 0)[part_m + row];
-      s_w[i] = x;
-      top = fmaxf(top, x);
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0) s_lse[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_lse[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-    __syncthreads();
-    // threads: 16-byte column group, and every stripe-th run
-    const int groups = dp / 4, stripes = kJoin / groups;
-    const int cg = tid % groups, st = tid / groups;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (st < stripes) {
-#pragma unroll 4
-      for (int i = st; i < nc; i += stripes) {
-        const float* part = partial(p, run + i, i == 0 ? lead : 0);
-        const float w = ex2(s_w[i] - base);
-        const float4 x = *reinterpret_cast<const float4*>(part + row * dp + cg * 4);
-        sum += w * part[part_m + kMaxRows + row];
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
-      }
-    }
-    s_part[tid] = acc;
-    s_lse[tid] = sum;
-    __syncthreads();
-    if (st == 0) {
-      for (int i = 1; i < stripes; ++i) {
-        const float4 x = s_part[tid + i * groups];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-        sum += s_lse[i * groups];
-      }
-      const bool none = sum == 0.f;
-      const float inv = none ? 0.f : 1.f / sum;
-      T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
-      if (cg * 4 < p.head_dim) {
-        uint2 v;
-        v.x = Pack<T>::two(none ? 0.f : acc.x * inv, none ? 0.f : acc.y * inv);
-        v.y = Pack<T>::two(none ? 0.f : acc.z * inv, none ? 0.f : acc.w * inv);
-        *reinterpret_cast<uint2*>(out + cg * 4) = v;
-      }
-      if (tid == 0 && p.lse != nullptr)
-        p.lse[static_cast<int64_t>(b) * p.h_q + h] =
-            none ? INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
-    }
-    return;
-  }
-
-  // ---- weights of keys [j0, j0 + kKeys), from the first one seen, of one key/value head
-  const int64_t u = blockIdx.x - row_blocks;
-  const int bg = static_cast<int>(u / chunks);
-  const int b = bg / p.h_k, g = bg - b * p.h_k, h = g * p.group;
-  const int n = len_of(b), first = first_key(p, n), t_b = tiles_of(p, n);
-  const int j0 = static_cast<int>(u - static_cast<int64_t>(bg) * chunks) * kKeys;
-  if (j0 >= n) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // no block may end before the first kernel
-    return;
-  }
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (clean_len(p, p.seqlens[b], runs == 0) == 0)
+      for (int hv = 0; hv < hv_n; ++hv) no_keys<T>(p, b, hv);
   int total;
-  const int before = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
-  if (b / per == tid) {
-    int at = before;
-    for (int i = tid * per; i < b; ++i) at += tiles_of(p, len_of(i));
-    s_before = at;
-  }
-  __syncthreads();
+  s_pre[tid] = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
   cut.total = static_cast<long long>(total) * hv_n;
   cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // a thread's keys: 4 neighbours at rel, 4 at rel + kKeys / 2 (the logits' rows start at
-  // the first key seen and are whole tiles)
-  const float* logits = p.logits + (static_cast<int64_t>(b) * p.h_q + h) * p.logit_stride;
-  const int rel0 = j0 + tid * 4, rel1 = rel0 + kKeys / 2, seen = n - first;
-  float w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 0.f;
-  for (int g0 = 0; g0 < p.group; g0 += 256) {
-    const int gn = min(256, p.group - g0);
-    __syncthreads();
-    for (int i = warp; i < gn; i += kJoin / 32) {  // the row's LSE, a warp each
-      const int hg = g0 + i, ht = hg / kMaxRows, row = hg - ht * kMaxRows;
-      const long long s0 = static_cast<long long>(s_before) * hv_n +
-                           static_cast<long long>(g * p.head_tiles + ht) * t_b;
-      const int c0 = cut.run_of(s0), c1 = cut.run_of(s0 + t_b - 1);
-      float lse2;
-      if (c0 == c1) {
-        lse2 = p.lse2[static_cast<int64_t>(b) * p.h_q + h + hg];
-      } else {
-        const int lead = cut.start(c0) >= s0 ? 0 : 1;
-        float top = -INFINITY, sum = 0.f;
-        for (int c = c0 + lane; c <= c1; c += 32)
-          top = fmaxf(top, partial(p, c, c == c0 ? lead : 0)[part_m + row]);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float base = top == -INFINITY ? 0.f : top;
-        for (int c = c0 + lane; c <= c1; c += 32) {
-          const float* part = partial(p, c, c == c0 ? lead : 0);
-          sum += ex2(part[part_m + row] - base) * part[part_m + kMaxRows + row];
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        lse2 = sum == 0.f ? INFINITY : base + log2f(sum);
-      }
-      if (lane == 0) s_lse[i] = lse2;
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int i = 0; i < gn; ++i) {
-      const float lse2 = s_lse[i];
-      const float* x = logits + (g0 + i) * p.logit_stride;
-      if (rel0 < seen) {
-        const float4 v = *reinterpret_cast<const float4*>(x + rel0);
-        w[0] += ex2(v.x - lse2);
-        w[1] += ex2(v.y - lse2);
-        w[2] += ex2(v.z - lse2);
-        w[3] += ex2(v.w - lse2);
-      }
-      if (rel1 < seen) {
-        const float4 v = *reinterpret_cast<const float4*>(x + rel1);
-        w[4] += ex2(v.x - lse2);
-        w[5] += ex2(v.y - lse2);
-        w[6] += ex2(v.z - lse2);
-        w[7] += ex2(v.w - lse2);
-      }
+  __syncthreads();
+  const int run = blockIdx.x / p.part_rows, row = blockIdx.x - run * p.part_rows;
+  bool mine = run + 1 < cut.runs;  // a run with an end inside the line
+  int b = 0, hv = 0, nc = 0, lead = 0;
+  if (mine) {
+    const long long r0 = cut.start(run), e = cut.start(run + 1);
+    int before;
+    b = find_sequence<kJoin>(p, s_pre, per, hv_n, e - 1, len_of, before);
+    const int t_b = tiles_of(p, len_of(b));
+    const long long line0 = static_cast<long long>(before) * hv_n;
+    hv = static_cast<int>((e - 1 - line0) / t_b);
+    const long long s0 = line0 + static_cast<long long>(hv) * t_b;
+    mine = s0 >= r0 && s0 + t_b > e &&
+           row < p.group - (hv % p.head_tiles) * kMaxRows;  // starts here, goes on, has this row
+    if (mine) {
+      nc = cut.run_of(s0 + t_b - 1) - run + 1;
+      lead = r0 == s0 ? 0 : 1;  // only in its first run can the segment be the second
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
+  const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
+  float top = -INFINITY, sum = 0.f;
+  for (int i = tid; i < nc; i += kJoin) {
+    const float x = partial(p, run + i, i == 0 ? lead : 0)[part_m + row];
+    s_w[i] = x;
+    top = fmaxf(top, x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  if (lane == 0) s_lse[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_lse[w]);
+  const float base = top == -INFINITY ? 0.f : top;
+  __syncthreads();
+  // threads: 16-byte column group, and every stripe-th run
+  const int groups = dp / 4, stripes = kJoin / groups;
+  const int cg = tid % groups, st = tid / groups;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (st < stripes) {
+#pragma unroll 4
+    for (int i = st; i < nc; i += stripes) {
+      const float* part = partial(p, run + i, i == 0 ? lead : 0);
+      const float w = ex2(s_w[i] - base);
+      const float4 x = *reinterpret_cast<const float4*>(part + row * dp + cg * 4);
+      sum += w * part[part_m + kMaxRows + row];
+      acc.x += w * x.x;
+      acc.y += w * x.y;
+      acc.z += w * x.z;
+      acc.w += w * x.w;
+    }
+  }
+  s_part[tid] = acc;
+  s_lse[tid] = sum;
+  __syncthreads();
+  if (st == 0) {
+    for (int i = 1; i < stripes; ++i) {
+      const float4 x = s_part[tid + i * groups];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+      sum += s_lse[i * groups];
+    }
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
+    if (cg * 4 < p.head_dim) {
+      uint2 v;
+      v.x = Pack<T>::two(none ? 0.f : acc.x * inv, none ? 0.f : acc.y * inv);
+      v.y = Pack<T>::two(none ? 0.f : acc.z * inv, none ? 0.f : acc.w * inv);
+      *reinterpret_cast<uint2*>(out + cg * 4) = v;
+    }
+    if (tid == 0) {
+      const float lse2 = none ? INFINITY : base + log2f(sum);
+      const int64_t at = static_cast<int64_t>(b) * p.h_q + h;
+      if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
+      if (p.lse2 != nullptr) p.lse2[at] = lse2;
+    }
+  }
+}
+
+// weights_out = weights_in + the group's sum of exp2(logit - LSE2).  A block takes kKeys keys,
+// from the first one seen, of one (sequence, key/value head), a thread four of them.
+constexpr int kKeys = 512;
+
+__global__ void __launch_bounds__(kJoin) weights_kernel(DecodeParams p, int chunks) {
+  const int tid = threadIdx.x;
+  const int bg = blockIdx.x / chunks, b = bg / p.h_k, g = bg - b * p.h_k, h = g * p.group;
+  const int n = clean_len(p, p.seqlens[b], false), first = first_key(p, n), seen = n - first;
+  const int j0 = (blockIdx.x - bg * chunks) * kKeys, rel = j0 + tid * 4;
   const int64_t at = (static_cast<int64_t>(b) * p.h_k + g) * p.w_stride;
   const float* in = p.w_in + at;
   float* out = p.w_out + at;
   // keys before the window keep their weights
   if (out != in)
     for (int j = j0 + tid; j < min(first, j0 + kKeys); j += kJoin) out[j] = in[j];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rel >= seen) return;
+  const float* logits = p.logits + (static_cast<int64_t>(b) * p.h_q + h) * p.logit_stride + rel;
+  const float* lse2 = p.lse2 + static_cast<int64_t>(b) * p.h_q + h;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < p.group; ++i) {
+    const float l = lse2[i];
+    const float4 v = *reinterpret_cast<const float4*>(logits + i * p.logit_stride);
+    w[0] += ex2(v.x - l);
+    w[1] += ex2(v.y - l);
+    w[2] += ex2(v.z - l);
+    w[3] += ex2(v.w - l);
+  }
+  const int j = first + rel;
+  if (rel + 3 < seen && ((reinterpret_cast<uintptr_t>(in + j) | reinterpret_cast<uintptr_t>(out + j)) & 15) == 0) {
+    float4 x = *reinterpret_cast<const float4*>(in + j);
+    x.x += w[0];
+    x.y += w[1];
+    x.z += w[2];
+    x.w += w[3];
+    *reinterpret_cast<float4*>(out + j) = x;
+  } else {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int rel = half ? rel1 : rel0, j = first + rel;
-    const float* v = w + half * 4;
-    if (rel + 3 < seen && ((reinterpret_cast<uintptr_t>(in + j) | reinterpret_cast<uintptr_t>(out + j)) & 15) == 0) {
-      float4 x = *reinterpret_cast<const float4*>(in + j);
-      x.x += v[0];
-      x.y += v[1];
-      x.z += v[2];
-      x.w += v[3];
-      *reinterpret_cast<float4*>(out + j) = x;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (rel + i < seen) out[j + i] = in[j + i] + v[i];
-    }
+    for (int i = 0; i < 4; ++i)
+      if (rel + i < seen) out[j + i] = in[j + i] + w[i];
   }
 }
 
@@ -882,20 +819,23 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (p.whole) return cudaSuccess;
-  const int chunks = p.w_in != nullptr ? ceil_div(p.max_seqlen, kKeys) : 0;
-  const int row_blocks = runs > 0 ? static_cast<int>(runs) * p.part_rows : 1;
-  const int64_t blocks = row_blocks + static_cast<int64_t>(p.batch) * p.h_k * chunks;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchAttribute early;  // starts while the kernel before it drains, and waits for it
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(runs > 0 ? runs * p.part_rows : 1));
   cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
+  cfg.attrs = &early;
   cfg.numAttrs = runs > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), row_blocks, dp, chunks);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), dp);
+  if (e != cudaSuccess || p.w_in == nullptr || p.max_seqlen == 0) return e;
+  const int chunks = ceil_div(p.max_seqlen, kKeys);
+  const int64_t blocks = static_cast<int64_t>(p.batch) * p.h_k * chunks;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_kernel, p, chunks);
 }
 
 }  // namespace
