@@ -85,6 +85,7 @@ struct DecodeParams {
   FastDiv chunks;       // 16-byte chunks of a row
   unsigned int* status;
   int whole;            // one block a segment, nothing to join
+  int tile_log2;        // keys of a tile
 };
 
 struct EvictParams {

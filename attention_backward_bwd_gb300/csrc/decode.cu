@@ -6,22 +6,24 @@
 // take a few per cent of the tensor pipe at full memory speed, whatever the group, so the
 // products are kept small and synchronous and the design goes into the loads.
 //
-// Split.  Keys come in tiles of 64.  All tiles of all (sequence, head) segments form one
-// line, cut into equal runs, one per resident block: ragged lengths balance by themselves,
-// and one long sequence uses every SM.  A segment that lies inside one run is finished
-// there; one that is cut leaves (O, maximum, sum) partials which a second small kernel
-// joins (it is launched early and waits for the first).  The cut depends on the lengths
-// alone, so results do not depend on timing.  (More and shorter runs, taken over by blocks
-// as they finish, were slower: 425 us with one run a block, 428 with two, 432 with four for
-// 64 sequences of 4096 to 16384 keys.)  Where every segment has at most kWholeTiles tiles
-// a block takes one segment and nothing is joined.
+// Split.  Keys come in tiles of about 32 KB (128 keys of 64 columns, 64 of 128, 32 above).
+// All tiles of all (sequence, head) segments form one line, cut into equal runs, one per
+// resident block: ragged lengths balance by themselves, and one long sequence uses every
+// SM.  A segment that lies inside one run is finished there; one that is cut leaves
+// (O, maximum, sum) partials which a second small kernel joins (it is launched early and
+// waits for the first).  The cut depends on the lengths alone, so results do not depend
+// on timing.  (More and shorter runs, taken over by blocks as they finish, were slower:
+// 425 us with one run a block, 428 with two, 432 with four for 64 sequences of 4096 to
+// 16384 keys.)  Where no sequence passes kWholeKeys a block takes one segment and nothing
+// is joined.
 //
 // Block.  Two warps look the pages up and keep a ring of shared-memory stages filled with
-// 16-byte asynchronous copies, several tiles ahead; eight warps compute.  The 16-byte chunks of
-// row r lie permuted by r % 8 inside each 128 bytes, so that neither the copies nor
-// ldmatrix meet a bank conflict (with padded rows the copies alone were 4 % slower).  Of a tile each compute warp takes
-// the logits of 8 keys; the warps share the running maximum and P through shared memory;
-// then each takes an eighth of the columns of O over all 64 keys, so they never join O.
+// 16-byte asynchronous copies, several tiles ahead; eight warps compute; two blocks share
+// an SM.  The 16-byte chunks of row r lie permuted by r % 8 inside each 128 bytes, so that
+// neither the copies nor ldmatrix meet a bank conflict (with padded rows the copies alone
+// were 4 % slower).  Of a tile the compute warps first take the logits of 8 keys each (16
+// of 128; of 32 keys, 8 keys over half of the columns), then the softmax of two rows each,
+// a lane a key, then an eighth of the columns of O over all keys, so they never join O.
 // (With four warps that also did the copies, the chain of dependent steps of a tile took
 // 3100 cycles against 2600 for its loads.)
 //
@@ -36,41 +38,40 @@ namespace attn {
 
 namespace {
 
-constexpr int kTile = 64;       // keys of a tile
 constexpr int kWarps = 8;       // compute warps
 constexpr int kCompute = kWarps * 32;
-constexpr int kCopy = 64;       // copying threads, one for each key of a tile
+constexpr int kCopy = 64;       // copying threads
 constexpr int kThreads = kCompute + kCopy;
 constexpr int kJoin = 128;      // threads of a join block
 constexpr int kMaxRows = 16;    // query heads of a block
 constexpr int kLens = 256;      // lengths kept in shared memory
-constexpr int kPPitch = 144;    // bytes of a P row (64 keys and 16 bytes)
-
+constexpr int kBlocks = 2;      // of an SM
 // Runs at most: sizes the partials without asking a device.
 constexpr int kMaxRuns = 320;
+// Up to this length sequences are taken whole (6.2 us against 8.2 for one of 128 keys).
+constexpr int kWholeKeys = 256;
 
-// Segments of at most this many tiles are taken whole: one launch instead of two (6.2 us
-// against 8.2 for one sequence of 128 keys).
-constexpr int kWholeTiles = 4;
+constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp == 128 ? 6 : 5); }
 
-// Stages: what fits twice on an SM up to 128 columns, once above (two blocks keep the
-// loads going while one of them synchronises; wider rows have fewer, larger tiles).
 template <int DP>
 struct Cfg {
+  static constexpr int kTile = 1 << tile_log2(DP);       // keys of a tile
   static constexpr int kPitch = DP * 2;
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = DP == 64 ? 6 : (DP == 128 ? 3 : (DP == 192 ? 4 : 3));
-  static constexpr int kBlocks = DP <= 128 ? 2 : 1;
-  static constexpr int kSlots = kStages + 2;
-  static constexpr int kSmem = kStages * kStageBytes + kSlots * (kTile * 16 + 32) +
-                               kMaxRows * kPPitch + 2 * kWarps * kMaxRows * 4 + kLens * 4;
+  static constexpr int kStages = DP == 192 ? 4 : 3;      // 96 KB
+  static constexpr int kSlots = kStages + 2;             // descriptors
+  static constexpr int kPlan = kTile > kCopy ? kTile / kCopy : 1;  // keys a copying thread looks up
+  static constexpr int kSplits = kTile == 32 ? 2 : 1;    // warps that share a key's logits
+  static constexpr int kSPitch = kTile * 4 + 16;         // bytes of a row of logits, then of P
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kTile * 16 + kSlots * 48 +
+                               kSplits * kMaxRows * kSPitch + kLens * 4;
 };
 
 struct __align__(16) TileDesc {
   int b, hv, rel;  // sequence, head tile, first key of the tile (from the first seen)
   int flags;
-  uint32_t valid[2];  // bit per key of the tile
-  int pad[2];
+  uint32_t valid[4];  // bit per key of the tile
+  int pad[4];
 };
 enum { kBegin = 1, kEnd = 2, kFull = 4, kSecond = 8, kNone = 16 };
 
@@ -84,7 +85,7 @@ __device__ __forceinline__ int clean_len(const DecodeParams& p, int n, bool tell
   return 0;
 }
 __device__ __forceinline__ int tiles_of(const DecodeParams& p, int n) {
-  return (n - first_key(p, n) + kTile - 1) / kTile;
+  return (n - first_key(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
 }
 
 // Where the line of tiles is cut.  Run i of `runs` is [i * total / runs, (i + 1) * total / runs).
@@ -196,13 +197,16 @@ template <int DP, bool EXACT>
 __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
                                           int idx, const DecodeParams& p, uint64_t policy) {
   constexpr int kLanes = DP == 64 ? 8 : (DP == 128 ? 16 : 32), kStep = kCopy / kLanes;
-  constexpr int kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
+  constexpr int kTile = Cfg<DP>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
   const int c = idx % kLanes, r0 = idx / kLanes;
   if (c >= (EXACT ? DP / 8 : static_cast<int>(p.chunks.d))) return;
   rows += r0;
   dst += r0 * kPitch + ((c ^ r0) << 4);  // r0 < kStep, and kStep divides 8
   auto at = [&](int i) { return (dst ^ (((i * kStep) & 7) << 4)) + i * kStep * kPitch; };
-  if ((valid[0] & valid[1]) == 0xffffffffu) {
+  uint32_t all = valid[0];
+#pragma unroll
+  for (int i = 1; i < kTile / 32; ++i) all &= valid[i];
+  if (all == 0xffffffffu) {
     static_assert(kIter % 8 == 0, "groups of eight rows");
 #pragma unroll
     for (int i0 = 0; i0 < kIter; i0 += 8) {
@@ -264,23 +268,24 @@ __device__ __forceinline__ void compute_barrier() {
 }
 
 template <typename T, int DP, bool EXACT>
-__global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
+__global__ void __launch_bounds__(kThreads, kBlocks)
     decode_kernel(DecodeParams p) {
   using C = Cfg<DP>;
-  constexpr int S = C::kStages, kPitch = C::kPitch, kSlots = C::kSlots;
-  constexpr int kSteps = DP / 16;       // k-steps of Q K^T
+  constexpr int S = C::kStages, kPitch = C::kPitch, kSlots = C::kSlots, kTile = C::kTile;
+  constexpr int kSteps = DP / 16 / C::kSplits;  // k-steps of Q K^T of a warp
+  constexpr int kGroups = kTile == 128 ? 2 : 1; // groups of 8 keys of a warp
+  constexpr int kPer = kTile / 32;      // keys of a lane in the softmax
   constexpr int kCols = DP / kWarps;    // columns of O of a warp
   constexpr int kNt = kCols / 8;        // their n-tiles
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_sums[kThreads / 32];
   __shared__ int s_pre[kThreads];
+  __shared__ float s_scale[kMaxRows], s_max[kMaxRows], s_sum[kMaxRows];
   unsigned char* ring = smem;
-  longlong2* rows = reinterpret_cast<longlong2*>(ring + S * C::kStageBytes);
-  TileDesc* desc = reinterpret_cast<TileDesc*>(rows + kSlots * kTile);
-  unsigned char* pbuf = reinterpret_cast<unsigned char*>(desc + kSlots);
-  float* smax = reinterpret_cast<float*>(pbuf + kMaxRows * kPPitch);  // [row][warp]
-  float* ssum = smax + kWarps * kMaxRows;
-  int* lens = reinterpret_cast<int*>(ssum + kWarps * kMaxRows);
+  longlong2* rows = reinterpret_cast<longlong2*>(ring + S * C::kStageBytes);  // of two tiles
+  TileDesc* desc = reinterpret_cast<TileDesc*>(rows + 2 * kTile);
+  unsigned char* sbuf = reinterpret_cast<unsigned char*>(desc + kSlots);      // logits, then P
+  int* lens = reinterpret_cast<int*>(sbuf + C::kSplits * kMaxRows * C::kSPitch);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
@@ -361,24 +366,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     const uint32_t kp = static_cast<uint32_t>(p.cache.k.sb / 8), ks = static_cast<uint32_t>(p.cache.k.ss / 8);
     const uint32_t vp = static_cast<uint32_t>(p.cache.v.sb / 8), vs = static_cast<uint32_t>(p.cache.v.ss / 8);
     // what plan() saw, for store_plan()
-    int pend_page = -1, pend_within = 0;
+    int pend_page[C::kPlan], pend_within[C::kPlan];
+    bool pend_live[C::kPlan];
     const char *pend_k = nullptr, *pend_v = nullptr;
-    bool pend_live = false;
     int4 pend = make_int4(0, 0, 0, 0);
     auto plan = [&]() {  // looks one tile up and moves on
+#pragma unroll
+      for (int i = 0; i < C::kPlan; ++i) pend_live[i] = false;
       if (left == 0) {
         pend.w = kNone;
-        pend_live = false;
         return;
       }
-      const int j = cfirst + ct * kTile + key;
-      pend_live = j < cn;
       pend_k = khead;
       pend_v = vhead;
-      if (pend_live) {
-        const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
-        pend_within = j - n * static_cast<int>(p.cache.page.d);
-        pend_page = table[n];
+#pragma unroll
+      for (int i = 0; i < C::kPlan; ++i) {
+        const int k = key + i * kCopy, j = cfirst + ct * kTile + k;
+        pend_live[i] = j < cn && k < kTile;
+        if (pend_live[i]) {
+          const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
+          pend_within[i] = j - n * static_cast<int>(p.cache.page.d);
+          pend_page[i] = table[n];
+        }
       }
       const bool at_end = ct == cnt - 1;
       pend = make_int4(cb, ch, ct * kTile,
@@ -404,48 +413,54 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
       }
       load_head();
     };
-    auto store_plan = [&](int slot) {
-      bool ok = pend_live;
-      if (ok && static_cast<unsigned>(pend_page) >= static_cast<unsigned>(p.cache.num_pages)) {
-        report(p.status, kBadPage);
-        ok = false;
-      }
-      longlong2 o = make_longlong2(0, 0);  // addresses of the key's row of k and of v
-      if (ok) {
-        const uint32_t page = static_cast<uint32_t>(pend_page), in = static_cast<uint32_t>(pend_within);
-        o.x = reinterpret_cast<long long>(
-            pend_k + ((static_cast<uint64_t>(page) * kp + static_cast<uint64_t>(in) * ks) << 4));
-        o.y = reinterpret_cast<long long>(
-            pend_v + ((static_cast<uint64_t>(page) * vp + static_cast<uint64_t>(in) * vs) << 4));
-      }
-      rows[slot * kTile + key] = o;
-      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) desc[slot].valid[key >> 5] = bits;
-      if (key == 0) *reinterpret_cast<int4*>(&desc[slot]) = pend;
-    };
     // Keys and values are read once, unless a group has several head tiles: they leave the
     // L2 first, so that logits and partials stay for the second kernel.
     const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-    for (int t = 0; t < S; ++t) {
-      plan();
+    auto store_plan = [&](int tile) {
+      TileDesc& d = desc[tile % kSlots];
+#pragma unroll
+      for (int i = 0; i < C::kPlan; ++i) {
+        bool ok = pend_live[i];
+        if (ok && static_cast<unsigned>(pend_page[i]) >= static_cast<unsigned>(p.cache.num_pages)) {
+          report(p.status, kBadPage);
+          ok = false;
+        }
+        longlong2 o = make_longlong2(0, 0);  // addresses of the key's row of k and of v
+        if (ok) {
+          const uint64_t page = static_cast<uint32_t>(pend_page[i]), in = static_cast<uint32_t>(pend_within[i]);
+          o.x = reinterpret_cast<long long>(pend_k + ((page * kp + in * ks) << 4));
+          o.y = reinterpret_cast<long long>(pend_v + ((page * vp + in * vs) << 4));
+        }
+        const int k = key + i * kCopy;
+        if (k < kTile) rows[(tile & 1) * kTile + k] = o;
+        const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0 && k < kTile) d.valid[k >> 5] = bits;
+      }
+      if (key == 0) *reinterpret_cast<int4*>(&d) = pend;
+    };
+    auto fetch = [&](int tile) {  // issues the copies of one tile, if there is one
+      const TileDesc& d = desc[tile % kSlots];
+      if (!(d.flags & kNone))
+        copy_rows<DP, EXACT>(rows + (tile & 1) * kTile, d.valid, ring_u + (tile % S) * C::kStageBytes, key, p,
+                             policy);
+      cp_commit();
+    };
+    // the first copies leave as soon as their rows are known
+    plan();
+    for (int t = 0; t < S - 1; ++t) {
       store_plan(t);
+      plan();
+      asm volatile("bar.sync 1, %0;" ::"n"(kCopy) : "memory");  // rows and descriptor of tile t
+      fetch(t);
     }
+    store_plan(S - 1);
     plan();  // tile S waits in the registers
     __syncthreads();
-    for (int t = 0; t < S - 1; ++t) {
-      if (!(desc[t].flags & kNone))
-        copy_rows<DP, EXACT>(rows + t * kTile, desc[t].valid, ring_u + t * C::kStageBytes, key, p, policy);
-      cp_commit();
-    }
     for (int t = 0; !(desc[t % kSlots].flags & kNone); ++t) {
       cp_wait<S - 2>();
       __syncthreads();  // tile t is there for all; the stage of tile t - 1 is free
-      const int next = t + S - 1, slot = next % kSlots;
-      if (!(desc[slot].flags & kNone))
-        copy_rows<DP, EXACT>(rows + slot * kTile, desc[slot].valid,
-                                          ring_u + (next % S) * C::kStageBytes, key, p, policy);
-      cp_commit();
-      store_plan((t + S) % kSlots);
+      fetch(t + S - 1);
+      store_plan(t + S);
       plan();
     }
     cp_wait<0>();
@@ -455,21 +470,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
   // ==================================================== attention
   uint32_t qf[kSteps][4];
   float o[kNt][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // softmax of rows `warp` and `warp` + 8
   const int row0 = lane >> 2, col2 = (lane & 3) * 2;
+  const int group8 = C::kSplits == 2 ? warp & 3 : warp, split = C::kSplits == 2 ? warp >> 2 : 0;
+  int b = 0, h0 = 0, hn = 0;  // of the segment: sequence, first query head and their number
   __syncthreads();
   for (int t = 0;; ++t) {
     const TileDesc& d = desc[t % kSlots];
     if (d.flags & kNone) break;
     if (d.flags & kBegin) {
       const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
-      const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
-      const T* q = static_cast<const T*>(p.q.ptr) + d.b * p.q.sb;
+      b = d.b;
+      h0 = g * p.group + ht * kMaxRows;
+      hn = min(kMaxRows, p.group - ht * kMaxRows);
+      const T* q = static_cast<const T*>(p.q.ptr) + b * p.q.sb;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = row0 + (i & 1) * 8, col = k * 16 + col2 + (i >> 1) * 8;
+          const int row = row0 + (i & 1) * 8, col = (split * kSteps + k) * 16 + col2 + (i >> 1) * 8;
           qf[k][i] = row < hn && (EXACT || col < p.head_dim)
                          ? *reinterpret_cast<const uint32_t*>(q + (h0 + row) * p.q.sh + col)
                          : 0u;
@@ -483,77 +502,79 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
     }
     __syncthreads();  // tile t is there for all
 
-    // ---- logits of this warp's 8 keys
+    // ---- products of q with this warp's keys
     const uint32_t kst = ring_u + (t % S) * C::kStageBytes;
-    float s[4];
-    {
-      float s1[4];
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      float s[4], s1[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = s1[i] = 0.f;
-      const uint32_t a = kst + (warp * 8 + (lane & 7)) * kPitch + (((lane >> 3) ^ (lane & 7)) << 4);
+      const int k0 = (group8 + gr * kWarps) * 8;
+      const uint32_t a = kst + (k0 + (lane & 7)) * kPitch;
 #pragma unroll
       for (int k = 0; k < kSteps; k += 2) {
         uint32_t kf[4];
-        ldsm4((a ^ ((k & 2) << 5)) + (k >> 2) * 128, kf);
+        ldsm4(a + (((split * kSteps * 2 + k * 2 + (lane >> 3)) ^ (lane & 7)) << 4), kf);
         mma16816<T>(s, qf[k], kf[0], kf[1]);
         mma16816<T>(s1, qf[k + 1], kf[2], kf[3]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += s1[i];
-    }
-    const uint32_t valid = d.valid[warp >> 2] >> ((warp & 3) * 8 + col2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = p.softcap > 0.f ? p.cap_out * tanh_exp(s[i] * p.cap_in) : s[i] * p.scale_log2;
-      s[i] = (valid >> (i & 1)) & 1u ? x : -INFINITY;
-    }
-    if (p.logits != nullptr) {
-      const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
-      const int hn = min(kMaxRows, p.group - ht * kMaxRows);
-      const int64_t h0 = static_cast<int64_t>(d.b) * p.h_q + g * p.group + ht * kMaxRows;
-#pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (row0 + r * 8 < hn)
-          *reinterpret_cast<float2*>(p.logits + (h0 + row0 + r * 8) * p.logit_stride + d.rel + warp * 8 +
-                                     col2) = make_float2(s[r * 2], s[r * 2 + 1]);
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = fmaxf(s[r * 2], s[r * 2 + 1]);
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if ((lane & 3) == 0) smax[(row0 + r * 8) * kWarps + warp] = top;
+        *reinterpret_cast<float2*>(sbuf + (split * kMaxRows + row0 + r * 8) * C::kSPitch + (k0 + col2) * 4) =
+            make_float2(s[r * 2] + s1[r * 2], s[r * 2 + 1] + s1[r * 2 + 1]);
     }
     compute_barrier();
 
-    // ---- P under the common maximum
-    float scale_o[2];
+    // ---- softmax of this warp's rows, a lane a key; P takes the place of the logits
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float4 a = *reinterpret_cast<const float4*>(smax + (row0 + r * 8) * kWarps);
-      const float4 b = *reinterpret_cast<const float4*>(smax + (row0 + r * 8) * kWarps + 4);
-      const float mx = fmaxf(m[r], fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
-                                         fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w))));
-      const float base = mx == -INFINITY ? 0.f : mx;
-      scale_o[r] = ex2(m[r] - base);
+      const int row = warp + r * 8;
+      if (row >= hn) break;
+      float* srow = reinterpret_cast<float*>(sbuf + row * C::kSPitch);
+      float x[kPer], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        x[i] = srow[lane + 32 * i];
+        if (C::kSplits == 2)
+          x[i] += *reinterpret_cast<const float*>(sbuf + (kMaxRows + row) * C::kSPitch + (lane + 32 * i) * 4);
+        x[i] = p.softcap > 0.f ? p.cap_out * tanh_exp(x[i] * p.cap_in) : x[i] * p.scale_log2;
+        if (!((d.valid[i] >> lane) & 1u)) x[i] = -INFINITY;
+        top = fmaxf(top, x[i]);
+      }
+      if (p.logits != nullptr) {
+        float* out = p.logits + (static_cast<int64_t>(b) * p.h_q + h0 + row) * p.logit_stride + d.rel + lane;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) out[32 * i] = x[i];
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      const float mx = fmaxf(m[r], top), base = mx == -INFINITY ? 0.f : mx;
+      const float scale = ex2(m[r] - base);
+      float sum = 0.f;
+      T* prow = reinterpret_cast<T*>(srow);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float e = ex2(x[i] - base);
+        sum += e;
+        prow[lane + 32 * i] = static_cast<T>(e);
+      }
       m[r] = mx;
-      const float p0 = ex2(s[r * 2] - base), p1 = ex2(s[r * 2 + 1] - base);
-      *reinterpret_cast<uint32_t*>(pbuf + (row0 + r * 8) * kPPitch + (warp * 8 + col2) * 2) =
-          Pack<T>::two(p0, p1);
-      l[r] = l[r] * scale_o[r] + (p0 + p1);
+      l[r] = l[r] * scale + sum;
+      if (lane == 0) s_scale[row] = scale;
     }
     compute_barrier();
 
     // ---- O += P V for this warp's columns
-#pragma unroll
-    for (int n = 0; n < kNt; ++n) {
-      o[n][0] *= scale_o[0];
-      o[n][1] *= scale_o[0];
-      o[n][2] *= scale_o[1];
-      o[n][3] *= scale_o[1];
-    }
     {
-      const uint32_t pa = smem_u32(pbuf) + (lane & 15) * kPPitch + (lane >> 4) * 16;
+      const float c0 = s_scale[row0], c1 = s_scale[row0 + 8];
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) {
+        o[n][0] *= c0;
+        o[n][1] *= c0;
+        o[n][2] *= c1;
+        o[n][3] *= c1;
+      }
+      const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16;
       const uint32_t va = kst + (kTile + lane) * kPitch;
 #pragma unroll
       for (int k = 0; k < kTile / 32; ++k) {
@@ -575,26 +596,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float x = l[r];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if ((lane & 3) == 0) ssum[(row0 + r * 8) * kWarps + warp] = x;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+        if (lane == 0) {
+          s_sum[warp + r * 8] = x;
+          s_max[warp + r * 8] = m[r];
+        }
       }
       compute_barrier();
-      const int g = d.hv / p.head_tiles, ht = d.hv - g * p.head_tiles;
-      const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
       const bool whole = (d.flags & kFull) != 0;
       float* part = partial(p, blockIdx.x, (d.flags & kSecond) ? 1 : 0);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = row0 + r * 8;
         if (row >= hn) continue;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += ssum[row * kWarps + w];
+        const float sum = s_sum[row];
         const bool none = sum == 0.f;
         const float inv = none ? 0.f : 1.f / sum;
         if (whole) {
-          T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + d.b * p.o.sb + (h0 + row) * p.o.sh;
+          T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + (h0 + row) * p.o.sh;
 #pragma unroll
           for (int n = 0; n < kNt; ++n) {
             const int col = warp * kCols + n * 8 + col2;
@@ -603,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
                   Pack<T>::two(none ? 0.f : o[n][r * 2] * inv, none ? 0.f : o[n][r * 2 + 1] * inv);
           }
           if (warp == 0 && (lane & 3) == 0) {
-            const float lse2 = none ? INFINITY : m[r] + log2f(sum);
-            const int64_t at = static_cast<int64_t>(d.b) * p.h_q + h0 + row;
+            const float lse2 = none ? INFINITY : s_max[row] + log2f(sum);
+            const int64_t at = static_cast<int64_t>(b) * p.h_q + h0 + row;
             if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
             if (p.lse2 != nullptr) p.lse2[at] = lse2;
           }
@@ -614,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kBlocks)
             *reinterpret_cast<float2*>(part + row * DP + warp * kCols + n * 8 + col2) =
                 make_float2(o[n][r * 2], o[n][r * 2 + 1]);
           if (warp == 0 && (lane & 3) == 0) {
-            part[p.part_rows * DP + row] = m[r];
+            part[p.part_rows * DP + row] = s_max[row];
             part[p.part_rows * DP + kMaxRows + row] = sum;
           }
         }
@@ -800,12 +820,14 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   p.part_rows = p.group < kMaxRows ? p.group : kMaxRows;
   p.part_stride = static_cast<int64_t>(p.part_rows) * dp + 2 * kMaxRows;
   p.chunks.set(static_cast<uint32_t>(p.head_dim / 8));
-  const int64_t most = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles * ceil_div(p.max_seqlen, kTile);
-  if (static_cast<int64_t>(p.batch) * ceil_div(p.max_seqlen, kTile) > INT32_MAX) return cudaErrorInvalidValue;
-  int64_t runs = static_cast<int64_t>(num_sms()) * (dp <= 128 ? 2 : 1);
+  p.tile_log2 = tile_log2(dp);
+  const int most_tiles = ceil_div(p.max_seqlen, 1 << p.tile_log2);
+  if (static_cast<int64_t>(p.batch) * most_tiles > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t most = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles * most_tiles;
+  int64_t runs = static_cast<int64_t>(num_sms()) * kBlocks;
   if (runs > kMaxRuns) runs = kMaxRuns;
   if (runs > most) runs = most;
-  p.whole = p.w_in == nullptr && p.max_seqlen <= kWholeTiles * kTile && runs > 0;
+  p.whole = p.w_in == nullptr && p.max_seqlen <= kWholeKeys && runs > 0;
   if (p.whole) runs = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles;
   if (runs > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
@@ -842,10 +864,10 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
 
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights) {
   DecodeWs w = {};
-  if (!weights && max_seqlen <= kWholeTiles * kTile) return w;  // nothing is joined
+  if (!weights && max_seqlen <= kWholeKeys) return w;  // nothing is joined
   const size_t rows = static_cast<size_t>(batch) * h_q;
   const int group = h_q / h_k, part_rows = group < kMaxRows ? group : kMaxRows;
-  w.logit_stride = round_up(max_seqlen, kTile);
+  w.logit_stride = round_up(max_seqlen, 1 << tile_log2(64));  // whole tiles of any width
   w.off_lse2 = 0;  // with weights only
   w.off_parts = weights ? align256(rows * 4) : 0;
   w.off_logits = w.off_parts + align256(static_cast<size_t>(kMaxRuns) * 2 *
