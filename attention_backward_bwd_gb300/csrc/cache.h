@@ -82,7 +82,8 @@ struct DecodeParams {
   int64_t part_stride;  // floats of a partial
   int part_rows;        // its rows of O (maxima and sums follow them)
   int head_tiles;       // 16-row tiles of a group
-  FastDiv chunks;       // 16-byte chunks of a row
+  int chunks;           // 16-byte chunks of a row
+  int lines;            // lines of tiles: one, or one a head tile
   unsigned int* status;
   int whole;            // one block a segment, nothing to join
   int tile_log2;        // keys of a tile

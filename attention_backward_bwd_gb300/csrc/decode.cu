@@ -9,7 +9,11 @@
 // Split.  Keys come in tiles of about 32 KB (128 keys of 64 columns, 64 of 128, 32 above).
 // All tiles of all (sequence, head) segments form one line, cut into equal runs, one per
 // resident block: ragged lengths balance by themselves, and one long sequence uses every
-// SM.  A segment that lies inside one run is finished there; one that is cut leaves
+// SM.  Where the blocks divide among the heads, every head has a line of its own instead,
+// all cut alike, and neighbouring blocks walk the same keys of different heads in step: a
+// token's heads lie side by side in memory, and rows that are not whole 128-byte lines
+// would otherwise be fetched again for the next head (heads of 112, 32 sequences up to
+// 8192 keys: 630 MB read for 491, 105 us; in step 86 us).  A segment that lies inside one run is finished there; one that is cut leaves
 // (O, maximum, sum) partials which a second small kernel joins (it is launched early and
 // waits for the first).  The cut depends on the lengths alone, so results do not depend
 // on timing.  (More and shorter runs, taken over by blocks as they finish, were slower:
@@ -88,7 +92,7 @@ __device__ __forceinline__ int tiles_of(const DecodeParams& p, int n) {
   return (n - first_key(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
 }
 
-// Where the line of tiles is cut.  Run i of `runs` is [i * total / runs, (i + 1) * total / runs).
+// Where a line of tiles is cut.  Run i of `runs` is [i * total / runs, (i + 1) * total / runs).
 struct Cut {
   long long total;
   int runs;
@@ -184,22 +188,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Partial of run c (its first or second cut segment): rows of O, then maxima and sums.
-__device__ __forceinline__ float* partial(const DecodeParams& p, int c, int second) {
-  return p.parts + (static_cast<int64_t>(c) * 2 + second) * p.part_stride;
+// Partial of a block (of its run's first or second cut segment): rows of O, then maxima
+// and sums.
+__device__ __forceinline__ float* partial(const DecodeParams& p, int block, int second) {
+  return p.parts + (static_cast<int64_t>(block) * 2 + second) * p.part_stride;
 }
 
 // Copies the rows of a tile, kLanes of the copying threads to a row.  `rows`: the addresses
 // of each key's rows of k and of v.
 // Addresses are read eight at a time before their copies are issued: a copy writes shared
 // memory, so a read behind it in program order waits until it has been issued.
-template <int DP, bool EXACT>
+template <int DP>
 __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
                                           int idx, const DecodeParams& p, uint64_t policy) {
   constexpr int kLanes = DP == 64 ? 8 : (DP == 128 ? 16 : 32), kStep = kCopy / kLanes;
   constexpr int kTile = Cfg<DP>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
   const int c = idx % kLanes, r0 = idx / kLanes;
-  if (c >= (EXACT ? DP / 8 : static_cast<int>(p.chunks.d))) return;
+  if (c >= p.chunks) return;
   rows += r0;
   dst += r0 * kPitch + ((c ^ r0) << 4);  // r0 < kStep, and kStep divides 8
   auto at = [&](int i) { return (dst ^ (((i * kStep) & 7) << 4)) + i * kStep * kPitch; };
@@ -267,7 +272,7 @@ __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 2, %0;" ::"n"(kCompute) : "memory");
 }
 
-template <typename T, int DP, bool EXACT>
+template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     decode_kernel(DecodeParams p) {
   using C = Cfg<DP>;
@@ -289,6 +294,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
+  // lines: one of all heads, or one of each; this block's line and its run of it
+  const int line_heads = p.lines > 1 ? 1 : hv_n;
+  const int run = blockIdx.x / p.lines, line = blockIdx.x - run * p.lines;
   const uint32_t ring_u = smem_u32(ring);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -305,12 +313,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   } else {
     int total;
     s_pre[tid] = scan_tiles<kThreads>(p, true, lens, s_sums, per, total);
-    cut.total = static_cast<long long>(total) * hv_n;
-    cut.runs = static_cast<int>(min(static_cast<long long>(gridDim.x), cut.total));
-    if (static_cast<int>(blockIdx.x) >= cut.runs) return;
+    cut.total = static_cast<long long>(total) * line_heads;
+    cut.runs = static_cast<int>(min(static_cast<long long>(gridDim.x / p.lines), cut.total));
+    if (run >= cut.runs) return;
   }
   // columns that no copy writes stay zero
-  if (!EXACT) {
+  if (p.head_dim < DP) {
     const int c0 = p.head_dim / 8, nc = DP / 8 - c0;
     for (int i = tid; i < S * 2 * kTile * nc; i += kThreads)
       *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ ((i / nc) & 7)) << 4)) = make_uint4(0, 0, 0, 0);
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       table = p.cache.table + cb * p.cache.table_stride;
     };
     auto load_head = [&]() {
-      const int g = ch / p.head_tiles, ht = ch - g * p.head_tiles;
+      const int hv = line + ch, g = hv / p.head_tiles, ht = hv - g * p.head_tiles;
       khead = reinterpret_cast<const char*>(static_cast<const T*>(p.cache.k.ptr) + g * p.cache.k.sh);
       vhead = reinterpret_cast<const char*>(static_cast<const T*>(p.cache.v.ptr) + g * p.cache.v.sh);
       // its queries are asked for a few tiles ahead
@@ -347,16 +355,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     auto len_of = [&](int b) { return b < kLens ? lens[b] : clean_len(p, p.seqlens[b], false); };
     if (p.whole) {
       cb = blockIdx.x / hv_n;
-      ch = blockIdx.x - cb * hv_n;
+      ch = blockIdx.x - cb * hv_n;  // one line
       load_seq(lens[0]);
       left = cnt;
     } else {
-      const long long r0 = cut.start(blockIdx.x);
-      left = static_cast<int>(cut.start(blockIdx.x + 1) - r0);
+      const long long r0 = cut.start(run);
+      left = static_cast<int>(cut.start(run + 1) - r0);
       int before;
-      cb = find_sequence<kThreads>(p, s_pre, per, hv_n, r0, len_of, before);
+      cb = find_sequence<kThreads>(p, s_pre, per, line_heads, r0, len_of, before);
       load_seq(len_of(cb));
-      const long long in = r0 - static_cast<long long>(before) * hv_n;
+      const long long in = r0 - static_cast<long long>(before) * line_heads;
       ch = static_cast<int>(in / cnt);
       ct = static_cast<int>(in - static_cast<long long>(ch) * cnt);
       seg_from_start = ct == 0;
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         }
       }
       const bool at_end = ct == cnt - 1;
-      pend = make_int4(cb, ch, ct * kTile,
+      pend = make_int4(cb, line + ch, ct * kTile,
                        (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) |
                            (at_end && seg_from_start ? kFull : 0) | (nth ? kSecond : 0));
       begin = 0;
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       begin = 1;
       nth = 1;
       seg_from_start = true;
-      if (++ch == hv_n) {
+      if (++ch == line_heads) {
         ch = 0;
         do {
           ++cb;
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     auto fetch = [&](int tile) {  // issues the copies of one tile, if there is one
       const TileDesc& d = desc[tile % kSlots];
       if (!(d.flags & kNone))
-        copy_rows<DP, EXACT>(rows + (tile & 1) * kTile, d.valid, ring_u + (tile % S) * C::kStageBytes, key, p,
+        copy_rows<DP>(rows + (tile & 1) * kTile, d.valid, ring_u + (tile % S) * C::kStageBytes, key, p,
                              policy);
       cp_commit();
     };
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = row0 + (i & 1) * 8, col = (split * kSteps + k) * 16 + col2 + (i >> 1) * 8;
-          qf[k][i] = row < hn && (EXACT || col < p.head_dim)
+          qf[k][i] = row < hn && col < p.head_dim
                          ? *reinterpret_cast<const uint32_t*>(q + (h0 + row) * p.q.sh + col)
                          : 0u;
         }
@@ -618,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
           for (int n = 0; n < kNt; ++n) {
             const int col = warp * kCols + n * 8 + col2;
-            if (EXACT || col < p.head_dim)
+            if (col < p.head_dim)
               *reinterpret_cast<uint32_t*>(out + col) =
                   Pack<T>::two(none ? 0.f : o[n][r * 2] * inv, none ? 0.f : o[n][r * 2 + 1] * inv);
           }
@@ -644,9 +652,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 }
 
 // Joins the partials of cut segments and writes the rows of empty sequences: a block takes
-// one row of the segment that starts in its run and is cut at its end, if there is one.
+// one row of the segment that starts in the run of a block of the first kernel (of which
+// there were `blocks`) and is cut at its end, if there is one.
 template <typename T>
-__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, int dp) {
+__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks, int dp) {
   __shared__ int s_sums[kJoin / 32];
   __shared__ int s_pre[kJoin];
   __shared__ float4 s_part[kJoin];
@@ -661,24 +670,27 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, i
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-    if (clean_len(p, p.seqlens[b], runs == 0) == 0)
+    if (clean_len(p, p.seqlens[b], blocks == 0) == 0)
       for (int hv = 0; hv < hv_n; ++hv) no_keys<T>(p, b, hv);
   int total;
   s_pre[tid] = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
-  cut.total = static_cast<long long>(total) * hv_n;
-  cut.runs = static_cast<int>(min(static_cast<long long>(runs), cut.total));
+  const int line_heads = p.lines > 1 ? 1 : hv_n;
+  cut.total = static_cast<long long>(total) * line_heads;
+  cut.runs = static_cast<int>(min(static_cast<long long>(blocks / p.lines), cut.total));
   __syncthreads();
-  const int run = blockIdx.x / p.part_rows, row = blockIdx.x - run * p.part_rows;
+  const int block = blockIdx.x / p.part_rows, row = blockIdx.x - block * p.part_rows;
+  const int run = block / p.lines, line = block - run * p.lines;
   bool mine = run + 1 < cut.runs;  // a run with an end inside the line
   int b = 0, hv = 0, nc = 0, lead = 0;
   if (mine) {
     const long long r0 = cut.start(run), e = cut.start(run + 1);
     int before;
-    b = find_sequence<kJoin>(p, s_pre, per, hv_n, e - 1, len_of, before);
+    b = find_sequence<kJoin>(p, s_pre, per, line_heads, e - 1, len_of, before);
     const int t_b = tiles_of(p, len_of(b));
-    const long long line0 = static_cast<long long>(before) * hv_n;
-    hv = static_cast<int>((e - 1 - line0) / t_b);
-    const long long s0 = line0 + static_cast<long long>(hv) * t_b;
+    const long long line0 = static_cast<long long>(before) * line_heads;
+    const int ch = static_cast<int>((e - 1 - line0) / t_b);
+    const long long s0 = line0 + static_cast<long long>(ch) * t_b;
+    hv = line + ch;
     mine = s0 >= r0 && s0 + t_b > e &&
            row < p.group - (hv % p.head_tiles) * kMaxRows;  // starts here, goes on, has this row
     if (mine) {
@@ -691,7 +703,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, i
   const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
   float top = -INFINITY, sum = 0.f;
   for (int i = tid; i < nc; i += kJoin) {
-    const float x = partial(p, run + i, i == 0 ? lead : 0)[part_m + row];
+    const float x = partial(p, block + i * p.lines, i == 0 ? lead : 0)[part_m + row];
     s_w[i] = x;
     top = fmaxf(top, x);
   }
@@ -710,7 +722,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int runs, i
   if (st < stripes) {
 #pragma unroll 4
     for (int i = st; i < nc; i += stripes) {
-      const float* part = partial(p, run + i, i == 0 ? lead : 0);
+      const float* part = partial(p, block + i * p.lines, i == 0 ? lead : 0);
       const float w = ex2(s_w[i] - base);
       const float4 x = *reinterpret_cast<const float4*>(part + row * dp + cg * 4);
       sum += w * part[part_m + kMaxRows + row];
@@ -796,7 +808,7 @@ __global__ void __launch_bounds__(kJoin) weights_kernel(DecodeParams p, int chun
 
 int pad_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
 
-template <typename T, int DP, bool EXACT>
+template <typename T, int DP>
 cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};  // devices with the attribute set
   int dev = 0;
@@ -804,12 +816,12 @@ cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(done.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(decode_kernel<T, DP, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  decode_kernel<T, DP, EXACT><<<runs, kThreads, Cfg<DP>::kSmem, stream>>>(p);
+  decode_kernel<T, DP><<<runs, kThreads, Cfg<DP>::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -819,25 +831,35 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   p.head_tiles = ceil_div(p.group, kMaxRows);
   p.part_rows = p.group < kMaxRows ? p.group : kMaxRows;
   p.part_stride = static_cast<int64_t>(p.part_rows) * dp + 2 * kMaxRows;
-  p.chunks.set(static_cast<uint32_t>(p.head_dim / 8));
+  p.chunks = p.head_dim / 8;
   p.tile_log2 = tile_log2(dp);
   const int most_tiles = ceil_div(p.max_seqlen, 1 << p.tile_log2);
   if (static_cast<int64_t>(p.batch) * most_tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t most = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles * most_tiles;
   int64_t runs = static_cast<int64_t>(num_sms()) * kBlocks;
   if (runs > kMaxRuns) runs = kMaxRuns;
-  if (runs > most) runs = most;
+  const int64_t heads = static_cast<int64_t>(p.h_k) * p.head_tiles;
+  // A line a head when that leaves at most a quarter of the blocks idle (64 heads of 64, 256
+  // of 304 blocks: 338 us against 371; 32 heads of 128, 288 blocks: 310 against 329).
+  p.lines = 1;
+  if (heads <= runs && runs % heads * 4 <= runs) {
+    p.lines = static_cast<int>(heads);
+    runs -= runs % heads;
+  }
+  if (runs > most) runs = most;  // a multiple of the heads, too
   p.whole = p.w_in == nullptr && p.max_seqlen <= kWholeKeys && runs > 0;
-  if (p.whole) runs = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles;
+  if (p.whole) {
+    runs = p.batch * heads;
+    p.lines = 1;
+  }
   if (runs > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  const bool exact = dp == p.head_dim;
   if (runs > 0) {
     const int r = static_cast<int>(runs);
-    if (dp == 64) e = exact ? launch_main<T, 64, true>(p, r, stream) : launch_main<T, 64, false>(p, r, stream);
-    else if (dp == 128) e = exact ? launch_main<T, 128, true>(p, r, stream) : launch_main<T, 128, false>(p, r, stream);
-    else if (dp == 192) e = exact ? launch_main<T, 192, true>(p, r, stream) : launch_main<T, 192, false>(p, r, stream);
-    else e = exact ? launch_main<T, 256, true>(p, r, stream) : launch_main<T, 256, false>(p, r, stream);
+    if (dp == 64) e = launch_main<T, 64>(p, r, stream);
+    else if (dp == 128) e = launch_main<T, 128>(p, r, stream);
+    else if (dp == 192) e = launch_main<T, 192>(p, r, stream);
+    else e = launch_main<T, 256>(p, r, stream);
     if (e != cudaSuccess) return e;
   }
   if (p.whole) return cudaSuccess;
