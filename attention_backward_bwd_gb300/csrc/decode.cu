@@ -52,7 +52,8 @@ constexpr int kLens = 256;      // lengths kept in shared memory
 constexpr int kBlocks = 2;      // of an SM
 // Runs at most: sizes the partials without asking a device.
 constexpr int kMaxRuns = 320;
-// Up to this length sequences are taken whole (6.2 us against 8.2 for one of 128 keys).
+// Up to this length, and while the blocks suffice, sequences are taken whole (6.2 us against
+// 8.2 for one of 128 keys; but 2048 segments of 63 to 256 keys 51.4 us against 41.2).
 constexpr int kWholeKeys = 256;
 
 constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp == 128 ? 6 : 5); }
@@ -651,22 +652,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   }
 }
 
-// Joins the partials of cut segments and writes the rows of empty sequences: a block takes
-// one row of the segment that starts in the run of a block of the first kernel (of which
-// there were `blocks`) and is cut at its end, if there is one.
+// Joins the partials of cut segments and writes the rows of empty sequences.  A block takes
+// rows_per rows of one segment, a warp a row or several that share its partials.  Where
+// there are more segments than blocks of the first kernel (`blocks`), its segment is the
+// one that starts in the run of such a block and is cut at its end, if there is one; else
+// (by_segment) it is counted off.
 template <typename T>
-__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks, int dp) {
+__global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks, int by_segment, int rows_per,
+                                                     int dp) {
   __shared__ int s_sums[kJoin / 32];
   __shared__ int s_pre[kJoin];
-  __shared__ float4 s_part[kJoin];
-  __shared__ float s_lse[kJoin];
-  __shared__ float s_w[kMaxRuns];
+  __shared__ float s_w[kJoin / 32][kMaxRuns];
+  __shared__ float4 s_part[kJoin / 32][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
   const int per = (p.batch + kJoin - 1) / kJoin;
   const int part_m = p.part_rows * dp;
   auto len_of = [&](int b) { return clean_len(p, p.seqlens[b], false); };
-  Cut cut;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
@@ -675,90 +677,129 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks,
   int total;
   s_pre[tid] = scan_tiles<kJoin>(p, false, nullptr, s_sums, per, total);
   const int line_heads = p.lines > 1 ? 1 : hv_n;
+  Cut cut;
   cut.total = static_cast<long long>(total) * line_heads;
   cut.runs = static_cast<int>(min(static_cast<long long>(blocks / p.lines), cut.total));
   __syncthreads();
-  const int block = blockIdx.x / p.part_rows, row = blockIdx.x - block * p.part_rows;
-  const int run = block / p.lines, line = block - run * p.lines;
-  bool mine = run + 1 < cut.runs;  // a run with an end inside the line
-  int b = 0, hv = 0, nc = 0, lead = 0;
-  if (mine) {
-    const long long r0 = cut.start(run), e = cut.start(run + 1);
-    int before;
-    b = find_sequence<kJoin>(p, s_pre, per, line_heads, e - 1, len_of, before);
+  const int row_blocks = (p.part_rows + rows_per - 1) / rows_per, shares = kJoin / 32 / rows_per;
+  const int at = blockIdx.x / row_blocks;
+  const int row = (blockIdx.x - at * row_blocks) * rows_per + warp / shares, share = warp % shares;
+  bool mine = false;
+  int b = 0, hv = 0, nc = 0, lead = 0, block = at;
+  if (by_segment) {
+    b = at / hv_n;
+    hv = at - b * hv_n;
     const int t_b = tiles_of(p, len_of(b));
-    const long long line0 = static_cast<long long>(before) * line_heads;
-    const int ch = static_cast<int>((e - 1 - line0) / t_b);
-    const long long s0 = line0 + static_cast<long long>(ch) * t_b;
-    hv = line + ch;
-    mine = s0 >= r0 && s0 + t_b > e &&
-           row < p.group - (hv % p.head_tiles) * kMaxRows;  // starts here, goes on, has this row
-    if (mine) {
+    if (t_b > 0) {
+      int before = s_pre[b / per];
+      for (int i = b / per * per; i < b; ++i) before += tiles_of(p, len_of(i));
+      const int line = p.lines > 1 ? hv : 0;
+      const long long s0 = static_cast<long long>(before) * line_heads +
+                           static_cast<long long>(hv - line) * t_b;
+      const int run = cut.run_of(s0);
       nc = cut.run_of(s0 + t_b - 1) - run + 1;
-      lead = r0 == s0 ? 0 : 1;  // only in its first run can the segment be the second
+      lead = cut.start(run) == s0 ? 0 : 1;
+      block = run * p.lines + line;
+      mine = nc > 1;
+    }
+  } else {
+    const int run = block / p.lines, line = block - run * p.lines;
+    if (run + 1 < cut.runs) {  // a run with an end inside the line
+      const long long r0 = cut.start(run), e = cut.start(run + 1);
+      int before;
+      b = find_sequence<kJoin>(p, s_pre, per, line_heads, e - 1, len_of, before);
+      const int t_b = tiles_of(p, len_of(b));
+      const long long line0 = static_cast<long long>(before) * line_heads;
+      const int ch = static_cast<int>((e - 1 - line0) / t_b);
+      const long long s0 = line0 + static_cast<long long>(ch) * t_b;
+      hv = line + ch;
+      mine = s0 >= r0 && s0 + t_b > e;  // starts here and goes on
+      if (mine) {
+        nc = cut.run_of(s0 + t_b - 1) - run + 1;
+        lead = r0 == s0 ? 0 : 1;  // only in its first run can the segment be the second
+      }
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine) return;
-  const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
+  const bool on = row < min(kMaxRows, p.group - (hv % p.head_tiles) * kMaxRows);
+  const int64_t stride = 2 * p.part_stride * p.lines;
+  const float* first = partial(p, block, lead);
+  const float* rest = partial(p, block, 0);
+  auto part = [&](int i) { return i == 0 ? first : rest + i * stride; };
   float top = -INFINITY, sum = 0.f;
-  for (int i = tid; i < nc; i += kJoin) {
-    const float x = partial(p, block + i * p.lines, i == 0 ? lead : 0)[part_m + row];
-    s_w[i] = x;
-    top = fmaxf(top, x);
-  }
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (on) {
+    float* w = s_w[warp];
+    for (int i = lane; i < nc; i += 32) {
+      w[i] = part(i)[part_m + row];
+      top = fmaxf(top, w[i]);
+    }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  if (lane == 0) s_lse[warp] = top;
-  __syncthreads();
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float base = top == -INFINITY ? 0.f : top;
+    for (int i = lane; i < nc; i += 32) {
+      w[i] = ex2(w[i] - base);
+      sum += w[i] * part(i)[part_m + kMaxRows + row];
+    }
 #pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_lse[w]);
-  const float base = top == -INFINITY ? 0.f : top;
-  __syncthreads();
-  // threads: 16-byte column group, and every stripe-th run
-  const int groups = dp / 4, stripes = kJoin / groups;
-  const int cg = tid % groups, st = tid / groups;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (st < stripes) {
-#pragma unroll 4
-    for (int i = st; i < nc; i += stripes) {
-      const float* part = partial(p, block + i * p.lines, i == 0 ? lead : 0);
-      const float w = ex2(s_w[i] - base);
-      const float4 x = *reinterpret_cast<const float4*>(part + row * dp + cg * 4);
-      sum += w * part[part_m + kMaxRows + row];
-      acc.x += w * x.x;
-      acc.y += w * x.y;
-      acc.z += w * x.z;
-      acc.w += w * x.w;
-    }
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (lane + 32 * c < dp / 4) {
+        const int col = row * dp + (lane + 32 * c) * 4;
+        for (int i0 = share; i0 < nc; i0 += 8 * shares) {
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i0 + k * shares < nc) x[k] = *reinterpret_cast<const float4*>(part(i0 + k * shares) + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i0 + k * shares < nc) {
+              const float f = w[i0 + k * shares];
+              acc[c].x += f * x[k].x;
+              acc[c].y += f * x[k].y;
+              acc[c].z += f * x[k].z;
+              acc[c].w += f * x[k].w;
+            }
+        }
+      }
   }
-  s_part[tid] = acc;
-  s_lse[tid] = sum;
-  __syncthreads();
-  if (st == 0) {
-    for (int i = 1; i < stripes; ++i) {
-      const float4 x = s_part[tid + i * groups];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
-      sum += s_lse[i * groups];
-    }
-    const bool none = sum == 0.f;
-    const float inv = none ? 0.f : 1.f / sum;
-    T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
-    if (cg * 4 < p.head_dim) {
-      uint2 v;
-      v.x = Pack<T>::two(none ? 0.f : acc.x * inv, none ? 0.f : acc.y * inv);
-      v.y = Pack<T>::two(none ? 0.f : acc.z * inv, none ? 0.f : acc.w * inv);
-      *reinterpret_cast<uint2*>(out + cg * 4) = v;
-    }
-    if (tid == 0) {
-      const float lse2 = none ? INFINITY : base + log2f(sum);
-      const int64_t at = static_cast<int64_t>(b) * p.h_q + h;
-      if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
-      if (p.lse2 != nullptr) p.lse2[at] = lse2;
-    }
+  if (shares > 1) {
+    s_part[warp][lane] = acc[0];
+    s_part[warp][lane + 32] = acc[1];
+    __syncthreads();
+    if (share == 0)
+      for (int i = 1; i < shares; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float4 x = s_part[warp + i][lane + 32 * c];
+          acc[c].x += x.x;
+          acc[c].y += x.y;
+          acc[c].z += x.z;
+          acc[c].w += x.w;
+        }
+  }
+  if (!on || share != 0) return;
+  const int h = (hv / p.head_tiles) * p.group + (hv % p.head_tiles) * kMaxRows + row;
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h * p.o.sh;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int col = (lane + 32 * c) * 4;
+    if (col >= p.head_dim) continue;
+    uint2 v;
+    v.x = Pack<T>::two(none ? 0.f : acc[c].x * inv, none ? 0.f : acc[c].y * inv);
+    v.y = Pack<T>::two(none ? 0.f : acc[c].z * inv, none ? 0.f : acc[c].w * inv);
+    *reinterpret_cast<uint2*>(out + col) = v;
+  }
+  if (lane == 0) {
+    const float lse2 = none ? INFINITY : (top == -INFINITY ? 0.f : top) + log2f(sum);
+    const int64_t at = static_cast<int64_t>(b) * p.h_q + h;
+    if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
+    if (p.lse2 != nullptr) p.lse2[at] = lse2;
   }
 }
 
@@ -808,6 +849,12 @@ __global__ void __launch_bounds__(kJoin) weights_kernel(DecodeParams p, int chun
 
 int pad_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
 
+// One block a segment, without partials.
+bool takes_whole(int batch, int h_k, int group, int max_seqlen, bool weights) {
+  return !weights && max_seqlen <= kWholeKeys &&
+         static_cast<int64_t>(batch) * h_k * ceil_div(group, kMaxRows) <= kMaxRuns;
+}
+
 template <typename T, int DP>
 cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};  // devices with the attribute set
@@ -847,7 +894,7 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     runs -= runs % heads;
   }
   if (runs > most) runs = most;  // a multiple of the heads, too
-  p.whole = p.w_in == nullptr && p.max_seqlen <= kWholeKeys && runs > 0;
+  p.whole = takes_whole(p.batch, p.h_k, p.group, p.max_seqlen, p.w_in != nullptr) && runs > 0;
   if (p.whole) {
     runs = p.batch * heads;
     p.lines = 1;
@@ -867,12 +914,17 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(runs > 0 ? runs * p.part_rows : 1));
+  // few segments have many partials each: then four warps share a row's
+  const int64_t segments = p.batch * heads;
+  const int by_segment = segments <= runs;
+  const int rows_per = segments * p.part_rows <= 2 * runs ? 1 : (p.part_rows > 2 ? 4 : p.part_rows);
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      runs > 0 ? (by_segment ? segments : runs) * ceil_div(p.part_rows, rows_per) : 1));
   cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = runs > 0 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), dp);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), by_segment, rows_per, dp);
   if (e != cudaSuccess || p.w_in == nullptr || p.max_seqlen == 0) return e;
   const int chunks = ceil_div(p.max_seqlen, kKeys);
   const int64_t blocks = static_cast<int64_t>(p.batch) * p.h_k * chunks;
@@ -886,7 +938,7 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
 
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights) {
   DecodeWs w = {};
-  if (!weights && max_seqlen <= kWholeKeys) return w;  // nothing is joined
+  if (takes_whole(batch, h_k, h_q / h_k, max_seqlen, weights)) return w;  // nothing is joined
   const size_t rows = static_cast<size_t>(batch) * h_q;
   const int group = h_q / h_k, part_rows = group < kMaxRows ? group : kMaxRows;
   w.logit_stride = round_up(max_seqlen, 1 << tile_log2(64));  // whole tiles of any width

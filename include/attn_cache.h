@@ -119,7 +119,7 @@ int attn_cache_append(const attn_tensor* q, const attn_tensor* oq, const attn_te
  * max_seqlen: bound on seqlens, at most max_pages * page_size.
  * workspace: at least attn_decode_workspace_size(...) bytes, 256-byte aligned,
  * not shared by calls that may overlap on the GPU.  It needs no clearing.  The size
- * is 0 (workspace may be NULL) for max_seqlen <= 256 without weights.
+ * is 0 (workspace may be NULL) for small batches with max_seqlen <= 256 without weights.
  * The result does not depend on timing: the same call gives the same bits.
  */
 size_t attn_decode_workspace_size(int batch, int h_q, int h_k, int head_dim, int max_seqlen,
