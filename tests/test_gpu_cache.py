@@ -176,6 +176,66 @@ def test_decode_matches_the_oracle(case, weights):
     check_decode(o, lse, q, kc, vc, table, lens, d ** -0.5, window, cap, w, w0)
 
 
+MANY = [
+    # batch, length of sequence i, hq, hk, D, page, window: more sequences than a block has
+    # threads or keeps lengths of, empty ones among them; and heads that do and do not divide
+    # the blocks, up to more heads than blocks
+    (700, lambda i: (i * 29) % 45 if i % 7 else 0, 4, 2, 64, 16, -1),
+    (400, lambda i: 300 + i % 3 if i % 50 == 0 else (i * 7) % 12, 6, 3, 128, 16, -1),
+    (330, lambda i: 0 if i < 300 else 260 + i, 2, 1, 64, 64, 500),
+    (2, lambda i: 700 * i + 30, 40, 40, 64, 32, -1),
+    (2, lambda i: 500 * i + 9, 70, 35, 96, 32, -1),
+    (1, lambda i: 600, 320, 320, 16, 16, -1),
+    (2, lambda i: 290 + i, 130, 65, 192, 16, -1),
+]
+
+
+@pytest.mark.parametrize("weights", [False, True], ids=["", "weights"])
+@pytest.mark.parametrize("case", MANY, ids=[f"{c[0]}seq-h{c[2]}/{c[3]}-d{c[4]}" for c in MANY])
+def test_decode_of_many_sequences_and_heads(case, weights):
+    batch, length, hq, hk, d, page, window = case
+    lens = [length(i) for i in range(batch)]
+    q, kc, vc, table = _decode_inputs(lens, hq, hk, d, page, False, torch.bfloat16)
+    w0 = torch.rand(batch, hk, max(lens), device="cuda") if weights else None
+    w = w0.clone() if weights else None
+    o, lse = ab.attn_decode(q, kc, vc, table, ints(lens), max_seqlen=max(lens),
+                            window=None if window < 0 else (window, 0), weights=w)
+    ab.check_device_status()
+    check_decode(o, lse, q, kc, vc, table, lens, d ** -0.5, window, 0.0, w, w0)
+
+
+def test_pages_behind_2_to_the_32_elements():
+    """A cache of more than 2^32 elements (10 GB, keys and values in the same pages): append,
+    decode and evict on its last pages."""
+    page, hk, d, pages = 256, 8, 64, 33200  # 4.35e9 elements
+    dt, lens, budget = torch.float16, [300, 40], 100
+    pool = torch.empty(pages, page, hk, d, dtype=dt, device="cuda")
+    assert pool.numel() > 2**32
+    table = ints([[pages - 1, pages - 3], [pages - 2, pages - 4]])
+    g = torch.Generator().manual_seed(40)
+    k = torch.randn(340, hk, d, generator=g).to(dt).cuda()
+    ab.attn_cache_append(k, k, pool, pool, table, ints([0, 0]), ints([0, 300, 340]))
+    ab.check_device_status()
+    assert torch.equal(pool[pages - 1], k[:256]) and torch.equal(pool[pages - 3, :44], k[256:300])
+    assert torch.equal(pool[pages - 2, :40], k[300:])
+    q = torch.randn(2, 16, d, generator=g).to(dt).cuda()
+    o, lse = ab.attn_decode(q, pool, pool, table, ints(lens), max_seqlen=300)
+    ab.check_device_status()
+    check_decode(o, lse, q, pool, pool, table, lens, d ** -0.5)
+    w = torch.rand(2, hk, 300, generator=g)
+    before = rows_of(pool, table, 0, 300).clone()
+    n2, _, _ = ab.attn_cache_evict(pool, pool, table, ints(lens), w.cuda(), budget, max_seqlen=300)
+    ab.check_device_status()
+    assert n2.tolist() == [100, 40]
+    after = rows_of(pool, table, 0, 300)
+    for h in range(hk):
+        kept = co.keep(w[0, h].numpy(), None, 0, budget, 0)
+        want = before[:, h].clone()
+        for a, z in co.moves(kept, budget):
+            want[z] = before[a, h]
+        assert torch.equal(after[:, h], want)
+
+
 def test_decode_outputs_and_weights_in_other_arrays_and_strides():
     lens, hq, hk, d = [40, 170], 4, 2, 64
     q, kc, vc, table = _decode_inputs(lens, hq, hk, d, 16, False, torch.bfloat16)
@@ -318,7 +378,8 @@ def _evict_check(kc, vc, table, lens, w, pos, seen, budget, recent, before, out)
     """Against the oracle; before = (k, v) copies, out = (seqlens, weights, positions)."""
     n2, w2, p2 = (None if t is None else t.cpu().numpy() for t in out)
     page, tab = kc.shape[1], table.cpu().numpy()
-    wk, wv = (t.cpu().clone() for t in before)
+    bk, bv = (t.cpu() for t in before)
+    wk, wv = bk.clone(), bv.clone()
     for b, n in enumerate(lens):
         m = min(n, budget)
         assert n2[b] == m
@@ -328,7 +389,7 @@ def _evict_check(kc, vc, table, lens, w, pos, seen, budget, recent, before, out)
             pp = pos[b, h].copy() if pos is not None else None
             for a, z in co.moves(kept, budget) if n > budget else []:
                 s, t = co.slot(tab[b], page, a), co.slot(tab[b], page, z)
-                wk[t[0], t[1], h], wv[t[0], t[1], h] = before[0][s[0], s[1], h].cpu(), before[1][s[0], s[1], h].cpu()
+                wk[t[0], t[1], h], wv[t[0], t[1], h] = bk[s[0], s[1], h], bv[s[0], s[1], h]
                 ww[z] = ww[a]
                 if pp is not None:
                     pp[z] = pp[a]
@@ -366,6 +427,20 @@ def test_evict_matches_the_oracle(case, ranks, inplace):
             assert np.array_equal(rest[0], w[b, :, m:], equal_nan=True) and np.array_equal(rest[1], pos[b, :, m:])
         else:
             assert (rest[0] == -9).all() and (rest[1] == -9).all()
+
+
+LARGE = [
+    # one block a head with more slots than it keeps keys of; several blocks a head; eight
+    ("bf16", [5000 - 3 * i for i in range(20)], 16, 8, 64, False, 4500, 50),
+    ("fp16", [2100 - i for i in range(25)], 4, 8, 16, True, 700, 100),
+    ("bf16", [40000, 38001], 2, 8, 100, False, 20000, 1000),
+]
+
+
+@pytest.mark.parametrize("ranks", ["coarse", "odd"])
+@pytest.mark.parametrize("case", LARGE, ids=[f"{len(c[1])}seq-h{c[2]}-to{c[6]}" for c in LARGE])
+def test_evict_of_long_and_many(case, ranks):
+    test_evict_matches_the_oracle(case, ranks, ranks == "coarse")
 
 
 def test_evict_without_positions_long_and_captured():
