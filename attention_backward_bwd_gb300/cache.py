@@ -36,6 +36,21 @@ def _fail(rc: int):
     raise AttnError(rc, lib().attn_last_error().decode())
 
 
+def _pack(form: struct.Struct, *values) -> bytes:
+    try:
+        return form.pack(*values)
+    except struct.error as e:
+        raise AttnError(-9, f"an argument does not fit its C type: {e}") from None
+
+
+def _int32(name, value) -> int:
+    """``value`` as an int that a C int holds (ctypes would drop the upper bits)."""
+    value = int(value)
+    if not -2**31 <= value < 2**31:
+        raise AttnError(-9, f"{name} ({value}) does not fit 32 bits")
+    return value
+
+
 def _call(fn, index, stream, made, *args):
     """Runs fn(*args, stream) with device ``index`` current.  ``made``: tensors
     allocated by the caller; their memory is kept from reuse until ``stream`` has
@@ -123,7 +138,7 @@ def _cache(k_cache, v_cache, table, index, dtype, batch):
         raise AttnError(-9, f"block_table must be an int32 tensor [{batch}, pages] on cuda:{index} with "
                             f"contiguous rows, got {table.dtype} {tuple(table.shape)} on {table.device}")
     per = table.shape[1]
-    return _PAGED.pack(k_cache.data_ptr(), ks[0], ks[1], ks[2], v_cache.data_ptr(), vs[0], vs[1], vs[2],
+    return _pack(_PAGED, k_cache.data_ptr(), ks[0], ks[1], ks[2], v_cache.data_ptr(), vs[0], vs[1], vs[2],
                        table.data_ptr(), table.stride(0), pages, size, per), heads, dim, per * size
 
 
@@ -142,7 +157,7 @@ def _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, to
     if positions.get_device() != index or positions.dtype is not _I32 or not positions.is_contiguous():
         raise AttnError(-9, f"positions must be a contiguous int32 tensor on cuda:{index}, got "
                             f"{positions.dtype} on {positions.device}")
-    return _ROTARY.pack(positions.data_ptr(), tokens, inv_freq.data_ptr(), n, axes,
+    return _pack(_ROTARY, positions.data_ptr(), tokens, inv_freq.data_ptr(), n, axes,
                         *sec, *(0, 0, 0, 0)[axes:], 1 if interleaved else 0, 1 if inverse else 0)
 
 
@@ -188,6 +203,7 @@ def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = Non
         tokens, lead = batch * seqlen, (batch, seqlen)
     else:
         raise AttnError(-2, f"q must be [B, S, H, D] or packed [total, H, D], got {tuple(shape)}")
+    _int32("the tokens' number", tokens)
     made = []
     sq = _rows("q", q, index, dtype, dims)
     out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
@@ -198,14 +214,14 @@ def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = Non
         if k.shape != (*lead, hk, d):
             raise AttnError(-2, f"q {tuple(shape)} and k {tuple(k.shape)} disagree on tokens or D")
         out_k, sok = _output("out_k", out_k, k, sk, index, dtype, made)
-        pk, pok = _TENSOR.pack(k.data_ptr(), *_stride3(sk)), _TENSOR.pack(out_k.data_ptr(), *_stride3(sok))
+        pk, pok = _pack(_TENSOR, k.data_ptr(), *_stride3(sk)), _pack(_TENSOR, out_k.data_ptr(), *_stride3(sok))
     elif out_k is not None:
         raise AttnError(-9, "out_k without k")
     rot = _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, tokens)
     if tokens == 0:
         return out_q, out_k
-    _call(lib().attn_rope, index, stream, made, _TENSOR.pack(q.data_ptr(), *_stride3(sq)), pk,
-          _TENSOR.pack(out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
+    _call(lib().attn_rope, index, stream, made, _pack(_TENSOR, q.data_ptr(), *_stride3(sq)), pk,
+          _pack(_TENSOR, out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
     return out_q, out_k
 
 
@@ -231,6 +247,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
     if v.shape != k.shape:
         raise AttnError(-2, f"v has shape {tuple(v.shape)}, k {tuple(k.shape)}")
     batch = _batch(seqlens)
+    _int32("the tokens' number", tokens)
     lens = _ints("seqlens", seqlens, index, batch)
     cache, heads, dim, _ = _cache(k_cache, v_cache, block_table, index, dtype, batch)
     if heads != hk or dim != d:
@@ -254,8 +271,8 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
         if q.shape != (tokens, hq, d):
             raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
         out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
-        q_arg = _TENSOR.pack(q.data_ptr(), 0, sq[0], sq[1])
-        oq_arg = _TENSOR.pack(out_q.data_ptr(), 0, so[0], so[1])
+        q_arg = _pack(_TENSOR, q.data_ptr(), 0, sq[0], sq[1])
+        oq_arg = _pack(_TENSOR, out_q.data_ptr(), 0, so[0], so[1])
     elif out_q is not None:
         raise AttnError(-9, "out_q without q")
     sp, width = None, 0
@@ -266,7 +283,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
     if tokens == 0:
         return out_q
     _call(lib().attn_cache_append, index, stream, made, q_arg, oq_arg,
-          _TENSOR.pack(k.data_ptr(), 0, sk[0], sk[1]), _TENSOR.pack(v.data_ptr(), 0, sv[0], sv[1]), dt,
+          _pack(_TENSOR, k.data_ptr(), 0, sk[0], sk[1]), _pack(_TENSOR, v.data_ptr(), 0, sv[0], sv[1]), dt,
           tokens, batch, hq, hk, d, cache, lens, cu, rot, sp, width, _ints("seen", seen, index, batch))
     return out_q
 
@@ -274,7 +291,8 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
 @functools.lru_cache(maxsize=256)
 def decode_workspace_size(batch: int, h_q: int, h_k: int, head_dim: int, max_seqlen: int,
                           weights: bool = False) -> int:
-    return int(lib().attn_decode_workspace_size(batch, h_q, h_k, head_dim, max_seqlen, int(weights)))
+    return int(lib().attn_decode_workspace_size(batch, h_q, h_k, head_dim, _int32("max_seqlen", max_seqlen),
+                                                int(weights)))
 
 
 def alloc_decode_workspace(q, k_cache, max_seqlen: int, weights: bool = False) -> torch.Tensor:
@@ -317,7 +335,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
     if dim != d or hk == 0 or hq % hk != 0:
         raise AttnError(-2, f"q {tuple(q.shape)} does not fit a cache {tuple(k_cache.shape)}")
     lens = _ints("seqlens", seqlens, index, batch)
-    max_seqlen = slots if max_seqlen is None else int(max_seqlen)
+    max_seqlen = _int32("max_seqlen", slots if max_seqlen is None else max_seqlen)
     made = []
     out, so = _output("out", out, q, sq, index, dtype, made)
     if lse is None:
@@ -344,9 +362,9 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
     opts = None
     if window is not None or softcap:
         left, right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-        opts = _OPTS.pack(left, right, float(softcap or 0.0), 0, 0)
-    _call(lib().attn_decode, index, stream, made, _TENSOR.pack(q.data_ptr(), sq[0], 0, sq[1]),
-          _TENSOR.pack(out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
+        opts = _pack(_OPTS, left, right, float(softcap or 0.0), 0, 0)
+    _call(lib().attn_decode, index, stream, made, _pack(_TENSOR, q.data_ptr(), sq[0], 0, sq[1]),
+          _pack(_TENSOR, out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
           d ** -0.5 if scale is None else float(scale), cache, lens, max_seqlen, opts, w_in, w_out,
           width, ws, size)
     return out, lse
@@ -354,7 +372,8 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
 
 @functools.lru_cache(maxsize=256)
 def evict_workspace_size(batch: int, h_k: int, budget: int, max_seqlen: int) -> int:
-    return int(lib().attn_cache_evict_workspace_size(batch, h_k, budget, max_seqlen))
+    return int(lib().attn_cache_evict_workspace_size(batch, h_k, _int32("budget", budget),
+                                                     _int32("max_seqlen", max_seqlen)))
 
 
 def alloc_evict_workspace(seqlens, k_cache, budget: int, max_seqlen: int) -> torch.Tensor:
@@ -382,8 +401,8 @@ def attn_cache_evict(k_cache, v_cache, block_table, seqlens, weights, budget: in
     batch = _batch(seqlens)
     cache, hk, d, slots = _cache(k_cache, v_cache, block_table, index, dtype, batch)
     lens = _ints("seqlens", seqlens, index, batch)
-    max_seqlen = slots if max_seqlen is None else int(max_seqlen)
-    budget = int(budget)
+    max_seqlen = _int32("max_seqlen", slots if max_seqlen is None else max_seqlen)
+    budget, recent = _int32("budget", budget), _int32("recent", recent)
     if weights_out is None:
         weights_out = weights
     w_in, width = _state("weights", weights, index, _F32, batch, hk, max_seqlen)
@@ -411,5 +430,5 @@ def attn_cache_evict(k_cache, v_cache, block_table, seqlens, weights, budget: in
     ws, size = _workspace(workspace, evict_workspace_size(batch, hk, budget, max_seqlen), k_cache,
                           index, made)
     _call(lib().attn_cache_evict, index, stream, made, cache, dt, batch, hk, d, lens, out, max_seqlen,
-          budget, int(recent), _ints("seen", seen, index, batch), w_in, w_out, p_in, p_out, width, ws, size)
+          budget, recent, _ints("seen", seen, index, batch), w_in, w_out, p_in, p_out, width, ws, size)
     return seqlens_out, weights_out, positions_out

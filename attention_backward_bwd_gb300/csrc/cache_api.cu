@@ -324,8 +324,10 @@ int attn_cache_evict(const attn_paged_kv* cache, int dtype, int batch, int h_k, 
                 recent);
   if (seqlens == nullptr || seqlens_out == nullptr || weights_in == nullptr || weights_out == nullptr)
     return fail(ATTN_ERR_NULL, "seqlens, seqlens_out, weights_in and weights_out must be given");
-  if (seqlens == seqlens_out)
-    return fail(ATTN_ERR_ARG, "seqlens_out must be another array than seqlens");
+  // blocks of one sequence read them while another writes its length
+  for (const int* in : {seqlens, seen})
+    if (in != nullptr && in < seqlens_out + batch && seqlens_out < in + batch)
+      return fail(ATTN_ERR_ARG, "seqlens_out must not overlap seqlens or seen");
   if ((positions_in == nullptr) != (positions_out == nullptr))
     return fail(ATTN_ERR_ARG, "positions_in and positions_out must both be given or both be NULL");
   if (recent > 0 && (positions_in == nullptr || seen == nullptr))

@@ -249,7 +249,7 @@ __device__ __forceinline__ int find_sequence(const DecodeParams& p, const int* p
   before = pre[lo];
   for (int b = lo * per;; ++b) {
     const int t = tiles_of(p, len_of(b));
-    if (r0 < static_cast<long long>(before + t) * hv_n) return b;
+    if (b + 1 >= p.batch || r0 < static_cast<long long>(before + t) * hv_n) return b;
     before += t;
   }
 }
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         do {
           ++cb;
           load_seq(len_of(cb));
-        } while (cnt == 0);
+        } while (cnt == 0 && cb + 1 < p.batch);
       }
       load_head();
     };

@@ -113,7 +113,7 @@ __device__ __forceinline__ TokenInfo locate(const RopeParams& p, int t, bool fir
     b = lo;
     const int c0 = p.cu[b], c1 = p.cu[b + 1];
     if (t >= p.cu[p.batch]) return info;  // behind the last sequence
-    if (t < c0 || t >= c1) {
+    if (c0 < 0 || t < c0 || t >= c1) {
       if (lane == 0) report(p.status, kBadOffsets);
       return info;
     }

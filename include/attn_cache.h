@@ -52,9 +52,9 @@ typedef struct {
  * inv_freq[i]: (x, y) -> (x cos - y sin, x sin + y cos).  The pair is
  * (x_i, x_{i + n_freq}), or (x_{2i}, x_{2i+1}) when interleaved != 0; elements
  * from 2 * n_freq on are copied.  inverse != 0 turns by the negative angle,
- * which is also the backward pass (the rotation's transpose).  The angle is
- * exact to about 2^-24 of a turn for every int32 position (it is reduced in
- * 64-bit fixed point); inv_freq must be finite.
+ * which is also the backward pass (the rotation's transpose).  For
+ * |inv_freq| <= 1 the angle is exact to about 2^-24 of a turn at every int32
+ * position (it is reduced in 64-bit fixed point); inv_freq must be finite.
  */
 typedef struct {
   const int* positions;   /* device int32, n_axes rows of one entry per token */
@@ -144,7 +144,7 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
  * moved state of slots < n, with 0 and -1 in slots [budget, n); further
  * entries are left as they were.  Sequences with n <= budget keep everything
  * (their state is copied when the outputs are other arrays).  Outputs may be
- * the inputs themselves, but seqlens_out must not be seqlens.
+ * the inputs themselves, but seqlens_out must overlap neither seqlens nor seen.
  * The state arrays are [batch][H_k][state_stride], state_stride >= max_seqlen.
  * positions_in and positions_out are given both or neither; recent > 0 needs
  * them and seen.  0 < budget, 0 <= recent <= budget.  A sequence whose

@@ -170,7 +170,9 @@ def test_workspace_sizes(lib):
     assert ab.decode_workspace_size(4, 5, 2, 128, 10) == 0
     assert ab.decode_workspace_size(4, 32, 8, 128, 256) == 0
     assert ab.decode_workspace_size(4, 32, 8, 128, 100, weights=True) > 0
-    assert ab.evict_workspace_size(4, 8, 100, 1000) >= 4 * 8 * (4 + 2 * 400)
+    # a head's sources and targets: at most as many as the budget, and as the slots above it
+    assert ab.evict_workspace_size(4, 8, 100, 1000) == 4 * 8 * 2 * 100 * 4
+    assert ab.evict_workspace_size(4, 8, 900, 1000) == 4 * 8 * 2 * 100 * 4
     assert ab.evict_workspace_size(4, 8, 100, 50) >= 4 * 8 * 4
     assert ab.evict_workspace_size(0, 8, 100, 50) == 0
 
@@ -192,3 +194,20 @@ def test_python_entry_points_refuse_what_is_not_on_a_gpu(lib):
     assert _code(ab.attn_cache_evict, c, c, table, n, torch.zeros(4, 2, 16), 4) == ARG
     assert _code(ab.attn_rope, q.float(), None, pos, inv) == DTYPE
     assert _code(ab.attn_decode, q.to("meta"), c, c, table, n) == ARG
+
+
+def test_evict_refuses_lengths_that_overlap(lib):
+    for n2 in (P, P + 4, P - 4):
+        assert evict(lib, n2=n2) == ARG, n2           # b = 2: seqlens is [P, P + 8)
+    for n2 in (2 * P, 2 * P + 4, 2 * P - 4):
+        assert evict(lib, n2=n2, recent=1, seen=2 * P, pi=P, po=P) == ARG, n2
+    assert evict(lib, n2=P + 8, ws=None) == WS        # beside it: refused for the next reason
+
+
+def test_integers_beyond_32_bits_are_refused(lib):
+    for bad in (2**31, 2**32 + 5, -2**31 - 1):
+        assert _code(binding_cache._int32, "x", bad) == ARG
+        assert _code(binding_cache._pack, binding_cache._OPTS, bad, 0, 0.0, 0, 0) == ARG
+        assert _code(ab.decode_workspace_size, 4, 32, 8, 128, bad) == ARG
+        assert _code(ab.evict_workspace_size, 4, 8, bad, 100) == ARG
+    assert binding_cache._int32("x", 2**31 - 1) == 2**31 - 1

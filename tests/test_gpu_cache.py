@@ -345,6 +345,32 @@ def test_decode_gives_the_same_bits_again_and_on_replay():
     check_decode(out, lse, q, kc, vc, table, new, d ** -0.5, weights=w2, weights_in=base)
 
 
+def test_lengths_beyond_32_bits_are_refused():
+    lens, hq, hk, d, page, dt = [20, 9], 4, 2, 64, 8, torch.float16
+    q = torch.randn(2, hq, d, dtype=dt, device="cuda")
+    kc, vc, table = make_cache(lens, hk, d, page, dt, 3)
+    for kw in (dict(max_seqlen=2**32 + 5), dict(window=(2**32, -1))):
+        with pytest.raises(ab.AttnError):
+            ab.attn_decode(q, kc, vc, table, ints(lens), **kw)
+    w = torch.zeros(2, hk, 24, device="cuda")
+    for budget, recent in ((2**32 + 5, 0), (5, 2**32)):
+        with pytest.raises(ab.AttnError):
+            ab.attn_cache_evict(kc, vc, table, ints(lens), w, budget, recent, max_seqlen=20)
+
+
+def test_append_offsets_far_below_zero_are_reported():
+    kc, vc, table = make_cache([16, 16], 2, 64, 8, torch.float16, 5)
+    k0, v0 = kc.clone(), vc.clone()
+    k, v = torch.randn(2, 4, 2, 64).half().cuda()
+    # the last one's place in its sequence passes 2^31
+    for first in (-1, -2**31):
+        ab.attn_cache_append(k, v, kc, vc, table, ints([0, 0]), ints([first, 4, 4]))
+        with pytest.raises(ab.AttnError) as e:
+            ab.check_device_status()
+        assert e.value.code == -9
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)
+
+
 def test_decode_on_two_streams_at_once():
     lens, hq, hk, d = [900, 40], 8, 2, 64
     sets = [_decode_inputs(lens, hq, hk, d, 16, False, torch.float16, seed=s) for s in (21, 22)]
