@@ -29,7 +29,9 @@ namespace attn {
 namespace {
 
 constexpr int kBins = 256;
-constexpr int kCap = 4096;  // keys of a block in shared memory; further ones are worked out again
+// keys of a block in shared memory; further ones are worked out again
+template <int T>
+constexpr int kCap = T == 512 ? 8192 : 4096;
 constexpr int kMaxCluster = 8;
 
 // Unsigned key in the order of the ranks: NaN lowest, then the floats (-0 = +0).
@@ -41,11 +43,13 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 constexpr uint32_t kInfKey = 0xFF800000u;  // rank_key(+inf): the rank of a recent slot
 
 template <int T>
-__global__ void __launch_bounds__(T, T == 256 ? 4 : 2) evict_kernel(EvictParams p, int cs, FastDiv chunks) {
+__global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(EvictParams p, int cs, FastDiv chunks) {
   constexpr int W = T / 32;
-  __shared__ uint32_t s_key[kCap];
+  constexpr int kOwn = T < kBins ? kBins / T : 1;  // bins of a thread
+  constexpr int kSums = kBins / kOwn / 32;         // warps that have some
+  __shared__ uint32_t s_key[kCap<T>];
   __shared__ int hist[4][kBins];
-  __shared__ int s_sums[kBins / 32];
+  __shared__ int s_sums[kSums];
   __shared__ int2 s_warp[W];        // counts of each warp's run: ties; or holes and movers
   __shared__ int2 s_tot[2];         // the block's, read by the cluster
   __shared__ int s_digit, s_left, s_equal;
@@ -96,13 +100,13 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 2) evict_kernel(EvictParams 
     const float x = w[j];
     const int q = pos != nullptr ? pos[j] : 0;
     const uint32_t k = p.recent > 0 && q >= recent_from ? kInfKey : rank_key(x);
-    if (j - first < kCap) s_key[j - first] = k;
+    if (j - first < kCap<T>) s_key[j - first] = k;
     atomicAdd(&hist[0][k >> 24], 1);
     if (copy_w) w_out[j] = j < p.budget ? x : 0.f;
     if (copy_pos) pos_out[j] = j < p.budget ? q : -1;
   }
   auto key = [&](int j) -> uint32_t {
-    if (j - first < kCap) return s_key[j - first];
+    if (j - first < kCap<T>) return s_key[j - first];
     return p.recent > 0 && pos[j] >= recent_from ? kInfKey : rank_key(w[j]);
   };
 
@@ -119,15 +123,21 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 2) evict_kernel(EvictParams 
         if (((k ^ prefix) >> (shift + 8)) == 0) atomicAdd(&hist[pass][(k >> shift) & 255u], 1);
       }
     sync_all();
-    // thread t: bin 255 - t, the highest first
-    int mine = 0;
-    if (tid < kBins) {
-      if (cs == 1)
-        mine = hist[pass][kBins - 1 - tid];
-      else
+    // a thread kOwn bins, the highest first
+    int bins[kOwn], mine = 0;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < cs) mine += cluster.map_shared_rank(&hist[pass][0], r)[kBins - 1 - tid];
+    for (int i = 0; i < kOwn; ++i) bins[i] = 0;
+    if (tid < kBins / kOwn) {
+      const int at = kBins - kOwn * (tid + 1);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < cs) {
+          const int* from = cs == 1 ? &hist[pass][at] : cluster.map_shared_rank(&hist[pass][at], r);
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) bins[i] += from[kOwn - 1 - i];
+        }
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) mine += bins[i];
     }
     int x = mine;
 #pragma unroll
@@ -135,15 +145,19 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 2) evict_kernel(EvictParams 
       const int y = __shfl_up_sync(0xffffffffu, x, i);
       if (lane >= i) x += y;
     }
-    if (lane == 31 && warp < kBins / 32) s_sums[warp] = x;
+    if (lane == 31 && warp < kSums) s_sums[warp] = x;
     __syncthreads();
     int above = x - mine;
 #pragma unroll
-    for (int v = 0; v < kBins / 32 - 1; ++v) above += v < warp ? s_sums[v] : 0;
-    if (above < need && above + mine >= need) {
-      s_digit = kBins - 1 - tid;
-      s_left = need - above;
-      s_equal = mine;
+    for (int v = 0; v < kSums - 1; ++v) above += v < warp ? s_sums[v] : 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (above < need && above + bins[i] >= need) {
+        s_digit = kBins - 1 - kOwn * tid - i;
+        s_left = need - above;
+        s_equal = bins[i];
+      }
+      above += bins[i];
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_digit) << shift;
@@ -320,13 +334,23 @@ cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream) {
   (void)dtype;  // rows are moved as 16-byte chunks
   const int64_t heads = static_cast<int64_t>(p.batch) * p.h_k;
   if (heads * kMaxCluster > INT32_MAX) return cudaErrorInvalidValue;
-  // blocks of a head: while all of them fit the device at once and each has 512 slots
+  // Blocks of a head: as many as keep its keys in shared memory (320 heads of 16000 slots:
+  // 457 us with one block, 133 with four), then while all blocks fit the device at once and
+  // each has 1024 slots (32 heads of 8192: 32 us with two, 21 with eight; of 1088: 10.0 with
+  // one, 11.6 with two).
+  const int64_t sms = num_sms();
   int cs = 1;
-  while (cs < kMaxCluster && heads * cs * 2 <= 4 * static_cast<int64_t>(num_sms()) &&
-         p.max_seqlen / (cs * 2) >= 512)
+  while (cs < kMaxCluster &&
+         (p.max_seqlen / cs > kCap<128> ||
+          (heads * cs * 2 <= 4 * sms && p.max_seqlen / (cs * 2) >= 1024)))
     cs *= 2;
-  return heads * cs <= 2 * static_cast<int64_t>(num_sms()) ? launch_t<512>(p, cs, stream)
-                                                           : launch_t<256>(p, cs, stream);
+  // Threads of a block: most where there are few blocks; fewer where there are many, which
+  // then pass their barriers side by side (1024 heads of 1088 slots: 29 us with 512, 21 with
+  // 256, 17 with 128; 400 heads: 16.5, 12.5, 14.4; 160 heads of 8192, two blocks each: 88,
+  // 84, 129).
+  if (heads * cs <= 2 * sms || p.max_seqlen / cs > kCap<256>) return launch_t<512>(p, cs, stream);
+  if (heads * cs <= 4 * sms) return launch_t<256>(p, cs, stream);
+  return launch_t<128>(p, cs, stream);
 }
 
 }  // namespace attn
