@@ -460,6 +460,9 @@ LARGE = [
     ("bf16", [5000 - 3 * i for i in range(20)], 16, 8, 64, False, 4500, 50),
     ("fp16", [2100 - i for i in range(25)], 4, 8, 16, True, 700, 100),
     ("bf16", [40000, 38001], 2, 8, 100, False, 20000, 1000),
+    # eight blocks with more slots than they keep keys of; many heads of several blocks each
+    ("fp16", [70001, 5], 1, 8, 64, False, 1000, 10),
+    ("bf16", [8700 - i for i in range(20)], 16, 8, 64, False, 8600, 50),
 ]
 
 
