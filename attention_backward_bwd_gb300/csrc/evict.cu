@@ -13,11 +13,11 @@
 // need no order.  Then the cluster's threads move state and rows, 16 bytes a thread.
 //
 // The bytes are few (n weights and positions a head, and the rows that move); what
-// bounds short heads is the chain of dependent steps.  Of 19.2 us for 1024 heads of 1025 to
+// bounds short heads is the chain of dependent steps.  Of 18.6 us for 1024 heads of 1025 to
 // 1088 slots cut to 1024, the launch and the keys take 6.2, the selection 2.7, the places
-// 3.4, the moves 7 (34 MB in all, 5.1 us at the memory's speed); of 22 us for 32 heads of
+// 3.4, the moves 6 (34 MB in all, 5.1 us at the memory's speed); of 23 us for 32 heads of
 // 5000 to 16000 slots 4.8, 5.5, 3.4 and 8.  Heads that move much are bound by memory again
-// (1024 heads of 8192 cut to 4096: 339 us, 1.1 GB moved as rows of 128 bytes in any order).
+// (1024 heads of 8192 cut to 4096: 327 us, 1.1 GB moved as rows of 128 bytes in any order).
 // The loops are short: a form with the keys in registers and every loop unrolled spent 52 %
 // of its warps' time fetching instructions.
 #include <cooperative_groups.h>
@@ -36,6 +36,7 @@ constexpr int kBins = 256;
 template <int T>
 constexpr int kCap = T == 512 ? 8192 : 4096;
 constexpr int kMaxCluster = 8;
+constexpr int kLeast = 1024;  // slots of a block where a head of the greatest length has several
 
 // Unsigned key in the order of the ranks: NaN lowest, then the floats (-0 = +0).
 __device__ __forceinline__ uint32_t rank_key(float w) {
@@ -45,8 +46,9 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 }
 constexpr uint32_t kInfKey = 0xFF800000u;  // rank_key(+inf): the rank of a recent slot
 
-template <int T>
-__global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(EvictParams p, int cs, FastDiv chunks) {
+// kSpread: a head has several blocks.  (One form for both made single blocks 2 us slower.)
+template <int T, bool kSpread>
+__global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(EvictParams p, int blocks_log2, FastDiv chunks) {
   constexpr int W = T / 32;
   constexpr int kOwn = T < kBins ? kBins / T : 1;  // bins of a thread
   constexpr int kSums = kBins / kOwn / 32;         // warps that have some
@@ -57,11 +59,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(Evict
   __shared__ int2 s_tot[2];         // the block's, read by the cluster
   __shared__ int s_digit, s_left, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
-  auto sync_all = [&]() {  // the blocks of this head
-    if (cs == 1) __syncthreads(); else cluster.sync();
-  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = blockIdx.x / cs, rank = blockIdx.x - bh * cs;
+  const int bh = kSpread ? blockIdx.x >> blocks_log2 : blockIdx.x;
+  const int rank = kSpread ? blockIdx.x & ((1 << blocks_log2) - 1) : 0;
   const int b = bh / p.h_k, h = bh - b * p.h_k;
   const int n = p.seqlens[b];
   if (n < 0 || n > p.max_seqlen) {
@@ -71,6 +71,16 @@ __global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(Evict
     }
     return;
   }
+  // The launch knows the bound of the lengths alone: of a shorter sequence's blocks as many
+  // leave as would have less than 512 slots (the cluster's barrier does not wait for them):
+  // 1024 heads of 1088 slots with a bound of 32768 take 39 us, 118 with all blocks at work.
+  int cs_log2 = kSpread ? blocks_log2 : 0;
+  while (cs_log2 > 0 && n >> cs_log2 < kLeast / 2) --cs_log2;
+  const int cs = kSpread ? 1 << cs_log2 : 1;
+  if (rank >= cs) return;
+  auto sync_all = [&]() {  // the blocks of this head
+    if (cs == 1) __syncthreads(); else cluster.sync();
+  };
   const int64_t base = static_cast<int64_t>(bh) * p.stride;
   const float* w = p.w_in + base;
   float* w_out = p.w_out + base;
@@ -87,7 +97,7 @@ __global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(Evict
   }
 
   // ---- runs: the block's slots are [first, last), the warp's [from_slot, to_slot)
-  const int per = (n + cs - 1) / cs;
+  const int per = (n + cs - 1) >> cs_log2;
   const int first = min(n, rank * per), last = min(n, first + per);
   const int run = ((last - first + W - 1) / W + 31) & ~31;
   const int from_slot = min(last, first + warp * run), to_slot = min(last, from_slot + run);
@@ -314,21 +324,21 @@ __global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(Evict
 }
 
 template <int T>
-cudaError_t launch_t(const EvictParams& p, int cs, cudaStream_t stream) {
+cudaError_t launch_t(const EvictParams& p, int cs_log2, cudaStream_t stream) {
   FastDiv chunks;
   chunks.set(static_cast<uint32_t>(p.head_dim / 8));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.h_k * cs);
+  cfg.gridDim = dim3((static_cast<unsigned>(p.batch) * p.h_k) << cs_log2);
   cfg.blockDim = dim3(T);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.x = 1u << cs_log2;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<T>, p, cs, chunks);
+  cfg.numAttrs = cs_log2 > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, cs_log2 > 0 ? evict_kernel<T, true> : evict_kernel<T, false>, p, cs_log2, chunks);
 }
 
 }  // namespace
@@ -342,18 +352,19 @@ cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream) {
   // each has 1024 slots (32 heads of 8192: 32 us with two, 21 with eight; of 1088: 10.0 with
   // one, 11.6 with two).
   const int64_t sms = num_sms();
-  int cs = 1;
-  while (cs < kMaxCluster &&
-         (p.max_seqlen / cs > kCap<128> ||
-          (heads * cs * 2 <= 4 * sms && p.max_seqlen / (cs * 2) >= 1024)))
-    cs *= 2;
+  int log2 = 0;
+  while ((1 << log2) < kMaxCluster &&
+         (p.max_seqlen >> log2 > kCap<128> ||
+          (heads << (log2 + 1) <= 4 * sms && p.max_seqlen >> (log2 + 1) >= kLeast)))
+    ++log2;
   // Threads of a block: most where there are few blocks; fewer where there are many, which
   // then pass their barriers side by side (1024 heads of 1088 slots: 29 us with 512, 21 with
   // 256, 17 with 128; 400 heads: 16.5, 12.5, 14.4; 160 heads of 8192, two blocks each: 88,
   // 84, 129).
-  if (heads * cs <= 2 * sms || p.max_seqlen / cs > kCap<256>) return launch_t<512>(p, cs, stream);
-  if (heads * cs <= 4 * sms) return launch_t<256>(p, cs, stream);
-  return launch_t<128>(p, cs, stream);
+  const int64_t blocks = heads << log2;
+  if (blocks <= 2 * sms || p.max_seqlen >> log2 > kCap<256>) return launch_t<512>(p, log2, stream);
+  if (blocks <= 4 * sms) return launch_t<256>(p, log2, stream);
+  return launch_t<128>(p, log2, stream);
 }
 
 }  // namespace attn

@@ -472,6 +472,25 @@ def test_evict_of_long_and_many(case, ranks):
     test_evict_matches_the_oracle(case, ranks, ranks == "coarse")
 
 
+@pytest.mark.parametrize("batch", [2, 40])
+def test_evict_under_a_loose_bound(batch):
+    """Lengths far below max_seqlen: some or all but one of a head's blocks leave."""
+    lens = ([1500, 300, 90, 2500, 70, 0, 5000, 64] * 5)[:batch]
+    hk, d, page, budget, recent, top = 8, 8, 16, 64, 9, 20000
+    kc, vc, table = make_cache(lens, hk, d, page, torch.float16, 12)
+    wide = torch.full((batch, -(-top // page)), 1 << 30, dtype=torch.int32, device="cuda")  # no such page
+    wide[:, :table.shape[1]] = table
+    rng = np.random.default_rng(13)
+    w = rng.integers(0, 9, (batch, hk, top)).astype(np.float32)
+    pos = np.stack([[rng.permutation(top) for _ in range(hk)] for _ in lens]).astype(np.int32)
+    seen = [n + 2 for n in lens]
+    before = kc.clone(), vc.clone()
+    out = ab.attn_cache_evict(kc, vc, wide, ints(lens), torch.from_numpy(w).cuda(), budget, recent,
+                              torch.from_numpy(pos).cuda(), ints(seen))
+    ab.check_device_status()
+    _evict_check(kc, vc, wide, lens, w, pos, seen, budget, recent, before, out)
+
+
 def test_evict_without_positions_long_and_captured():
     lens, hk, d, budget = [40000, 300], 2, 64, 1000
     kc, vc, table = make_cache(lens, hk, d, 64, torch.bfloat16, 8)
