@@ -204,6 +204,24 @@ def test_decode_of_many_sequences_and_heads(case, weights):
     check_decode(o, lse, q, kc, vc, table, lens, d ** -0.5, window, 0.0, w, w0)
 
 
+@pytest.mark.parametrize("window", [-1, 900])
+def test_decode_weights_of_long_among_many_under_a_loose_bound(window):
+    """A block of the weights' kernel takes more than one stretch of its keys."""
+    batch, hq, hk, d, page, top = 320, 16, 8, 64, 16, 3000
+    lens = [1300 + i if i % 40 == 3 else i % 11 for i in range(batch)]
+    q, kc, vc, table = _decode_inputs(lens, hq, hk, d, page, False, torch.float16)
+    wide = torch.full((batch, -(-top // page)), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    w0, w1 = torch.rand(batch, hk, top, device="cuda"), torch.full((batch, hk, top), -3.0, device="cuda")
+    o, lse = ab.attn_decode(q, kc, vc, wide, ints(lens), window=None if window < 0 else (window, 0),
+                            max_seqlen=top, weights=w0, weights_out=w1)
+    ab.check_device_status()
+    base = w0.clone()
+    for b, n in enumerate(lens):
+        base[b, :, n:] = -3.0
+    check_decode(o, lse, q, kc, vc, wide, lens, d ** -0.5, window, weights=w1, weights_in=base)
+
+
 def test_pages_behind_2_to_the_32_elements():
     """A cache of more than 2^32 elements (10 GB, keys and values in the same pages): append,
     decode and evict on its last pages."""
