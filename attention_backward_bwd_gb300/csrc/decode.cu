@@ -47,6 +47,7 @@ constexpr int kCompute = kWarps * 32;
 constexpr int kCopy = 64;       // copying threads
 constexpr int kThreads = kCompute + kCopy;
 constexpr int kJoin = 128;      // threads of a join block
+constexpr int kAhead = 8;       // partials of a lane in flight there
 constexpr int kMaxRows = 16;    // query heads of a block
 constexpr int kLens = 256;      // lengths kept in shared memory
 constexpr int kBlocks = 2;      // of an SM
@@ -731,8 +732,21 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks,
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   if (on) {
     float* w = s_w[warp];
+    // rows of the first partials are on their way while the maxima are compared
+    float4 x[2][kAhead];
+    auto load = [&](int c, int i0) {
+      const int col = row * dp + (lane + 32 * c) * 4;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * shares < nc) x[c][k] = *reinterpret_cast<const float4*>(part(i0 + k * shares) + col);
+    };
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (lane + 32 * c < dp / 4) load(c, share);
+    float sums = 0.f;  // of partial `lane`
     for (int i = lane; i < nc; i += 32) {
       w[i] = part(i)[part_m + row];
+      if (i == lane) sums = part(i)[part_m + kMaxRows + row];
       top = fmaxf(top, w[i]);
     }
 #pragma unroll
@@ -740,31 +754,26 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks,
     const float base = top == -INFINITY ? 0.f : top;
     for (int i = lane; i < nc; i += 32) {
       w[i] = ex2(w[i] - base);
-      sum += w[i] * part(i)[part_m + kMaxRows + row];
+      sum += w[i] * (i == lane ? sums : part(i)[part_m + kMaxRows + row]);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (lane + 32 * c < dp / 4) {
-        const int col = row * dp + (lane + 32 * c) * 4;
-        for (int i0 = share; i0 < nc; i0 += 8 * shares) {
-          float4 x[8];
+      if (lane + 32 * c < dp / 4)
+        for (int i0 = share; i0 < nc; i0 += kAhead * shares) {
+          if (i0 != share) load(c, i0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i0 + k * shares < nc) x[k] = *reinterpret_cast<const float4*>(part(i0 + k * shares) + col);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < kAhead; ++k)
             if (i0 + k * shares < nc) {
               const float f = w[i0 + k * shares];
-              acc[c].x += f * x[k].x;
-              acc[c].y += f * x[k].y;
-              acc[c].z += f * x[k].z;
-              acc[c].w += f * x[k].w;
+              acc[c].x += f * x[c][k].x;
+              acc[c].y += f * x[c][k].y;
+              acc[c].z += f * x[c][k].z;
+              acc[c].w += f * x[c][k].w;
             }
         }
-      }
   }
   if (shares > 1) {
     s_part[warp][lane] = acc[0];
