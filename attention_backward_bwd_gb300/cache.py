@@ -25,6 +25,7 @@ _TENSOR = struct.Struct("@Pqqq")
 _PAGED = struct.Struct("@PqqqPqqqPqiii4x")
 _ROTARY = struct.Struct("@PqPii4iii")
 _OPTS = struct.Struct("@iif4xPP")
+_tensor = _TENSOR.pack  # pointers and strides always fit
 _I32, _F32 = torch.int32, torch.float32
 # The current stream as an integer, without a Stream object around it (a call of a few
 # microseconds is mostly marshalling).
@@ -214,14 +215,14 @@ def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = Non
         if k.shape != (*lead, hk, d):
             raise AttnError(-2, f"q {tuple(shape)} and k {tuple(k.shape)} disagree on tokens or D")
         out_k, sok = _output("out_k", out_k, k, sk, index, dtype, made)
-        pk, pok = _pack(_TENSOR, k.data_ptr(), *_stride3(sk)), _pack(_TENSOR, out_k.data_ptr(), *_stride3(sok))
+        pk, pok = _tensor(k.data_ptr(), *_stride3(sk)), _tensor(out_k.data_ptr(), *_stride3(sok))
     elif out_k is not None:
         raise AttnError(-9, "out_k without k")
     rot = _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, tokens)
     if tokens == 0:
         return out_q, out_k
-    _call(lib().attn_rope, index, stream, made, _pack(_TENSOR, q.data_ptr(), *_stride3(sq)), pk,
-          _pack(_TENSOR, out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
+    _call(lib().attn_rope, index, stream, made, _tensor(q.data_ptr(), *_stride3(sq)), pk,
+          _tensor(out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
     return out_q, out_k
 
 
@@ -271,8 +272,8 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
         if q.shape != (tokens, hq, d):
             raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
         out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
-        q_arg = _pack(_TENSOR, q.data_ptr(), 0, sq[0], sq[1])
-        oq_arg = _pack(_TENSOR, out_q.data_ptr(), 0, so[0], so[1])
+        q_arg = _tensor(q.data_ptr(), 0, sq[0], sq[1])
+        oq_arg = _tensor(out_q.data_ptr(), 0, so[0], so[1])
     elif out_q is not None:
         raise AttnError(-9, "out_q without q")
     sp, width = None, 0
@@ -283,7 +284,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
     if tokens == 0:
         return out_q
     _call(lib().attn_cache_append, index, stream, made, q_arg, oq_arg,
-          _pack(_TENSOR, k.data_ptr(), 0, sk[0], sk[1]), _pack(_TENSOR, v.data_ptr(), 0, sv[0], sv[1]), dt,
+          _tensor(k.data_ptr(), 0, sk[0], sk[1]), _tensor(v.data_ptr(), 0, sv[0], sv[1]), dt,
           tokens, batch, hq, hk, d, cache, lens, cu, rot, sp, width, _ints("seen", seen, index, batch))
     return out_q
 
@@ -363,8 +364,8 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
     if window is not None or softcap:
         left, right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
         opts = _pack(_OPTS, left, right, float(softcap or 0.0), 0, 0)
-    _call(lib().attn_decode, index, stream, made, _pack(_TENSOR, q.data_ptr(), sq[0], 0, sq[1]),
-          _pack(_TENSOR, out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
+    _call(lib().attn_decode, index, stream, made, _tensor(q.data_ptr(), sq[0], 0, sq[1]),
+          _tensor(out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
           d ** -0.5 if scale is None else float(scale), cache, lens, max_seqlen, opts, w_in, w_out,
           width, ws, size)
     return out, lse

@@ -15,7 +15,8 @@
  * page, stride_h between heads, so a [num_pages, H_k, page_size, D] allocation
  * is passed by its strides).  Slot j of sequence b is slot j % page_size of
  * page block_table[b * table_stride + j / page_size].  Any page size >= 1.
- * Pages that a call writes (append, evict) must belong to one sequence only.
+ * Pages that a call writes (append, evict) must belong to one sequence only, and stand
+ * once in its row of the table.
  *
  * Device-side checks.  Lengths, block tables and offsets live in device
  * memory, so the kernels check them: a page outside [0, num_pages) is never
@@ -116,7 +117,8 @@ int attn_cache_append(const attn_tensor* q, const attn_tensor* oq, const attn_te
  * with weights_stride >= max_seqlen: weights_out[b][g][j] = weights_in[b][g][j]
  * + the sum over the group's query heads of softmax(s)_j, for j < seqlens[b];
  * further entries are left as they were.  They may be the same array.
- * max_seqlen: bound on seqlens, at most max_pages * page_size.
+ * max_seqlen: bound on seqlens, at most max_pages * page_size (the logits kept for the
+ * weights make the workspace grow with it).
  * workspace: at least attn_decode_workspace_size(...) bytes, 256-byte aligned,
  * not shared by calls that may overlap on the GPU.  It needs no clearing.  The size
  * is 0 (workspace may be NULL) for small batches with max_seqlen <= 256 without weights.
