@@ -6,7 +6,9 @@
 // take a few per cent of the tensor pipe at full memory speed, whatever the group, so the
 // products are kept small and synchronous and the design goes into the loads.
 //
-// Split.  Keys come in tiles of about 32 KB (128 keys of 64 columns, 64 of 128, 32 above).
+// Split.  Keys come in tiles of about 32 KB (128 keys of 64 columns, 64 of
+// up to 128, 32 above; rows of 65 to 96 columns take 192 bytes and four stages: 64 sequences
+// of 4000 keys, 8 heads of 96, 127 us against 136 with 256 bytes and three, of 80 119 and 125).
 // All tiles of all (sequence, head) segments form one line, cut into equal runs, one per
 // resident block: ragged lengths balance by themselves, and one long sequence uses every
 // SM.  Where the blocks divide among the heads, every head has a line of its own instead,
@@ -57,14 +59,14 @@ constexpr int kMaxRuns = 320;
 // 8.2 for one of 128 keys; but 2048 segments of 63 to 256 keys 51.4 us against 41.2).
 constexpr int kWholeKeys = 256;
 
-constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp == 128 ? 6 : 5); }
+constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp <= 128 ? 6 : 5); }
 
 template <int DP>
 struct Cfg {
   static constexpr int kTile = 1 << tile_log2(DP);       // keys of a tile
   static constexpr int kPitch = DP * 2;
   static constexpr int kStageBytes = 2 * kTile * kPitch;
-  static constexpr int kStages = DP == 192 ? 4 : 3;      // 96 KB
+  static constexpr int kStages = DP == 96 || DP == 192 ? 4 : 3;  // 96 KB
   static constexpr int kSlots = kStages + 2;             // descriptors
   static constexpr int kPlan = kTile > kCopy ? kTile / kCopy : 1;  // keys a copying thread looks up
   static constexpr int kSplits = kTile == 32 ? 2 : 1;    // warps that share a key's logits
@@ -196,6 +198,13 @@ __device__ __forceinline__ float* partial(const DecodeParams& p, int block, int 
   return p.parts + (static_cast<int64_t>(block) * 2 + second) * p.part_stride;
 }
 
+// What a row's chunk numbers are permuted by (exclusive or): eight rows, four of them where a
+// row is one and a half times 128 bytes and its neighbours start 64 bytes apart.
+template <int DP>
+__host__ __device__ constexpr int perm(int row) {
+  return DP % 64 == 0 ? row & 7 : (row >> 1) & 3;
+}
+
 // Copies the rows of a tile, kLanes of the copying threads to a row.  `rows`: the addresses
 // of each key's rows of k and of v.
 // Addresses are read eight at a time before their copies are issued: a copy writes shared
@@ -203,13 +212,13 @@ __device__ __forceinline__ float* partial(const DecodeParams& p, int block, int 
 template <int DP>
 __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
                                           int idx, const DecodeParams& p, uint64_t policy) {
-  constexpr int kLanes = DP == 64 ? 8 : (DP == 128 ? 16 : 32), kStep = kCopy / kLanes;
+  constexpr int kLanes = DP == 64 ? 8 : (DP <= 128 ? 16 : 32), kStep = kCopy / kLanes;
   constexpr int kTile = Cfg<DP>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
   const int c = idx % kLanes, r0 = idx / kLanes;
   if (c >= p.chunks) return;
   rows += r0;
-  dst += r0 * kPitch + ((c ^ r0) << 4);  // r0 < kStep, and kStep divides 8
-  auto at = [&](int i) { return (dst ^ (((i * kStep) & 7) << 4)) + i * kStep * kPitch; };
+  dst += r0 * kPitch + ((c ^ perm<DP>(r0)) << 4);  // r0 < kStep, and kStep divides 8
+  auto at = [&](int i) { return (dst ^ (perm<DP>(i * kStep) << 4)) + i * kStep * kPitch; };
   uint32_t all = valid[0];
 #pragma unroll
   for (int i = 1; i < kTile / 32; ++i) all &= valid[i];
@@ -282,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   constexpr int kSteps = DP / 16 / C::kSplits;  // k-steps of Q K^T of a warp
   constexpr int kGroups = kTile == 128 ? 2 : 1; // groups of 8 keys of a warp
   constexpr int kPer = kTile / 32;      // keys of a lane in the softmax
-  constexpr int kCols = DP / kWarps;    // columns of O of a warp
+  constexpr int kCols = DP == 96 ? 16 : DP / kWarps;  // columns of O of a warp (of 96 two warps have none)
   constexpr int kNt = kCols / 8;        // their n-tiles
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_sums[kThreads / 32];
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   if (p.head_dim < DP) {
     const int c0 = p.head_dim / 8, nc = DP / 8 - c0;
     for (int i = tid; i < S * 2 * kTile * nc; i += kThreads)
-      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ ((i / nc) & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ perm<DP>(i / nc)) << 4)) = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
 
@@ -482,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   float o[kNt][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // softmax of rows `warp` and `warp` + 8
   const int row0 = lane >> 2, col2 = (lane & 3) * 2;
+  const bool has_columns = DP % (kCols * kWarps) == 0 || warp * kCols < DP;
   const int group8 = C::kSplits == 2 ? warp & 3 : warp, split = C::kSplits == 2 ? warp >> 2 : 0;
   int b = 0, h0 = 0, hn = 0;  // of the segment: sequence, first query head and their number
   __syncthreads();
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
       for (int k = 0; k < kSteps; k += 2) {
         uint32_t kf[4];
-        ldsm4(a + (((split * kSteps * 2 + k * 2 + (lane >> 3)) ^ (lane & 7)) << 4), kf);
+        ldsm4(a + (((split * kSteps * 2 + k * 2 + (lane >> 3)) ^ perm<DP>(lane & 7)) << 4), kf);
         mma16816<T>(s, qf[k], kf[0], kf[1]);
         mma16816<T>(s1, qf[k + 1], kf[2], kf[3]);
       }
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     compute_barrier();
 
     // ---- O += P V for this warp's columns
-    {
+    if (has_columns) {
       const float c0 = s_scale[row0], c1 = s_scale[row0 + 8];
 #pragma unroll
       for (int n = 0; n < kNt; ++n) {
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
           uint32_t vf[4];
-          ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ (lane & 7)) << 4), vf);
+          ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
           mma16816<T>(o[n], p0, vf[0], vf[1]);
           mma16816<T>(o[n], p1, vf[2], vf[3]);
         }
@@ -641,8 +651,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         } else {
 #pragma unroll
           for (int n = 0; n < kNt; ++n)
-            *reinterpret_cast<float2*>(part + row * DP + warp * kCols + n * 8 + col2) =
-                make_float2(o[n][r * 2], o[n][r * 2 + 1]);
+            if (has_columns)
+              *reinterpret_cast<float2*>(part + row * DP + warp * kCols + n * 8 + col2) =
+                  make_float2(o[n][r * 2], o[n][r * 2 + 1]);
           if (warp == 0 && (lane & 3) == 0) {
             part[p.part_rows * DP + row] = s_max[row];
             part[p.part_rows * DP + kMaxRows + row] = sum;
@@ -861,7 +872,7 @@ __global__ void __launch_bounds__(kJoin) weights_kernel(DecodeParams p, int bloc
   }
 }
 
-int pad_dim(int d) { return d <= 64 ? 64 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256)); }
+int pad_dim(int d) { return d <= 64 ? 64 : (d <= 96 ? 96 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256))); }
 
 // One block a segment, without partials.
 bool takes_whole(int batch, int h_k, int group, int max_seqlen, bool weights) {
@@ -918,6 +929,7 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   if (runs > 0) {
     const int r = static_cast<int>(runs);
     if (dp == 64) e = launch_main<T, 64>(p, r, stream);
+    else if (dp == 96) e = launch_main<T, 96>(p, r, stream);
     else if (dp == 128) e = launch_main<T, 128>(p, r, stream);
     else if (dp == 192) e = launch_main<T, 192>(p, r, stream);
     else e = launch_main<T, 256>(p, r, stream);

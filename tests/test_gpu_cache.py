@@ -147,6 +147,8 @@ DECODE = [
     ("bf16", [2500], 8, 1, 248, 256, False, 2000, 0.0),
     ("bf16", [6000], 8, 2, 64, 16, False, -1, 0.0),          # split over the length
     ("fp16", [1 + (i * 37) % 300 for i in range(70)], 4, 2, 32, 16, False, -1, 0.0),
+    ("bf16", [6000, 77], 12, 2, 88, 16, True, -1, 0.0),
+    ("fp16", [3, 5000, 900], 20, 10, 96, 1, False, 4000, 15.0),
 ]
 
 
