@@ -33,8 +33,11 @@
 // (With four warps that also did the copies, the chain of dependent steps of a tile took
 // 3100 cycles against 2600 for its loads.)
 //
-// P is rounded to the inputs' type for the P V product (half a step of relative error
-// on each, averaged by the sum); the sum itself, maxima and logits stay fp32.
+// P is rounded to the inputs' type for the P V product: half a step of relative error on each
+// weight.  In fp16 it is taken times 2^15 (kPScale), so that weights lose bits below 2^-29 of
+// the largest and vanish below 2^-40.  (Unscaled they vanished below 2^-25: 16383 keys beside
+// one of 2^30 times their weight and of value 0 gave O = 0 in place of 1.5e-5.)  The sum itself,
+// maxima and logits stay fp32, without the factor.
 #include <atomic>
 
 #include "cache.h"
@@ -58,6 +61,10 @@ constexpr int kMaxRuns = 320;
 // Up to this length, and while the blocks suffice, sequences are taken whole (6.2 us against
 // 8.2 for one of 128 keys; but 2048 segments of 63 to 256 keys 51.4 us against 41.2).
 constexpr int kWholeKeys = 256;
+
+// Factor of P in shared memory and of O until it is written (a power of two: exact).
+template <typename T>
+constexpr float kPScale = Pack<T>::kIsBf16 ? 1.f : 32768.f;
 
 constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp <= 128 ? 6 : 5); }
 
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       for (int i = 0; i < kPer; ++i) {
         const float e = ex2(x[i] - base);
         sum += e;
-        prow[lane + 32 * i] = static_cast<T>(e);
+        prow[lane + 32 * i] = static_cast<T>(e * kPScale<T>);
       }
       m[r] = mx;
       l[r] = l[r] * scale + sum;
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         if (row >= hn) continue;
         const float sum = s_sum[row];
         const bool none = sum == 0.f;
-        const float inv = none ? 0.f : 1.f / sum;
+        const float inv = none ? 0.f : 1.f / kPScale<T> / sum;
         if (whole) {
           T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + (h0 + row) * p.o.sh;
 #pragma unroll
@@ -653,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           for (int n = 0; n < kNt; ++n)
             if (has_columns)
               *reinterpret_cast<float2*>(part + row * DP + warp * kCols + n * 8 + col2) =
-                  make_float2(o[n][r * 2], o[n][r * 2 + 1]);
+                  make_float2(o[n][r * 2] * (1.f / kPScale<T>), o[n][r * 2 + 1] * (1.f / kPScale<T>));
           if (warp == 0 && (lane & 3) == 0) {
             part[p.part_rows * DP + row] = s_max[row];
             part[p.part_rows * DP + kMaxRows + row] = sum;
