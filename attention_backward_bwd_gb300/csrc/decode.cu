@@ -29,15 +29,20 @@
 // neither the copies nor ldmatrix meet a bank conflict (with padded rows the copies alone
 // were 4 % slower).  Of a tile the compute warps first take the logits of 8 keys each (16
 // of 128; of 32 keys, 8 keys over half of the columns), then the softmax of two rows each,
-// a lane a key, then an eighth of the columns of O over all keys, so they never join O.
+// a lane a key or two, then an eighth of the columns of O over all keys, so they never join O.
 // (With four warps that also did the copies, the chain of dependent steps of a tile took
 // 3100 cycles against 2600 for its loads.)
 //
-// P is rounded to the inputs' type for the P V product: half a step of relative error on each
-// weight.  In fp16 it is taken times 2^15 (kPScale), so that weights lose bits below 2^-29 of
-// the largest and vanish below 2^-40.  (Unscaled they vanished below 2^-25: 16383 keys beside
-// one of 2^30 times their weight and of value 0 gave O = 0 in place of 1.5e-5.)  The sum itself,
-// maxima and logits stay fp32, without the factor.
+// P enters the P V product as two numbers of the inputs' type, its rounded value and the rounded
+// remainder, so that the weights are right to 2^-16 in bf16 and 2^-22 in fp16 and O's error is
+// that of its own rounding.  (With the rounded value alone it was 1.3 to 1.4 times that.)  Groups
+// of up to 8 query heads have the remainders in the product's rows 8 to 15, which are empty
+// there, and take the same time (8 heads of 128, 64 sequences of 4000 keys, 173 us); larger ones
+// take a second product (4 heads of 64 with 16 query heads each 74.8 us against 64.6, with 20
+// 128 against 108).  In fp16 P is taken times 2^15 (kPScale), so that its finest step
+// is 2^-39 of the largest weight.  (Unscaled, weights vanished below 2^-25: 16383 keys
+// beside one of 2^30 times their weight and of value 0 gave O = 0 in place of 1.5e-5.)  The sum
+// itself, maxima and logits stay fp32, without the factor.
 #include <atomic>
 
 #include "cache.h"
@@ -285,6 +290,12 @@ __device__ __forceinline__ void no_keys(const DecodeParams& p, int b, int hv) {
       p.lse[static_cast<int64_t>(b) * p.h_q + h0 + i] = INFINITY;
 }
 
+// O and what P's remainders add to it.  Of an infinite value a remainder of 0 or below makes
+// a NaN, where the weight itself has made the infinity that O is.
+__device__ __forceinline__ float with_rest(float o, float rest) {
+  return fabsf(rest) < INFINITY ? o + rest : o;
+}
+
 // Barrier of the compute warps.
 __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 2, %0;" ::"n"(kCompute) : "memory");
@@ -298,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   constexpr int kSteps = DP / 16 / C::kSplits;  // k-steps of Q K^T of a warp
   constexpr int kGroups = kTile == 128 ? 2 : 1; // groups of 8 keys of a warp
   constexpr int kPer = kTile / 32;      // keys of a lane in the softmax
+  constexpr int kPair = kPer > 1 ? 2 : 1;  // of them neighbours
   constexpr int kCols = DP == 96 ? 16 : DP / kWarps;  // columns of O of a warp (of 96 two warps have none)
   constexpr int kNt = kCols / 8;        // their n-tiles
   extern __shared__ __align__(128) unsigned char smem[];
@@ -501,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   const bool has_columns = DP % (kCols * kWarps) == 0 || warp * kCols < DP;
   const int group8 = C::kSplits == 2 ? warp & 3 : warp, split = C::kSplits == 2 ? warp >> 2 : 0;
   int b = 0, h0 = 0, hn = 0;  // of the segment: sequence, first query head and their number
+  bool paired = false;        // the remainders of P take the rows from 8 on
   __syncthreads();
   for (int t = 0;; ++t) {
     const TileDesc& d = desc[t % kSlots];
@@ -510,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       b = d.b;
       h0 = g * p.group + ht * kMaxRows;
       hn = min(kMaxRows, p.group - ht * kMaxRows);
+      paired = hn <= kMaxRows / 2;
       const T* q = static_cast<const T*>(p.q.ptr) + b * p.q.sb;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
@@ -552,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
     compute_barrier();
 
-    // ---- softmax of this warp's rows, a lane a key; P takes the place of the logits
+    // ---- softmax of this warp's rows; P takes the place of the logits.  A lane takes kPair
+    // neighbouring keys of every 32 * kPair.
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = warp + r * 8;
@@ -560,18 +575,33 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       float* srow = reinterpret_cast<float*>(sbuf + row * C::kSPitch);
       float x[kPer], top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        x[i] = srow[lane + 32 * i];
-        if (C::kSplits == 2)
-          x[i] += *reinterpret_cast<const float*>(sbuf + (kMaxRows + row) * C::kSPitch + (lane + 32 * i) * 4);
-        x[i] = p.softcap > 0.f ? p.cap_out * tanh_exp(x[i] * p.cap_in) : x[i] * p.scale_log2;
-        if (!((d.valid[i] >> lane) & 1u)) x[i] = -INFINITY;
-        top = fmaxf(top, x[i]);
+      for (int i = 0; i < kPer; i += kPair) {
+        const int key = kPair * lane + 32 * i;
+        if (kPair == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(srow + key);
+          x[i] = v.x;
+          x[i + kPair - 1] = v.y;
+        } else {
+          x[i] = srow[key];
+        }
+        const uint32_t valid = d.valid[key >> 5] >> (key & 31);
+#pragma unroll
+        for (int k = 0; k < kPair; ++k) {
+          float& y = x[i + k];
+          if (C::kSplits == 2) y += reinterpret_cast<const float*>(sbuf + (kMaxRows + row) * C::kSPitch)[key + k];
+          y = p.softcap > 0.f ? p.cap_out * tanh_exp(y * p.cap_in) : y * p.scale_log2;
+          if (!((valid >> k) & 1u)) y = -INFINITY;
+          top = fmaxf(top, y);
+        }
       }
       if (p.logits != nullptr) {
-        float* out = p.logits + (static_cast<int64_t>(b) * p.h_q + h0 + row) * p.logit_stride + d.rel + lane;
+        float* out = p.logits + (static_cast<int64_t>(b) * p.h_q + h0 + row) * p.logit_stride + d.rel + kPair * lane;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) out[32 * i] = x[i];
+        for (int i = 0; i < kPer; i += kPair)
+          if (kPair == 2)
+            *reinterpret_cast<float2*>(out + 32 * i) = make_float2(x[i], x[i + kPair - 1]);
+          else
+            out[32 * i] = x[i];
       }
 #pragma unroll
       for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
@@ -579,15 +609,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       const float scale = ex2(m[r] - base);
       float sum = 0.f;
       T* prow = reinterpret_cast<T*>(srow);
+      T* rest = paired ? reinterpret_cast<T*>(sbuf + (row + 8) * C::kSPitch) : prow + kTile;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float e = ex2(x[i] - base);
-        sum += e;
-        prow[lane + 32 * i] = static_cast<T>(e * kPScale<T>);
+      for (int i = 0; i < kPer; i += kPair) {
+        const int key = kPair * lane + 32 * i;
+        const float e0 = ex2(x[i] - base), e1 = kPair == 2 ? ex2(x[i + kPair - 1] - base) : 0.f;
+        sum += e0 + e1;
+        const uint32_t hi = Pack<T>::two(e0 * kPScale<T>, e1 * kPScale<T>);
+        const float2 h = Pack<T>::unpack(hi);
+        const uint32_t lo = Pack<T>::two(e0 * kPScale<T> - h.x, e1 * kPScale<T> - h.y);
+        if (kPair == 2) {
+          *reinterpret_cast<uint32_t*>(prow + key) = hi;
+          *reinterpret_cast<uint32_t*>(rest + key) = lo;
+        } else {
+          reinterpret_cast<unsigned short*>(prow)[key] = static_cast<unsigned short>(hi);
+          reinterpret_cast<unsigned short*>(rest)[key] = static_cast<unsigned short>(lo);
+        }
       }
       m[r] = mx;
       l[r] = l[r] * scale + sum;
-      if (lane == 0) s_scale[row] = scale;
+      if (lane == 0) {
+        s_scale[row] = scale;
+        if (paired) s_scale[row + 8] = scale;
+      }
     }
     compute_barrier();
 
@@ -603,23 +647,58 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
       const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16;
       const uint32_t va = kst + (kTile + lane) * kPitch;
+      if (paired) {
 #pragma unroll
-      for (int k = 0; k < kTile / 32; ++k) {
-        uint32_t p0[4], p1[4];
-        ldsm4(pa + k * 64, p0);
-        ldsm4(pa + k * 64 + 32, p1);
+        for (int k = 0; k < kTile / 32; ++k) {
+          uint32_t p0[4], p1[4];
+          ldsm4(pa + k * 64, p0);
+          ldsm4(pa + k * 64 + 32, p1);
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-          uint32_t vf[4];
-          ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
-          mma16816<T>(o[n], p0, vf[0], vf[1]);
-          mma16816<T>(o[n], p1, vf[2], vf[3]);
+          for (int n = 0; n < kNt; ++n) {
+            uint32_t vf[4];
+            ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
+            mma16816<T>(o[n], p0, vf[0], vf[1]);
+            mma16816<T>(o[n], p1, vf[2], vf[3]);
+          }
         }
+      } else {
+        float rest[kNt][4];
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rest[n][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k) {
+          uint32_t p0[4], p1[4], r0[4], r1[4];
+          ldsm4(pa + k * 64, p0);
+          ldsm4(pa + k * 64 + 32, p1);
+          ldsm4(pa + kTile * 2 + k * 64, r0);
+          ldsm4(pa + kTile * 2 + k * 64 + 32, r1);
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            uint32_t vf[4];
+            ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
+            mma16816<T>(o[n], p0, vf[0], vf[1]);
+            mma16816<T>(rest[n], r0, vf[0], vf[1]);
+            mma16816<T>(o[n], p1, vf[2], vf[3]);
+            mma16816<T>(rest[n], r1, vf[2], vf[3]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][i] = with_rest(o[n][i], rest[n][i]);
       }
     }
 
     if (d.flags & kEnd) {
       // ---- this run's part of the segment is complete
+      if (paired)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          o[n][0] = with_rest(o[n][0], o[n][2]);
+          o[n][1] = with_rest(o[n][1], o[n][3]);
+        }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float x = l[r];

@@ -1,5 +1,5 @@
-"""attn_decode where most of the softmax's weight lies on keys whose values are zero (attention
-sinks), so that the output is made of the small weights alone."""
+"""attn_decode's weights in the product with V: their precision, small ones that make up the output
+because the largest lies on a key of value zero (an attention sink), and infinite values."""
 import math
 
 import numpy as np
@@ -47,3 +47,49 @@ def test_fp16_weights_far_below_the_largest_keep_their_share(d, bits):
     off = np.abs(f64(o) - ref["o"]) - bound
     assert (off <= 0).all(), f"O is {off.max():.3e} beyond its bound, at {np.abs(ref['o']).max():.3e}"
     assert (np.abs(f64(lse) - ref["lse"]) <= bl).all()
+
+
+# of a weight that enters the product as a number of the type and its remainder in the type
+WEIGHT = {torch.float16: 2.0 ** -22, torch.bfloat16: 2.0 ** -16}
+
+
+@pytest.mark.parametrize("d", [8, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("hq,hk", [(8, 8), (16, 2), (18, 2), (32, 2), (40, 2)])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+def test_weights_are_more_precise_than_the_type(dt, hq, hk, d):
+    """O within half a step of its own, the weights' error (two roundings to the type, the
+    logits' and the exponential's) and the product's fp32 sums, 2^-22 of the magnitudes a key."""
+    lens, page = [2, 3, 5, 9, 40, 300, 3000, 1], 16
+    g = torch.Generator().manual_seed(60)
+    per = -(-max(lens) // page)
+    kc, vc = (torch.randn(len(lens) * per, page, hk, d, generator=g).to(dt) for _ in range(2))
+    table = torch.randperm(len(lens) * per, generator=g).to(torch.int32).view(-1, per)
+    q = torch.randn(len(lens), hq, d, generator=g).to(dt)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, _ = ab.attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), n, scale=0.5 / d ** 0.5)
+    ab.check_device_status()
+    for b, m in enumerate(lens):
+        rows = table[b].long()
+        k, v = (f64(c[rows].flatten(0, 1)[:m]) for c in (kc, vc))
+        ref = co.decode(f64(q[b]), k, v, 0.5 / d ** 0.5)
+        _, _, prob = decode_bounds({**ref, "vsum": np.zeros((hq, d))}, d, dt, 0.0)
+        bound = HALF_STEP[dt] * np.abs(ref["o"]) + (WEIGHT[dt] + m * 2.0 ** -22 + prob)[:, None] * ref["absv"] + \
+            2.0 ** -39 * np.repeat(np.abs(v).sum(0), hq // hk, axis=0) + SMALLEST[dt]
+        off = np.abs(f64(o[b]) - ref["o"]) - bound
+        assert (off <= 0).all(), f"length {m}: O is {off.max():.3e} beyond its bound"
+
+
+@pytest.mark.parametrize("hq", [2, 16, 20])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+def test_infinite_values_stay_infinite(dt, hq):
+    n, d, page = 500, 64, 16
+    g = torch.Generator().manual_seed(61)
+    k, v = (torch.randn(n // page + 1, page, 1, d, generator=g).to(dt) for _ in range(2))
+    v.view(-1, d)[70, 3] = float("inf")
+    v.view(-1, d)[300, 9] = -float("inf")
+    table = torch.arange(n // page + 1, dtype=torch.int32)[None]
+    o, _ = ab.attn_decode(torch.randn(1, hq, d, generator=g).to(dt).cuda(), k.cuda(), v.cuda(), table.cuda(),
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), scale=0.05)
+    assert torch.isposinf(o[0, :, 3]).all() and torch.isneginf(o[0, :, 9]).all()
+    rest = [c for c in range(d) if c not in (3, 9)]
+    assert o[0][:, rest].isfinite().all()
