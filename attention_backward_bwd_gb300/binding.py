@@ -184,6 +184,30 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _side(stream, index):
+    """``stream`` (a stream object or a handle) as a stream of device ``index`` that torch knows;
+    None for the current stream."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                     device=index)
+
+
+def _new(side, make, *args, **kw):
+    """make(*args, **kw), for a kernel on ``side`` (None: on the current stream) to write.
+
+    A block that the current stream's pool hands out may still be in use there, which only that
+    stream waits for; so the block is taken from ``side``'s, and recorded for the caller's stream,
+    which uses it afterwards."""
+    if side is None:
+        return make(*args, **kw)
+    caller = torch.cuda.current_stream(side.device)
+    with torch.cuda.stream(side):
+        t = make(*args, **kw)
+    t.record_stream(caller)
+    return t
+
+
 def _dims(q: torch.Tensor, k: torch.Tensor, cu_q, cu_k, max_q, max_k):
     if cu_q is not None:
         if q.dim() != 3 or k.dim() != 3:

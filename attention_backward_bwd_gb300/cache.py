@@ -7,7 +7,8 @@ AttnError before anything is launched.  Lengths, block tables and offsets live o
 the device and are checked there; check_device_status() reports what was bad.
 
 The calls run on the device of their tensors, on ``stream`` (default: that device's
-current stream).
+current stream).  What a call allocates itself belongs to that stream; the caller orders
+``stream`` behind the work that makes its inputs, and its later work behind ``stream``.
 """
 from __future__ import annotations
 
@@ -17,7 +18,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .binding import ATTN_BF16, ATTN_FP16, AttnError, lib
+from .binding import ATTN_BF16, ATTN_FP16, AttnError, _new, _side, lib
 
 _DTYPES = {torch.float16: ATTN_FP16, torch.bfloat16: ATTN_BF16}
 # attn_tensor, attn_paged_kv, attn_rotary and attn_opts as a C compiler lays them out
@@ -52,10 +53,8 @@ def _int32(name, value) -> int:
     return value
 
 
-def _call(fn, index, stream, made, *args):
-    """Runs fn(*args, stream) with device ``index`` current.  ``made``: tensors
-    allocated by the caller; their memory is kept from reuse until ``stream`` has
-    passed them."""
+def _call(fn, index, stream, *args):
+    """Runs fn(*args, stream) with device ``index`` current."""
     raw = _raw_stream(index) if stream is None else \
         stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if torch.cuda.current_device() == index:
@@ -65,11 +64,6 @@ def _call(fn, index, stream, made, *args):
             rc = fn(*args, raw)
     if rc != 0:
         _fail(rc)
-    if stream is not None:
-        other = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(raw, device=index)
-        for t in made:
-            t.record_stream(other)
 
 
 def _first(t: torch.Tensor, name: str):
@@ -167,11 +161,10 @@ def _stride3(s):
     return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
-def _output(name, out, x, sx, index, dtype, made):
+def _output(name, out, x, sx, index, dtype, side):
     """(out, its strides): allocated like x, or checked against it."""
     if out is None:
-        out = torch.empty_like(x)
-        made.append(out)
+        out = _new(side, torch.empty_like, x)
         return out, out.stride()
     so = _rows(name, out, index, dtype, len(sx))
     if out.shape != x.shape:
@@ -205,23 +198,23 @@ def attn_rope(q, k, positions, inv_freq, sections: Optional[Sequence[int]] = Non
     else:
         raise AttnError(-2, f"q must be [B, S, H, D] or packed [total, H, D], got {tuple(shape)}")
     _int32("the tokens' number", tokens)
-    made = []
+    side = _side(stream, index)
     sq = _rows("q", q, index, dtype, dims)
-    out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
+    out_q, so = _output("out_q", out_q, q, sq, index, dtype, side)
     hk, pk, pok = hq, None, None
     if k is not None:
         sk = _rows("k", k, index, dtype, dims)
         hk = k.shape[-2]
         if k.shape != (*lead, hk, d):
             raise AttnError(-2, f"q {tuple(shape)} and k {tuple(k.shape)} disagree on tokens or D")
-        out_k, sok = _output("out_k", out_k, k, sk, index, dtype, made)
+        out_k, sok = _output("out_k", out_k, k, sk, index, dtype, side)
         pk, pok = _tensor(k.data_ptr(), *_stride3(sk)), _tensor(out_k.data_ptr(), *_stride3(sok))
     elif out_k is not None:
         raise AttnError(-9, "out_k without k")
     rot = _rotary(positions, inv_freq, sections, interleaved, inverse, index, lead, tokens)
     if tokens == 0:
         return out_q, out_k
-    _call(lib().attn_rope, index, stream, made, _tensor(q.data_ptr(), *_stride3(sq)), pk,
+    _call(lib().attn_rope, index, stream, _tensor(q.data_ptr(), *_stride3(sq)), pk,
           _tensor(out_q.data_ptr(), *_stride3(so)), pok, dt, batch, seqlen, hq, hk, d, rot)
     return out_q, out_k
 
@@ -261,7 +254,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
         raise AttnError(-9, "positions and inv_freq go together")
     rot = None if positions is None else \
         _rotary(positions, inv_freq, sections, interleaved, False, index, (tokens,), tokens)
-    made = []
+    side = _side(stream, index)
     q_arg = oq_arg = None
     hq = hk
     if q is not None:
@@ -271,7 +264,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
         hq = q.shape[1]
         if q.shape != (tokens, hq, d):
             raise AttnError(-2, f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree on tokens or D")
-        out_q, so = _output("out_q", out_q, q, sq, index, dtype, made)
+        out_q, so = _output("out_q", out_q, q, sq, index, dtype, side)
         q_arg = _tensor(q.data_ptr(), 0, sq[0], sq[1])
         oq_arg = _tensor(out_q.data_ptr(), 0, so[0], so[1])
     elif out_q is not None:
@@ -283,7 +276,7 @@ def attn_cache_append(k, v, k_cache, v_cache, block_table, seqlens, cu_seqlens=N
         sp, width = _state("slot_positions", slot_positions, index, _I32, batch, hk, 1)
     if tokens == 0:
         return out_q
-    _call(lib().attn_cache_append, index, stream, made, q_arg, oq_arg,
+    _call(lib().attn_cache_append, index, stream, q_arg, oq_arg,
           _tensor(k.data_ptr(), 0, sk[0], sk[1]), _tensor(v.data_ptr(), 0, sv[0], sv[1]), dt,
           tokens, batch, hq, hk, d, cache, lens, cu, rot, sp, width, _ints("seen", seen, index, batch))
     return out_q
@@ -302,17 +295,17 @@ def alloc_decode_workspace(q, k_cache, max_seqlen: int, weights: bool = False) -
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
-def _workspace(workspace, need, like, index, made):
-    """(pointer, bytes) of the caller's workspace or of a new one (none if none is needed)."""
+def _workspace(workspace, need, like, index, side):
+    """(pointer, bytes, tensor) of the caller's workspace or of a new one (none if none is needed),
+    which the caller holds until its call is queued."""
     if workspace is None:
         if need == 0:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        made.append(workspace)
+            return None, 0, None
+        workspace = _new(side, torch.empty, need, dtype=torch.uint8, device=like.device)
     elif workspace.get_device() != index or workspace.dtype is not torch.uint8 or \
             not workspace.is_contiguous():
         raise AttnError(-9, f"workspace must be a contiguous uint8 tensor on cuda:{index}")
-    return workspace.data_ptr(), workspace.numel()
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[int] = None,
@@ -337,11 +330,10 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
         raise AttnError(-2, f"q {tuple(q.shape)} does not fit a cache {tuple(k_cache.shape)}")
     lens = _ints("seqlens", seqlens, index, batch)
     max_seqlen = _int32("max_seqlen", slots if max_seqlen is None else max_seqlen)
-    made = []
-    out, so = _output("out", out, q, sq, index, dtype, made)
+    side = _side(stream, index)
+    out, so = _output("out", out, q, sq, index, dtype, side)
     if lse is None:
-        lse = torch.empty((batch, hq), dtype=_F32, device=q.device)
-        made.append(lse)
+        lse = _new(side, torch.empty, (batch, hq), dtype=_F32, device=q.device)
     elif lse.get_device() != index or lse.dtype is not _F32 or lse.shape != (batch, hq) or \
             not lse.is_contiguous():
         raise AttnError(-2, f"lse must be a contiguous float32 tensor {(batch, hq)} on cuda:{index}")
@@ -358,13 +350,13 @@ def attn_decode(q, k_cache, v_cache, block_table, seqlens, max_seqlen: Optional[
         raise AttnError(-9, "weights_out without weights")
     if batch == 0:
         return out, lse
-    ws, size = _workspace(workspace, decode_workspace_size(batch, hq, hk, d, max_seqlen, w_in is not None),
-                          q, index, made)
+    ws, size, _held = _workspace(workspace, decode_workspace_size(batch, hq, hk, d, max_seqlen, w_in is not None),
+                                 q, index, side)
     opts = None
     if window is not None or softcap:
         left, right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
         opts = _pack(_OPTS, left, right, float(softcap or 0.0), 0, 0)
-    _call(lib().attn_decode, index, stream, made, _tensor(q.data_ptr(), sq[0], 0, sq[1]),
+    _call(lib().attn_decode, index, stream, _tensor(q.data_ptr(), sq[0], 0, sq[1]),
           _tensor(out.data_ptr(), so[0], 0, so[1]), lse.data_ptr(), dt, batch, hq, hk, d,
           d ** -0.5 if scale is None else float(scale), cache, lens, max_seqlen, opts, w_in, w_out,
           width, ws, size)
@@ -421,15 +413,14 @@ def attn_cache_evict(k_cache, v_cache, block_table, seqlens, weights, budget: in
         raise AttnError(-9, "positions_out without slot_positions")
     if len(widths) != 1:
         raise AttnError(-2, "weights, slot_positions and their outputs must have the same shape")
-    made = []
+    side = _side(stream, index)
     if seqlens_out is None:
-        seqlens_out = torch.empty_like(seqlens)
-        made.append(seqlens_out)
+        seqlens_out = _new(side, torch.empty_like, seqlens)
     out = _ints("seqlens_out", seqlens_out, index, batch)
     if batch == 0:
         return seqlens_out, weights_out, positions_out
-    ws, size = _workspace(workspace, evict_workspace_size(batch, hk, budget, max_seqlen), k_cache,
-                          index, made)
-    _call(lib().attn_cache_evict, index, stream, made, cache, dt, batch, hk, d, lens, out, max_seqlen,
+    ws, size, _held = _workspace(workspace, evict_workspace_size(batch, hk, budget, max_seqlen), k_cache,
+                                 index, side)
+    _call(lib().attn_cache_evict, index, stream, cache, dt, batch, hk, d, lens, out, max_seqlen,
           budget, recent, _ints("seen", seen, index, batch), w_in, w_out, p_in, p_out, width, ws, size)
     return seqlens_out, weights_out, positions_out

@@ -1,0 +1,217 @@
+"""Buffers that a call allocates while ``stream`` names another stream than the current one.
+
+The allocator hands a block out again as soon as its last use has been queued on the stream that
+the block belongs to.  A block of the current stream that another stream writes at once may
+still be in use; so whatever a call allocates has to belong to the stream that runs it, and what
+it returns has to be recorded on the caller's.  Shown here on the CPU with stand-ins for the
+tensors, the allocator and the library; the test on the GPU looks at the blocks themselves.
+"""
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import attention_backward_bwd_gb300 as ab
+from attention_backward_bwd_gb300 import binding, cache
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+        self.device = "cuda:0"
+
+
+class FakeTensor:
+    """What the bindings look at of a CUDA tensor."""
+
+    is_cuda, device = True, SimpleNamespace(type="cuda")
+
+    def __init__(self, shape, dtype=torch.float16, owner=None):
+        self.shape, self.dtype, self.owner, self.seen_by = tuple(shape), dtype, owner, []
+
+    def stride(self, i=None):
+        s = [1] * len(self.shape)
+        for k in range(len(s) - 2, -1, -1):
+            s[k] = s[k + 1] * self.shape[k + 1]
+        return tuple(s) if i is None else s[i]
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for x in self.shape:
+            n *= x
+        return n
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def is_contiguous(self):
+        return True
+
+    def record_stream(self, stream):
+        self.seen_by.append(stream.cuda_stream)
+
+
+class FakeTorch:
+    """torch, with streams and an allocator of its own."""
+
+    def __init__(self):
+        self.made, self.now = [], FakeStream(7)
+        self.cuda = SimpleNamespace(
+            Stream=FakeStream, ExternalStream=lambda h, device=None: FakeStream(h), stream=self._stream,
+            current_stream=lambda device=None: self.now, current_device=lambda: 0,
+            is_available=lambda: False)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    @contextlib.contextmanager
+    def _stream(self, s):
+        before, self.now = self.now, s
+        yield
+        self.now = before
+
+    def _new(self, shape, dtype):
+        t = FakeTensor(shape, dtype, self.now.cuda_stream)
+        self.made.append(t)
+        return t
+
+    def empty(self, *shape, dtype=None, device=None):
+        return self._new(shape[0] if isinstance(shape[0], (tuple, list)) else shape, dtype)
+
+    def empty_like(self, t):
+        return self._new(t.shape, t.dtype)
+
+
+class FakeLib:
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 1024
+
+        def call(*a):
+            s = a[-1]
+            self.streams.append(s)
+            return 0
+        return call
+
+
+I32, F32 = torch.int32, torch.float32
+
+
+def _rope(**kw):
+    q = FakeTensor((6, 2, 64))
+    return ab.attn_rope(q, q, FakeTensor((6,), I32), FakeTensor((32,), F32), **kw)
+
+
+def _append(**kw):
+    x, c = FakeTensor((3, 2, 64)), FakeTensor((9, 16, 2, 64))
+    return (ab.attn_cache_append(x, x, c, c, FakeTensor((3, 3), I32), FakeTensor((3,), I32), q=x,
+                                 positions=FakeTensor((3,), I32), inv_freq=FakeTensor((32,), F32), **kw),)
+
+
+def _decode(**kw):
+    c = FakeTensor((90, 16, 2, 64))
+    return ab.attn_decode(FakeTensor((3, 4, 64)), c, c, FakeTensor((3, 30), I32), FakeTensor((3,), I32), **kw)
+
+
+def _evict(**kw):
+    c = FakeTensor((9, 16, 2, 64))
+    return ab.attn_cache_evict(c, c, FakeTensor((3, 3), I32), FakeTensor((3,), I32), FakeTensor((3, 2, 48), F32),
+                               16, **kw)[:1]
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    t, lib = FakeTorch(), FakeLib()
+    for m in (binding, cache):
+        monkeypatch.setattr(m, "torch", t)
+        monkeypatch.setattr(m, "lib", lambda: lib)
+    monkeypatch.setattr(cache, "_raw_stream", lambda index: t.now.cuda_stream)
+    for f in (cache.decode_workspace_size, cache.evict_workspace_size):
+        f.cache_clear()
+    yield t, lib
+    for f in (cache.decode_workspace_size, cache.evict_workspace_size):
+        f.cache_clear()
+
+
+@pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("call,allocated", [(_rope, 2), (_append, 1), (_decode, 3), (_evict, 2)])
+def test_buffers_belong_to_the_stream_that_runs_the_call(fake, call, allocated, as_handle):
+    t, lib = fake
+    out = call(stream=99 if as_handle else FakeStream(99))
+    assert lib.streams == [99] and t.now.cuda_stream == 7
+    assert [x.owner for x in t.made] == [99] * allocated
+    for x in out:
+        assert 7 in x.seen_by  # the caller's stream reads it later
+
+
+@pytest.mark.parametrize("call,allocated", [(_rope, 2), (_append, 1), (_decode, 3), (_evict, 2)])
+def test_buffers_of_calls_on_the_current_stream(fake, call, allocated):
+    t, lib = fake
+    call()
+    assert lib.streams == [7] and [x.owner for x in t.made] == [7] * allocated
+
+
+# ------------------------------------------------------------------ on the GPU
+
+def _busy_block(nbytes, stream):
+    """A block of ``nbytes`` that the current stream still has to read: its address, where it is
+    copied to and what it holds.  It was given back to the allocator already."""
+    block = torch.full((nbytes,), 77, dtype=torch.uint8, device="cuda")
+    copy = torch.empty_like(block)
+    stream.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    copy.copy_(block)
+    at = block.data_ptr()
+    del block
+    return at, copy
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["rope", "append", "decode", "evict"])
+def test_a_block_in_use_is_not_taken_by_another_stream(call):
+    batch, hq, hk, d, page, n, dt = 8, 16, 4, 128, 16, 2048, torch.float16
+    per = n // page
+    side = torch.cuda.Stream()
+    kc, vc = (torch.randn(batch * per, page, hk, d, device="cuda").to(dt) for _ in range(2))
+    table = torch.arange(batch * per, dtype=torch.int32, device="cuda").view(batch, per)
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    x = torch.randn(n, hk, d, device="cuda").to(dt)
+    pos, inv = torch.arange(n, dtype=torch.int32, device="cuda"), torch.rand(d // 2, device="cuda")
+    q, w = torch.randn(batch, hq, d, device="cuda").to(dt), torch.rand(batch, hk, n, device="cuda")
+    none, cu = lens * 0, torch.arange(0, n + 1, n // batch, dtype=torch.int32, device="cuda")
+    runs = {
+        "rope": lambda **kw: ab.attn_rope(x, None, pos, inv, **kw)[0],
+        "append": lambda **kw: ab.attn_cache_append(x, x, kc, vc, table, none, cu, q=x, positions=pos,
+                                                    inv_freq=inv, **kw),
+        "decode": lambda **kw: ab.attn_decode(q, kc, vc, table, lens, max_seqlen=n, **kw)[0],
+        "evict": lambda **kw: ab.attn_cache_evict(kc, vc, table, lens, w, 100, **kw)[0],
+    }
+    size = {"rope": x.numel() * 2, "append": x.numel() * 2,
+            "decode": ab.decode_workspace_size(batch, hq, hk, d, n),
+            "evict": ab.evict_workspace_size(batch, hk, 100, n)}[call]
+    state = kc, vc, w
+    saved = [t.clone() for t in state]
+    want = [t.clone() for t in (runs[call](), *state)]
+    for t, old in zip(state, saved):
+        t.copy_(old)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    at, copy = _busy_block(size, side)
+    got = runs[call](stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    ab.check_device_status()
+    assert (copy == 77).all()
+    assert all(torch.equal(x, y) for x, y in zip((got, *state), want))
+    if call in ("rope", "append"):
+        assert got.data_ptr() != at
