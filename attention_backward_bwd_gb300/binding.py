@@ -2,10 +2,10 @@
 operators of include/attn_cache.h are called from cache.py).
 
 Argument marshalling only: torch tensors are turned into pointers and element
-strides, outputs and workspace are allocated with torch (device memory), and
-every step of the computation runs in the library's CUDA kernels.  There is no
-CPU or PyTorch fallback: if the library is missing or a call fails, an
-exception is raised.
+strides, outputs and workspace are allocated with torch (device memory of the
+stream that runs the call), and every step of the computation runs in the
+library's CUDA kernels.  There is no CPU or PyTorch fallback: if the library is
+missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
@@ -304,10 +304,11 @@ def attn_fwd(q, k, v, causal: bool = False, scale: Optional[float] = None, cu_se
                    {"cu_seqlens_q": (cu_seqlens_q, b + 1), "cu_seqlens_k": (cu_seqlens_k, b + 1),
                     "seqused_q": (seqused_q, b), "seqused_k": (seqused_k, b)}, True, varlen)
     scale = d ** -0.5 if scale is None else float(scale)
-    o = torch.empty_like(q) if out is None else out
+    side = _side(stream, q.get_device())
+    o = _new(side, torch.empty_like, q) if out is None else out
     if lse is None:
         shape = (hq, sq) if varlen else (b, hq, sq)
-        lse = torch.empty(shape, dtype=torch.float32, device=q.device)
+        lse = _new(side, torch.empty, shape, dtype=torch.float32, device=q.device)
     dq_, dk_, dv_, do_ = _desc(q), _desc(k), _desc(v), _desc(o)
     args = [ctypes.byref(dq_), ctypes.byref(dk_), ctypes.byref(dv_), ctypes.byref(do_), _ptr(lse),
             _dtype_code(q), b, sq, sk, hq, hk, d, scale, int(bool(causal)), _ptr(cu_seqlens_q),
@@ -375,11 +376,12 @@ def attn_bwd(q, k, v, o, lse, do, causal: bool = False, scale: Optional[float] =
     if workspace is not None and not (workspace.is_cuda and workspace.device == q.device):
         raise AttnError(-9, f"workspace must be a CUDA tensor on {q.device}")
     scale = d ** -0.5 if scale is None else float(scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    side = _side(stream, q.get_device())
+    dq = _new(side, torch.empty_like, q) if dq is None else dq
+    dk = _new(side, torch.empty_like, k) if dk is None else dk
+    dv = _new(side, torch.empty_like, v) if dv is None else dv
     if workspace is None:
-        workspace = alloc_workspace(q, cu_seqlens_q, deterministic)
+        workspace = _new(side, alloc_workspace, q, cu_seqlens_q, deterministic)
     descs = [_desc(t) for t in (q, k, v, o)]
     d_do, d_dq, d_dk, d_dv = _desc(do), _desc(dq), _desc(dk), _desc(dv)
     args = [*(ctypes.byref(x) for x in descs), _ptr(lse), ctypes.byref(d_do), ctypes.byref(d_dq),
@@ -428,8 +430,9 @@ def attn_bwd_host(q, k, v, o, lse, do, dq=None, dk=None, dv=None, causal: bool =
     dv = torch.empty(v.shape, dtype=v.dtype, pin_memory=pin) if dv is None else dv
     need = host_buffer_size(b, sq, sk, hq, hk, d, chunks)
     if device_buffer is None:
-        device_buffer = torch.empty(max(need, 256), dtype=torch.uint8,
-                                    device=device if device is not None else "cuda")
+        device = torch.device("cuda" if device is None else device)
+        device_buffer = _new(_side(stream, device.index), torch.empty, max(need, 256),
+                             dtype=torch.uint8, device=device)
     descs = [_desc(t) for t in (q, k, v, o)]
     d_do, d_dq, d_dk, d_dv = _desc(do), _desc(dq), _desc(dk), _desc(dv)
     opts = _opts(window, softcap)
@@ -470,8 +473,9 @@ def attn_bwd_host_varlen(q, k, v, o, lse, do, cu_seqlens_q, cu_seqlens_k, dq=Non
     if need == 0:
         raise AttnError(-9, L.attn_last_error().decode() or "invalid varlen arguments")
     if device_buffer is None:
-        device_buffer = torch.empty(need, dtype=torch.uint8,
-                                    device=device if device is not None else "cuda")
+        device = torch.device("cuda" if device is None else device)
+        device_buffer = _new(_side(stream, device.index), torch.empty, need, dtype=torch.uint8,
+                             device=device)
     descs = [_desc(t) for t in (q, k, v, o)]
     d_do, d_dq, d_dk, d_dv = _desc(do), _desc(dq), _desc(dk), _desc(dv)
     opts = _opts(window, softcap)

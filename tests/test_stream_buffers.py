@@ -82,8 +82,11 @@ class FakeTorch:
         self.made.append(t)
         return t
 
-    def empty(self, *shape, dtype=None, device=None):
-        return self._new(shape[0] if isinstance(shape[0], (tuple, list)) else shape, dtype)
+    def empty(self, *shape, dtype=None, device=None, pin_memory=None):
+        shape = tuple(shape[0]) if isinstance(shape[0], (tuple, list)) else shape
+        if pin_memory is not None:  # host memory
+            return torch.empty(shape, dtype=dtype)
+        return self._new(shape, dtype)
 
     def empty_like(self, t):
         return self._new(t.shape, t.dtype)
@@ -129,6 +132,28 @@ def _evict(**kw):
                                16, **kw)[:1]
 
 
+def _fwd(**kw):
+    q = FakeTensor((2, 64, 4, 64))
+    return ab.attn_fwd(q, q, q, **kw)
+
+
+def _bwd(**kw):
+    q, k = FakeTensor((2, 64, 4, 64)), FakeTensor((2, 64, 2, 64))
+    return ab.attn_bwd(q, k, k, q, FakeTensor((2, 4, 64), F32), q, **kw)
+
+
+def _bwd_host(**kw):
+    q, lse = torch.randn(2, 64, 4, 64).half(), torch.zeros(2, 4, 64)
+    ab.attn_bwd_host(q, q, q, q, lse, q, **kw)
+    return ()
+
+
+def _bwd_host_varlen(**kw):
+    q, lse, cu = torch.randn(64, 4, 64).half(), torch.zeros(4, 64), torch.tensor([0, 30, 64])
+    ab.attn_bwd_host_varlen(q, q, q, q, lse, q, cu, cu, **kw)
+    return ()
+
+
 @pytest.fixture
 def fake(monkeypatch):
     t, lib = FakeTorch(), FakeLib()
@@ -143,8 +168,13 @@ def fake(monkeypatch):
         f.cache_clear()
 
 
+# each call and how many buffers it allocates on the device
+CALLS = [(_rope, 2), (_append, 1), (_decode, 3), (_evict, 2), (_fwd, 2), (_bwd, 4), (_bwd_host, 1),
+         (_bwd_host_varlen, 1)]
+
+
 @pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
-@pytest.mark.parametrize("call,allocated", [(_rope, 2), (_append, 1), (_decode, 3), (_evict, 2)])
+@pytest.mark.parametrize("call,allocated", CALLS)
 def test_buffers_belong_to_the_stream_that_runs_the_call(fake, call, allocated, as_handle):
     t, lib = fake
     out = call(stream=99 if as_handle else FakeStream(99))
@@ -154,7 +184,7 @@ def test_buffers_belong_to_the_stream_that_runs_the_call(fake, call, allocated, 
         assert 7 in x.seen_by  # the caller's stream reads it later
 
 
-@pytest.mark.parametrize("call,allocated", [(_rope, 2), (_append, 1), (_decode, 3), (_evict, 2)])
+@pytest.mark.parametrize("call,allocated", CALLS)
 def test_buffers_of_calls_on_the_current_stream(fake, call, allocated):
     t, lib = fake
     call()
@@ -174,6 +204,29 @@ def _busy_block(nbytes, stream):
     at = block.data_ptr()
     del block
     return at, copy
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["forward", "backward"])
+def test_a_block_in_use_is_not_taken_by_training_calls(call):
+    b, n, hq, hk, d = 2, 512, 4, 2, 128
+    side = torch.cuda.Stream()
+    q, do = (torch.randn(b, n, hq, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn(b, n, hk, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    o, lse = ab.attn_fwd(q, k, v, causal=True)
+    run = {"forward": lambda **kw: ab.attn_fwd(q, k, v, causal=True, **kw),
+           "backward": lambda **kw: ab.attn_bwd(q, k, v, o, lse, do, causal=True, deterministic=True, **kw)}[call]
+    want = [t.clone() for t in run()]
+    size = q.numel() * 2 if call == "forward" else ab.workspace_size(b, n, hq, d, True)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    _, copy = _busy_block(size, side)
+    got = run(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    ab.check_device_status()
+    assert (copy == 77).all()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 @pytest.mark.gpu
