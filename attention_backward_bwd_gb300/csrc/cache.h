@@ -28,6 +28,10 @@ constexpr unsigned int kBadLength = 0xB0000011u;   // seqlens / slots out of ran
 constexpr unsigned int kBadPage = 0xB0000012u;     // block_table entry outside [0, num_pages)
 constexpr unsigned int kBadOffsets = 0xB0000013u;  // cu_seqlens of an append
 
+// Longest sequence of a decode or an eviction.  Their kernels count slots in 32 bits and step past
+// the last one by up to 8 * 512 slots (evict.cu: a head's threads) or a tile.
+constexpr int kMaxLength = INT32_MAX - 8191;
+
 struct PagedArg {
   TensorArg k, v;  // sb: page, ss: slot, sh: head
   const int* table;

@@ -69,6 +69,14 @@ int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out) {
   return ATTN_OK;
 }
 
+int check_length(const attn_paged_kv* c, int max_seqlen) {
+  if (max_seqlen < 0 || max_seqlen > static_cast<int64_t>(c->max_pages) * c->page_size)
+    return fail(ATTN_ERR_ARG, "max_seqlen (%d) must lie in [0, max_pages * page_size]", max_seqlen);
+  if (max_seqlen > kMaxLength)
+    return fail(ATTN_ERR_ARG, "max_seqlen (%d) must be at most 2^31 - 8192", max_seqlen);
+  return ATTN_OK;
+}
+
 int check_rotary(const attn_rotary* r, int64_t tokens, int head_dim, RotaryArg* out) {
   if (r->n_freq < 1 || 2 * r->n_freq > head_dim)
     return fail(ATTN_ERR_SHAPE, "n_freq must lie in [1, head_dim / 2 = %d], got %d", head_dim / 2,
@@ -237,7 +245,8 @@ int attn_cache_append(const attn_tensor* q, const attn_tensor* oq, const attn_te
 
 size_t attn_decode_workspace_size(int batch, int h_q, int h_k, int head_dim, int max_seqlen,
                                   int with_weights) {
-  if (batch <= 0 || h_k <= 0 || h_q <= 0 || h_q % h_k != 0 || head_dim <= 0 || max_seqlen < 0)
+  if (batch <= 0 || h_k <= 0 || h_q <= 0 || h_q % h_k != 0 || head_dim <= 0 || max_seqlen < 0 ||
+      max_seqlen > kMaxLength)
     return 0;
   return decode_ws(batch, h_q, h_k, head_dim, max_seqlen, with_weights != 0).total;
 }
@@ -257,9 +266,7 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = check_cache(cache, batch, h_k, &p.cache))) return rc;
-  if (max_seqlen < 0 ||
-      max_seqlen > static_cast<int64_t>(cache->max_pages) * cache->page_size)
-    return fail(ATTN_ERR_ARG, "max_seqlen (%d) must lie in [0, max_pages * page_size]", max_seqlen);
+  if ((rc = check_length(cache, max_seqlen))) return rc;
   if ((rc = check_rows(q, "q", batch, 1, h_q))) return rc;
   if ((rc = check_rows(o, "o", batch, 1, h_q))) return rc;
   if (seqlens == nullptr) return fail(ATTN_ERR_NULL, "seqlens is NULL");
@@ -301,7 +308,7 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
 }
 
 size_t attn_cache_evict_workspace_size(int batch, int h_k, int budget, int max_seqlen) {
-  if (batch <= 0 || h_k <= 0 || budget <= 0 || max_seqlen < 0) return 0;
+  if (batch <= 0 || h_k <= 0 || budget <= 0 || max_seqlen < 0 || max_seqlen > kMaxLength) return 0;
   return evict_ws(batch, h_k, budget, max_seqlen).total;
 }
 
@@ -316,9 +323,7 @@ int attn_cache_evict(const attn_paged_kv* cache, int dtype, int batch, int h_k, 
   EvictParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = check_cache(cache, batch, h_k, &p.cache))) return rc;
-  if (max_seqlen < 0 ||
-      max_seqlen > static_cast<int64_t>(cache->max_pages) * cache->page_size)
-    return fail(ATTN_ERR_ARG, "max_seqlen (%d) must lie in [0, max_pages * page_size]", max_seqlen);
+  if ((rc = check_length(cache, max_seqlen))) return rc;
   if (budget <= 0 || recent < 0 || recent > budget)
     return fail(ATTN_ERR_ARG, "budget (%d) must be positive and recent (%d) in [0, budget]", budget,
                 recent);

@@ -1010,7 +1010,6 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     runs = p.batch * heads;
     p.lines = 1;
   }
-  if (runs > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (runs > 0) {
     const int r = static_cast<int>(runs);

@@ -117,8 +117,8 @@ int attn_cache_append(const attn_tensor* q, const attn_tensor* oq, const attn_te
  * with weights_stride >= max_seqlen: weights_out[b][g][j] = weights_in[b][g][j]
  * + the sum over the group's query heads of softmax(s)_j, for j < seqlens[b];
  * further entries are left as they were.  They may be the same array.
- * max_seqlen: bound on seqlens, at most max_pages * page_size (the logits kept for the
- * weights make the workspace grow with it).
+ * max_seqlen: bound on seqlens, at most max_pages * page_size and 2^31 - 8192 (the logits
+ * kept for the weights make the workspace grow with it).
  * workspace: at least attn_decode_workspace_size(...) bytes, 256-byte aligned,
  * not shared by calls that may overlap on the GPU.  It needs no clearing.  The size
  * is 0 (workspace may be NULL) for small batches with max_seqlen <= 256 without weights.
@@ -149,8 +149,8 @@ int attn_decode(const attn_tensor* q, const attn_tensor* o, float* lse, int dtyp
  * the inputs themselves, but seqlens_out must overlap neither seqlens nor seen.
  * The state arrays are [batch][H_k][state_stride], state_stride >= max_seqlen.
  * positions_in and positions_out are given both or neither; recent > 0 needs
- * them and seen.  0 < budget, 0 <= recent <= budget.  A sequence whose
- * length is negative or above max_seqlen is left as it is, with
+ * them and seen.  0 < budget, 0 <= recent <= budget; max_seqlen as in attn_decode.
+ * A sequence whose length is negative or above max_seqlen is left as it is, with
  * seqlens_out[b] = 0, and reported; a row whose page is bad is not copied.
  * Pages from ceil(budget / page_size) on are free for the caller afterwards.
  */

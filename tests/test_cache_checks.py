@@ -211,3 +211,19 @@ def test_integers_beyond_32_bits_are_refused(lib):
         assert _code(ab.decode_workspace_size, 4, 32, 8, 128, bad) == ARG
         assert _code(ab.evict_workspace_size, 4, 8, bad, 100) == ARG
     assert binding_cache._int32("x", 2**31 - 1) == 2**31 - 1
+
+
+def test_lengths_next_to_2_to_the_31_are_refused(lib):
+    """Tiles and runs of slots are counted in 32 bits: from 2^31 - 8191 on they could pass them."""
+    last, wide = 2**31 - 8192, paged(size=1, per=2**31 - 1, ts=2**31 - 1)
+    for most in (last + 1, 2**31 - 64, 2**31 - 1):
+        assert decode(lib, c=wide, most=most, ws=None) == ARG, most
+        assert decode(lib, c=wide, most=most, wi=P, wo=P, width=2**31, ws=None) == ARG, most
+        assert evict(lib, c=wide, most=most, width=2**31, ws=None) == ARG, most
+        assert lib.attn_decode_workspace_size(1, 1, 1, 64, most, 1) == 0
+        assert lib.attn_cache_evict_workspace_size(1, 1, 100, most) == 0
+    # the longest one allowed is refused for the next reason, and its workspace holds its logits
+    assert decode(lib, c=wide, most=last, ws=None) == WS
+    assert evict(lib, c=wide, most=last, width=2**31, ws=None) == WS
+    assert lib.attn_decode_workspace_size(1, 1, 1, 64, last, 1) >= 4 * last
+    assert lib.attn_cache_evict_workspace_size(1, 1, 2**30, last) >= 8 * (last - 2**30)

@@ -93,3 +93,29 @@ def test_infinite_values_stay_infinite(dt, hq):
     assert torch.isposinf(o[0, :, 3]).all() and torch.isneginf(o[0, :, 9]).all()
     rest = [c for c in range(d) if c not in (3, 9)]
     assert o[0][:, rest].isfinite().all()
+
+
+def test_the_longest_sequence():
+    """2^31 - 8192 keys, nearly all of them on one page that the table names again and again: the
+    weights lie on the first key and on the last."""
+    n, page, d, dt = 2**31 - 8192, 4096, 8, torch.float16
+    g = torch.Generator().manual_seed(62)
+    kc = torch.full((3, page, 1, d), -6e4).to(dt).cuda()
+    vc = torch.randn(3, page, 1, d, generator=g).to(dt).cuda()
+    table = torch.zeros(2, 2**31 // page - 1, dtype=torch.int32, device="cuda")
+    last = (n - 1) // page, (n - 1) % page
+    table[0, 0], table[0, last[0]] = 1, 2
+    kc[1, 0], kc[2, last[1]] = 0.25, 0.5
+    kc[2, last[1] + 1:] = 6e4  # behind the last key
+    q = torch.ones(2, 1, d, dtype=dt, device="cuda")
+    lens = torch.tensor([n, 0], dtype=torch.int32, device="cuda")
+    o, lse = ab.attn_decode(q, kc, vc, table, lens, max_seqlen=n, scale=1.0)
+    ab.check_device_status()
+    k = np.array([[[0.25] * d], [[0.5] * d]])
+    v = np.stack([f64(vc[1, 0]), f64(vc[2, last[1]])])
+    ref = co.decode(np.ones((1, d)), k, v, 1.0)
+    _, bl, prob = decode_bounds({**ref, "vsum": np.zeros((1, d))}, d, dt, 0.0)
+    bound = HALF_STEP[dt] * np.abs(ref["o"]) + (WEIGHT[dt] + 2.0 ** -20 + prob)[:, None] * ref["absv"]
+    assert (np.abs(f64(o[0]) - ref["o"]) <= bound).all()
+    assert (np.abs(f64(lse[0]) - ref["lse"]) <= bl).all()
+    assert (o[1] == 0).all() and torch.isposinf(lse[1]).all()
