@@ -48,7 +48,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 // Device status words: [0] = 0 or the site of a bounded wait that gave up;
 // [1] = 0 or the code of a failed cu_seqlens validation;
-// [2] = 0 or the code of a bad length, page or offset met by a serving operator
+// [2] = 0 or one bit each for bad lengths, pages and offsets met by the serving operators
 // (reported, but it stops no later call).
 __device__ unsigned int g_device_status[3] = {0u, 0u, 0u};
 
@@ -488,26 +488,25 @@ int attn_check_device_status(attn_stream_t stream) {
   unsigned int v[3] = {0u, 0u, 0u};
   e = cudaMemcpyFromSymbol(v, g_device_status, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e, "read device status");
-  if (v[0] != 0 || v[1] != 0 || v[2] != 0) {
-    const unsigned int zero[3] = {0u, 0u, 0u};
-    e = cudaMemcpyToSymbol(g_device_status, zero, sizeof(zero));
-    if (e != cudaSuccess) return cuda_fail(e, "clear device status");
-    if (v[1] != 0) {
-      // codes 0xB0000001..4: cu_seqlens; 0xB0000005 / 6: seqused_q / seqused_k
-      const char* what = v[1] == 0xB0000005u   ? "seqused_q"
-                         : v[1] == 0xB0000006u ? "seqused_k"
-                                               : "cu_seqlens";
-      return fail(ATTN_ERR_ARG, "%s failed device-side validation (code 0x%08x)", what, v[1]);
-    }
-    if (v[0] == 0) {
-      const char* what = v[2] == kBadPage     ? "a block_table entry names no page"
-                         : v[2] == kBadLength ? "seqlens: a length or slot out of range"
-                                              : "cu_seqlens of an append";
-      return fail(ATTN_ERR_ARG, "%s (device-side check, code 0x%08x)", what, v[2]);
-    }
-    return fail(ATTN_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (site 0x%08x)", v[0]);
+  // one word a call: what else is pending stays for the next one
+  const int word = v[1] != 0 ? 1 : (v[0] != 0 ? 0 : 2);
+  if (v[word] == 0) return ATTN_OK;
+  const unsigned int zero = 0u;
+  e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero), word * sizeof(zero));
+  if (e != cudaSuccess) return cuda_fail(e, "clear device status");
+  if (word == 1) {
+    // codes 0xB0000001..4: cu_seqlens; 0xB0000005 / 6: seqused_q / seqused_k
+    const char* what = v[1] == 0xB0000005u   ? "seqused_q"
+                       : v[1] == 0xB0000006u ? "seqused_k"
+                                             : "cu_seqlens";
+    return fail(ATTN_ERR_ARG, "%s failed device-side validation (code 0x%08x)", what, v[1]);
   }
-  return ATTN_OK;
+  if (word == 2)
+    return fail(ATTN_ERR_ARG, "device-side check of a serving call:%s%s%s",
+                (v[2] & kBadPage) ? " a block_table entry names no page;" : "",
+                (v[2] & kBadLength) ? " a length or slot of seqlens is out of range;" : "",
+                (v[2] & kBadOffsets) ? " cu_seqlens of an append" : "");
+  return fail(ATTN_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (site 0x%08x)", v[0]);
 }
 
 void attn_set_wait_timeout_ns(int64_t ns) {

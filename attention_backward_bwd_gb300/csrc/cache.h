@@ -23,10 +23,10 @@ struct FastDiv {
 #endif
 };
 
-// Codes of the device status word of these operators (status_word()[2]).
-constexpr unsigned int kBadLength = 0xB0000011u;   // seqlens / slots out of range
-constexpr unsigned int kBadPage = 0xB0000012u;     // block_table entry outside [0, num_pages)
-constexpr unsigned int kBadOffsets = 0xB0000013u;  // cu_seqlens of an append
+// Bits of the device status word of these operators (status_word()[2]).
+constexpr unsigned int kBadLength = 1u;   // seqlens / slots out of range
+constexpr unsigned int kBadPage = 2u;     // block_table entry outside [0, num_pages)
+constexpr unsigned int kBadOffsets = 4u;  // cu_seqlens of an append
 
 // Longest sequence of a decode or an eviction.  Their kernels count slots in 32 bits and step past
 // the last one by up to 8 * 512 slots (evict.cu: a head's threads) or a tile.
@@ -128,9 +128,7 @@ struct DecodeWs {
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights);
 
 #ifdef __CUDACC__
-__device__ __forceinline__ void report(unsigned int* status, unsigned int code) {
-  atomicCAS(status, 0u, code);
-}
+__device__ __forceinline__ void report(unsigned int* status, unsigned int bit) { atomicOr(status, bit); }
 
 // Page and slot within it of slot j (0 <= j < max_pages * page_size) of a
 // sequence's table row; false (and reported) when the table names no page.

@@ -331,11 +331,14 @@ int attn_bwd_postprocess(const attn_tensor* q, const attn_tensor* k, const attn_
                          attn_stream_t stream);
 
 /*
- * attn_check_device_status -- synchronises `stream`, then reads and clears the
- * device status word.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (a bounded
- * wait inside a kernel gave up; attn_last_error names the wait site),
+ * attn_check_device_status -- synchronises `stream`, then reads the device
+ * status word, reports one condition and clears that one.  Returns ATTN_OK,
  * ATTN_ERR_ARG (cu_seqlens or seqused_q/k failed the device-side check;
- * attn_last_error names which) or ATTN_ERR_CUDA (the stream reported an error).
+ * attn_last_error names which), ATTN_ERR_DEVICE_TIMEOUT (a bounded wait inside
+ * a kernel gave up; attn_last_error names the wait site), ATTN_ERR_ARG for what
+ * the calls of attn_cache.h met (lengths, pages and offsets together), or
+ * ATTN_ERR_CUDA (the stream reported an error).  Where several are pending they
+ * come in this order, one a call, until ATTN_OK says that none is left.
  * The status word is one per device and stays set until this call clears it.
  * While a failed cu_seqlens / seqused check is recorded there, the kernels of
  * EVERY later varlen or seqused call on that device (any stream, any host
