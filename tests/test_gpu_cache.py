@@ -559,6 +559,46 @@ def test_evict_reports_bad_lengths_and_pages():
     assert "page" in str(e.value)
 
 
+@pytest.mark.parametrize("bad", [4, 0], ids=["source", "target"])
+def test_evict_leaves_out_the_rows_of_bad_pages_alone(bad):
+    """Rows that would come from or go to a page that does not exist stay out; every other row,
+    and all of the state, moves as it would without it."""
+    lens, hk, d, budget, page = [40, 40, 37], 2, 64, 10, 8
+    kc, vc, table = make_cache(lens, hk, d, page, torch.float16, 12)
+    rng = np.random.default_rng(2)
+    w = rng.random((3, hk, 40)).astype(np.float32)
+    pos = np.stack([[rng.permutation(40) for _ in range(hk)] for _ in lens]).astype(np.int32)
+    before = kc.clone(), vc.clone()
+    good = table.cpu().numpy().copy()
+    table[:2, bad] = torch.tensor([kc.shape[0] + 3, -1], dtype=torch.int32, device="cuda")
+    n2, w2, p2 = ab.attn_cache_evict(kc, vc, table, ints(lens), torch.from_numpy(w).cuda(), budget, 0,
+                                     torch.from_numpy(pos).cuda(), max_seqlen=40)
+    with pytest.raises(ab.AttnError) as e:
+        ab.check_device_status()
+    assert e.value.code == -9 and "page" in str(e.value)
+    ab.check_device_status()
+    assert n2.tolist() == [budget] * 3
+    want = [t.cpu().clone() for t in before]
+    moved = left_out = 0
+    for b, n in enumerate(lens):
+        for h in range(hk):
+            kept = co.keep(w[b, h, :n], None, 0, budget, 0)
+            ww, pp = w[b, h].copy(), pos[b, h].copy()
+            for a, z in co.moves(kept, budget):
+                ww[z], pp[z] = ww[a], pp[a]
+                if b < 2 and (a if bad == 4 else z) // page == bad:
+                    left_out += 1
+                    continue
+                moved += 1
+                s, t = co.slot(good[b], page, a), co.slot(good[b], page, z)
+                for x, old in zip(want, before):
+                    x[t[0], t[1], h] = old[s[0], s[1], h].cpu()
+            ww[budget:n], pp[budget:n] = 0, -1
+            assert np.array_equal(w2[b, h].cpu().numpy(), ww) and np.array_equal(p2[b, h].cpu().numpy(), pp)
+    assert moved > 0 and left_out > 0
+    assert torch.equal(kc.cpu(), want[0]) and torch.equal(vc.cpu(), want[1])
+
+
 # ------------------------------------------------------------------ together
 
 def test_serving_loop_with_eviction():
