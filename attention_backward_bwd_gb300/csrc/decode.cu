@@ -28,8 +28,9 @@
 // an SM.  The 16-byte chunks of row r lie permuted by r % 8 inside each 128 bytes, so that
 // neither the copies nor ldmatrix meet a bank conflict (with padded rows the copies alone
 // were 4 % slower).  Of a tile the compute warps first take the logits of 8 keys each (16
-// of 128; of 32 keys, 8 keys over half of the columns), then the softmax of two rows each,
-// a lane a key or two, then an eighth of the columns of O over all keys, so they never join O.
+// of 128; of 32 keys, 8 keys over half of the columns), then the softmax of one or two rows
+// each, a lane a key or two, then an eighth of the columns of O over all keys (larger groups:
+// below).
 // (With four warps that also did the copies, the chain of dependent steps of a tile took
 // 3100 cycles against 2600 for its loads.)
 //
@@ -37,12 +38,16 @@
 // remainder, so that the weights are right to 2^-16 in bf16 and 2^-22 in fp16 and O's error is
 // that of its own rounding.  (With the rounded value alone it was 1.3 to 1.4 times that.)  Groups
 // of up to 8 query heads have the remainders in the product's rows 8 to 15, which are empty
-// there, and take the same time (8 heads of 128, 64 sequences of 4000 keys, 173 us); larger ones
-// take a second product (4 heads of 64 with 16 query heads each 74.8 us against 64.6, with 20
-// 128 against 108).  In fp16 P is taken times 2^15 (kPScale), so that its finest step
-// is 2^-39 of the largest weight.  (Unscaled, weights vanished below 2^-25: 16383 keys
-// beside one of 2^30 times their weight and of value 0 gave O = 0 in place of 1.5e-5.)  The sum
-// itself, maxima and logits stay fp32, without the factor.
+// there, at no cost (64 sequences of 4000 keys, 8 heads of 128: 152 us with and without).  Larger
+// groups (kLarge) take a second product: 4 heads of 64 with 16 query heads each 61.5 us against
+// 57.3, 64 heads on one of 128 95.7 against 83.9.  There the warps read P from shared memory at
+// a rate near its limit (eight warps all of it, for their columns), so that two or four of them
+// share columns and take a part of the tile's keys each; with all keys a warp the same took
+// 68.4 and 99.7.  (Parts for the smaller groups too made heads of 80 6 % slower.)  In fp16 P is
+// taken times 2^15 (kPScale), so that its finest step is 2^-39 of the largest weight.
+// (Unscaled, weights vanished below 2^-25: 16383 keys beside one of 2^30 times their weight and
+// of value 0 gave O = 0 in place of 1.5e-5.)  The sum itself, maxima and logits stay fp32,
+// without the factor.
 #include <atomic>
 
 #include "cache.h"
@@ -73,7 +78,7 @@ constexpr float kPScale = Pack<T>::kIsBf16 ? 1.f : 32768.f;
 
 constexpr int tile_log2(int dp) { return dp == 64 ? 7 : (dp <= 128 ? 6 : 5); }
 
-template <int DP>
+template <int DP, bool kLarge>
 struct Cfg {
   static constexpr int kTile = 1 << tile_log2(DP);       // keys of a tile
   static constexpr int kPitch = DP * 2;
@@ -83,8 +88,12 @@ struct Cfg {
   static constexpr int kPlan = kTile > kCopy ? kTile / kCopy : 1;  // keys a copying thread looks up
   static constexpr int kSplits = kTile == 32 ? 2 : 1;    // warps that share a key's logits
   static constexpr int kSPitch = kTile * 4 + 16;         // bytes of a row of logits, then of P
-  static constexpr int kSmem = kStages * kStageBytes + 2 * kTile * 16 + kSlots * 48 +
-                               kSplits * kMaxRows * kSPitch + kLens * 4;
+  // warps that share columns of O, each over its part of the tile's keys
+  static constexpr int kParts = !kLarge || kTile == 32 ? 1 : kTile / 32;
+  static constexpr int kSBytes = kSplits * kMaxRows * kSPitch;
+  static constexpr int kXBytes = kParts / 2 * kMaxRows * DP * 4;  // O of half of them, in the same place
+  static constexpr int kSBuf = kSBytes > kXBytes ? kSBytes : kXBytes;
+  static constexpr int kSmem = kStages * kStageBytes + 2 * kTile * 16 + kSlots * 48 + kSBuf + kLens * 4;
 };
 
 struct __align__(16) TileDesc {
@@ -225,7 +234,7 @@ template <int DP>
 __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
                                           int idx, const DecodeParams& p, uint64_t policy) {
   constexpr int kLanes = DP == 64 ? 8 : (DP <= 128 ? 16 : 32), kStep = kCopy / kLanes;
-  constexpr int kTile = Cfg<DP>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP>::kPitch;
+  constexpr int kTile = Cfg<DP, false>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP, false>::kPitch;
   const int c = idx % kLanes, r0 = idx / kLanes;
   if (c >= p.chunks) return;
   rows += r0;
@@ -301,16 +310,19 @@ __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 2, %0;" ::"n"(kCompute) : "memory");
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kLarge>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     decode_kernel(DecodeParams p) {
-  using C = Cfg<DP>;
+  using C = Cfg<DP, kLarge>;
   constexpr int S = C::kStages, kPitch = C::kPitch, kSlots = C::kSlots, kTile = C::kTile;
   constexpr int kSteps = DP / 16 / C::kSplits;  // k-steps of Q K^T of a warp
   constexpr int kGroups = kTile == 128 ? 2 : 1; // groups of 8 keys of a warp
   constexpr int kPer = kTile / 32;      // keys of a lane in the softmax
   constexpr int kPair = kPer > 1 ? 2 : 1;  // of them neighbours
-  constexpr int kCols = DP == 96 ? 16 : DP / kWarps;  // columns of O of a warp (of 96 two warps have none)
+  constexpr int kSets = kLarge ? 2 : 1; // of 8 query heads
+  constexpr int kParts = C::kParts, kColWarps = kWarps / kParts;
+  // columns of O of a warp (of 96 two warps have none, but with parts)
+  constexpr int kCols = DP == 96 && kParts == 1 ? 16 : DP / kColWarps;
   constexpr int kNt = kCols / 8;        // their n-tiles
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_sums[kThreads / 32];
@@ -320,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   longlong2* rows = reinterpret_cast<longlong2*>(ring + S * C::kStageBytes);  // of two tiles
   TileDesc* desc = reinterpret_cast<TileDesc*>(rows + 2 * kTile);
   unsigned char* sbuf = reinterpret_cast<unsigned char*>(desc + kSlots);      // logits, then P
-  int* lens = reinterpret_cast<int*>(sbuf + C::kSplits * kMaxRows * C::kSPitch);
+  int* lens = reinterpret_cast<int*>(sbuf + C::kSBuf);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hv_n = p.h_k * p.head_tiles;
@@ -510,10 +522,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   float o[kNt][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // softmax of rows `warp` and `warp` + 8
   const int row0 = lane >> 2, col2 = (lane & 3) * 2;
-  const bool has_columns = DP % (kCols * kWarps) == 0 || warp * kCols < DP;
+  const int cw = warp % kColWarps, part_of = warp / kColWarps;
+  const bool has_columns = DP % (kCols * kColWarps) == 0 || cw * kCols < DP;
   const int group8 = C::kSplits == 2 ? warp & 3 : warp, split = C::kSplits == 2 ? warp >> 2 : 0;
   int b = 0, h0 = 0, hn = 0;  // of the segment: sequence, first query head and their number
-  bool paired = false;        // the remainders of P take the rows from 8 on
   __syncthreads();
   for (int t = 0;; ++t) {
     const TileDesc& d = desc[t % kSlots];
@@ -523,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       b = d.b;
       h0 = g * p.group + ht * kMaxRows;
       hn = min(kMaxRows, p.group - ht * kMaxRows);
-      paired = hn <= kMaxRows / 2;
       const T* q = static_cast<const T*>(p.q.ptr) + b * p.q.sb;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         mma16816<T>(s1, qf[k + 1], kf[2], kf[3]);
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < kSets; ++r)
         *reinterpret_cast<float2*>(sbuf + (split * kMaxRows + row0 + r * 8) * C::kSPitch + (k0 + col2) * 4) =
             make_float2(s[r * 2] + s1[r * 2], s[r * 2 + 1] + s1[r * 2 + 1]);
     }
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     // ---- softmax of this warp's rows; P takes the place of the logits.  A lane takes kPair
     // neighbouring keys of every 32 * kPair.
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < kSets; ++r) {
       const int row = warp + r * 8;
       if (row >= hn) break;
       float* srow = reinterpret_cast<float*>(sbuf + row * C::kSPitch);
@@ -609,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       const float scale = ex2(m[r] - base);
       float sum = 0.f;
       T* prow = reinterpret_cast<T*>(srow);
-      T* rest = paired ? reinterpret_cast<T*>(sbuf + (row + 8) * C::kSPitch) : prow + kTile;
+      T* rest = kLarge ? prow + kTile : reinterpret_cast<T*>(sbuf + (row + 8) * C::kSPitch);
 #pragma unroll
       for (int i = 0; i < kPer; i += kPair) {
         const int key = kPair * lane + 32 * i;
@@ -630,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       l[r] = l[r] * scale + sum;
       if (lane == 0) {
         s_scale[row] = scale;
-        if (paired) s_scale[row + 8] = scale;
+        if (!kLarge) s_scale[row + 8] = scale;
       }
     }
     compute_barrier();
@@ -645,62 +656,49 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         o[n][2] *= c1;
         o[n][3] *= c1;
       }
-      const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16;
-      const uint32_t va = kst + (kTile + lane) * kPitch;
-      if (paired) {
+      const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16 + part_of * (kTile / kParts * 2);
+      const uint32_t va = kst + (kTile + part_of * (kTile / kParts) + lane) * kPitch;
+      float rest[kNt][4];
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k) {
-          uint32_t p0[4], p1[4];
-          ldsm4(pa + k * 64, p0);
-          ldsm4(pa + k * 64 + 32, p1);
+      for (int n = 0; n < kNt; ++n)
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            uint32_t vf[4];
-            ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
-            mma16816<T>(o[n], p0, vf[0], vf[1]);
-            mma16816<T>(o[n], p1, vf[2], vf[3]);
-          }
-        }
-      } else {
-        float rest[kNt][4];
+        for (int i = 0; i < 4; ++i) rest[n][i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) rest[n][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kTile / 32; ++k) {
-          uint32_t p0[4], p1[4], r0[4], r1[4];
-          ldsm4(pa + k * 64, p0);
-          ldsm4(pa + k * 64 + 32, p1);
+      for (int k = 0; k < kTile / 32 / kParts; ++k) {
+        uint32_t p0[4], p1[4], r0[4], r1[4];
+        ldsm4(pa + k * 64, p0);
+        ldsm4(pa + k * 64 + 32, p1);
+        if (kLarge) {
           ldsm4(pa + kTile * 2 + k * 64, r0);
           ldsm4(pa + kTile * 2 + k * 64 + 32, r1);
-#pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            uint32_t vf[4];
-            ldsm4_t(va + k * 32 * kPitch + (((warp * kNt + n) ^ perm<DP>(lane)) << 4), vf);
-            mma16816<T>(o[n], p0, vf[0], vf[1]);
-            mma16816<T>(rest[n], r0, vf[0], vf[1]);
-            mma16816<T>(o[n], p1, vf[2], vf[3]);
-            mma16816<T>(rest[n], r1, vf[2], vf[3]);
-          }
         }
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          uint32_t vf[4];
+          ldsm4_t(va + k * 32 * kPitch + (((cw * kNt + n) ^ perm<DP>(lane)) << 4), vf);
+          mma16816<T>(o[n], p0, vf[0], vf[1]);
+          if (kLarge) mma16816<T>(rest[n], r0, vf[0], vf[1]);
+          mma16816<T>(o[n], p1, vf[2], vf[3]);
+          if (kLarge) mma16816<T>(rest[n], r1, vf[2], vf[3]);
+        }
+      }
+      if (kLarge)
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[n][i] = with_rest(o[n][i], rest[n][i]);
-      }
     }
 
     if (d.flags & kEnd) {
       // ---- this run's part of the segment is complete
-      if (paired)
+      if (!kLarge)
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
           o[n][0] = with_rest(o[n][0], o[n][2]);
           o[n][1] = with_rest(o[n][1], o[n][3]);
         }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kSets; ++r) {
         float x = l[r];
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
@@ -710,12 +708,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         }
       }
       compute_barrier();
+      // the warps' parts of O are added up, half of them to the others at a time
+#pragma unroll
+      for (int h = kParts / 2; h > 0; h /= 2) {
+        float* x = reinterpret_cast<float*>(sbuf) + ((part_of % h) * kColWarps + cw) * (kNt * 128) + lane;
+        if (part_of >= h && part_of < 2 * h)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[(n * 4 + i) * 32] = o[n][i];
+        compute_barrier();
+        if (part_of < h)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] += x[(n * 4 + i) * 32];
+        if (h > 1) compute_barrier();
+      }
       const bool whole = (d.flags & kFull) != 0;
       float* part = partial(p, blockIdx.x, (d.flags & kSecond) ? 1 : 0);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kSets; ++r) {
         const int row = row0 + r * 8;
-        if (row >= hn) continue;
+        if (row >= hn || part_of > 0) continue;
         const float sum = s_sum[row];
         const bool none = sum == 0.f;
         const float inv = none ? 0.f : 1.f / kPScale<T> / sum;
@@ -723,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + (h0 + row) * p.o.sh;
 #pragma unroll
           for (int n = 0; n < kNt; ++n) {
-            const int col = warp * kCols + n * 8 + col2;
+            const int col = cw * kCols + n * 8 + col2;
             if (col < p.head_dim)
               *reinterpret_cast<uint32_t*>(out + col) =
                   Pack<T>::two(none ? 0.f : o[n][r * 2] * inv, none ? 0.f : o[n][r * 2 + 1] * inv);
@@ -738,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
           for (int n = 0; n < kNt; ++n)
             if (has_columns)
-              *reinterpret_cast<float2*>(part + row * DP + warp * kCols + n * 8 + col2) =
+              *reinterpret_cast<float2*>(part + row * DP + cw * kCols + n * 8 + col2) =
                   make_float2(o[n][r * 2] * (1.f / kPScale<T>), o[n][r * 2 + 1] * (1.f / kPScale<T>));
           if (warp == 0 && (lane & 3) == 0) {
             part[p.part_rows * DP + row] = s_max[row];
@@ -966,7 +981,7 @@ bool takes_whole(int batch, int h_k, int group, int max_seqlen, bool weights) {
          static_cast<int64_t>(batch) * h_k * ceil_div(group, kMaxRows) <= kMaxRuns;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kLarge>
 cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};  // devices with the attribute set
   int dev = 0;
@@ -974,13 +989,18 @@ cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(done.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(decode_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<DP>::kSmem);
+    e = cudaFuncSetAttribute(decode_kernel<T, DP, kLarge>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<DP, kLarge>::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  decode_kernel<T, DP><<<runs, kThreads, Cfg<DP>::kSmem, stream>>>(p);
+  decode_kernel<T, DP, kLarge><<<runs, kThreads, Cfg<DP, kLarge>::kSmem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, int DP>
+cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
+  return p.group > kMaxRows / 2 ? launch_main<T, DP, true>(p, runs, stream) : launch_main<T, DP, false>(p, runs, stream);
 }
 
 template <typename T>
