@@ -3,25 +3,27 @@
 // For each (sequence, key/value head) the query heads of the group share every key and
 // value, so the work is one pass over the cached rows: bound by the memory they lie in.
 // With up to 16 query heads as the M rows of an m16n8k16 product, S = Q K^T and O += P V
-// take a few per cent of the tensor pipe at full memory speed, whatever the group, so the
-// products are kept small and synchronous and the design goes into the loads.
+// keep the tensor pipe busy for a fifth of the time at full memory speed (heads of 128; groups
+// above 8 half as long again), so the products are kept small and synchronous and the design
+// goes into the loads.
 //
 // Split.  Keys come in tiles of about 32 KB (128 keys of 64 columns, 64 of
 // up to 128, 32 above; rows of 65 to 96 columns take 192 bytes and four stages: 64 sequences
-// of 4000 keys, 8 heads of 96, 127 us against 136 with 256 bytes and three, of 80 119 and 125).
+// of 4000 keys, 8 heads of 96, 129 us against 138 with 256 bytes and three, of 80 119 and 127,
+// of 72 139 and 148; but 16 heads without groups of 72 291 both ways, of 88 337 and 329).
 // All tiles of all (sequence, head) segments form one line, cut into equal runs, one per
 // resident block: ragged lengths balance by themselves, and one long sequence uses every
 // SM.  Where the blocks divide among the heads, every head has a line of its own instead,
 // all cut alike, and neighbouring blocks walk the same keys of different heads in step: a
 // token's heads lie side by side in memory, and rows that are not whole 128-byte lines
 // would otherwise be fetched again for the next head (heads of 112, 32 sequences up to
-// 8192 keys: 630 MB read for 491, 105 us; in step 86 us).  A segment that lies inside one run is finished there; one that is cut leaves
-// (O, maximum, sum) partials which a second small kernel joins (it is launched early and
-// waits for the first).  The cut depends on the lengths alone, so results do not depend
-// on timing.  (More and shorter runs, taken over by blocks as they finish, were slower:
-// 425 us with one run a block, 428 with two, 432 with four for 64 sequences of 4096 to
-// 16384 keys.)  Where no sequence passes kWholeKeys a block takes one segment and nothing
-// is joined.
+// 8192 keys: 630 MB read for 491, 105 us; in step 86 us).  A segment that lies inside one run
+// is finished there; one that is cut leaves (O, maximum, sum) partials which a second small
+// kernel joins (it is launched early and waits for the first).  The cut depends on the lengths
+// alone, so results do not depend on timing.  (More and shorter runs, taken over by blocks as
+// they finish, were slower: when 64 sequences of 4096 to 16384 keys took 425 us, 380 since, two
+// runs a block took 428 and four 432.)  Where no sequence passes kWholeKeys a block takes one
+// segment and nothing is joined.
 //
 // Block.  Two warps look the pages up and keep a ring of shared-memory stages filled with
 // 16-byte asynchronous copies, several tiles ahead; eight warps compute; two blocks share
@@ -68,8 +70,8 @@ constexpr int kLens = 256;      // lengths kept in shared memory
 constexpr int kBlocks = 2;      // of an SM
 // Runs at most: sizes the partials without asking a device.
 constexpr int kMaxRuns = 320;
-// Up to this length, and while the blocks suffice, sequences are taken whole (6.2 us against
-// 8.2 for one of 128 keys; but 2048 segments of 63 to 256 keys 51.4 us against 41.2).
+// Up to this length, and while the blocks suffice, sequences are taken whole (5.5 us against
+// 6.9 for one of 128 keys; but 2048 segments of 63 to 256 keys 39.7 us against 31.5).
 constexpr int kWholeKeys = 256;
 
 // Factor of P in shared memory and of O until it is written (a power of two: exact).
@@ -261,9 +263,10 @@ __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t*
     for (int i = 0; i < kIter; ++i) {
       const longlong2 a = rows[i * kStep];
       const bool ok = a.x != 0;
-      cp_async16_or_zero(at(i), ok ? a.x + c * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok, policy);
-      cp_async16_or_zero(at(i) + kTile * kPitch, ok ? a.y + c * 16 : reinterpret_cast<long long>(p.cache.v.ptr),
-                         ok, policy);
+      const long long k = ok ? a.x + c * 16 : reinterpret_cast<long long>(p.cache.k.ptr);
+      const long long v = ok ? a.y + c * 16 : reinterpret_cast<long long>(p.cache.v.ptr);
+      cp_async16_or_zero(at(i), k, ok, policy);
+      cp_async16_or_zero(at(i) + kTile * kPitch, v, ok, policy);
     }
   }
 }
@@ -363,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   if (p.head_dim < DP) {
     const int c0 = p.head_dim / 8, nc = DP / 8 - c0;
     for (int i = tid; i < S * 2 * kTile * nc; i += kThreads)
-      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ perm<DP>(i / nc)) << 4)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(ring + (i / nc) * kPitch + (((c0 + i % nc) ^ perm<DP>(i / nc)) << 4)) =
+          make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
 
@@ -599,14 +603,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
         for (int k = 0; k < kPair; ++k) {
           float& y = x[i + k];
-          if (C::kSplits == 2) y += reinterpret_cast<const float*>(sbuf + (kMaxRows + row) * C::kSPitch)[key + k];
+          if (C::kSplits == 2)
+            y += reinterpret_cast<const float*>(sbuf + (kMaxRows + row) * C::kSPitch)[key + k];
           y = p.softcap > 0.f ? p.cap_out * tanh_exp(y * p.cap_in) : y * p.scale_log2;
           if (!((valid >> k) & 1u)) y = -INFINITY;
           top = fmaxf(top, y);
         }
       }
       if (p.logits != nullptr) {
-        float* out = p.logits + (static_cast<int64_t>(b) * p.h_q + h0 + row) * p.logit_stride + d.rel + kPair * lane;
+        float* out = p.logits + (static_cast<int64_t>(b) * p.h_q + h0 + row) * p.logit_stride + d.rel +
+                     kPair * lane;
 #pragma unroll
         for (int i = 0; i < kPer; i += kPair)
           if (kPair == 2)
@@ -656,8 +662,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         o[n][2] *= c1;
         o[n][3] *= c1;
       }
-      const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16 + part_of * (kTile / kParts * 2);
-      const uint32_t va = kst + (kTile + part_of * (kTile / kParts) + lane) * kPitch;
+      const int first = part_of * (kTile / kParts);  // key of this warp's part
+      const uint32_t pa = smem_u32(sbuf) + (lane & 15) * C::kSPitch + (lane >> 4) * 16 + first * 2;
+      const uint32_t va = kst + (kTile + first + lane) * kPitch;
       float rest[kNt][4];
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
@@ -1000,7 +1007,8 @@ cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
 
 template <typename T, int DP>
 cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
-  return p.group > kMaxRows / 2 ? launch_main<T, DP, true>(p, runs, stream) : launch_main<T, DP, false>(p, runs, stream);
+  return p.group > kMaxRows / 2 ? launch_main<T, DP, true>(p, runs, stream)
+                                : launch_main<T, DP, false>(p, runs, stream);
 }
 
 template <typename T>

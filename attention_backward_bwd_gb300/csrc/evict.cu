@@ -16,8 +16,9 @@
 // bounds short heads is the chain of dependent steps.  Of 18.6 us for 1024 heads of 1025 to
 // 1088 slots cut to 1024, the launch and the keys take 6.2, the selection 2.7, the places
 // 3.4, the moves 6 (34 MB in all, 5.1 us at the memory's speed); of 23 us for 32 heads of
-// 5000 to 16000 slots 4.8, 5.5, 3.4 and 8.  Heads that move much are bound by memory again
-// (1024 heads of 8192 cut to 4096: 327 us, 1.1 GB moved as rows of 128 bytes in any order).
+// 5000 to 16000 slots 4.8, 5.5, 3.4 and 8.  Heads that move much are bound by the moves: 1024
+// heads of 8192 slots cut to 4096 take 334 us for 1.3 GB, 57 % of the copy bandwidth, since rows
+// of 128 bytes lie in any order and each thread goes from the lists to the table to its rows.
 // The loops are short: a form with the keys in registers and every loop unrolled spent 52 %
 // of its warps' time fetching instructions.
 #include <cooperative_groups.h>
@@ -48,7 +49,8 @@ constexpr uint32_t kInfKey = 0xFF800000u;  // rank_key(+inf): the rank of a rece
 
 // kSpread: a head has several blocks.  (One form for both made single blocks 2 us slower.)
 template <int T, bool kSpread>
-__global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T) evict_kernel(EvictParams p, int blocks_log2, FastDiv chunks) {
+__global__ void __launch_bounds__(T, T == 128 ? 7 : 1024 / T)
+    evict_kernel(EvictParams p, int blocks_log2, FastDiv chunks) {
   constexpr int W = T / 32;
   constexpr int kOwn = T < kBins ? kBins / T : 1;  // bins of a thread
   constexpr int kSums = kBins / kOwn / 32;         // warps that have some
@@ -338,7 +340,8 @@ cudaError_t launch_t(const EvictParams& p, int cs_log2, cudaStream_t stream) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = cs_log2 > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, cs_log2 > 0 ? evict_kernel<T, true> : evict_kernel<T, false>, p, cs_log2, chunks);
+  return cudaLaunchKernelEx(&cfg, cs_log2 > 0 ? evict_kernel<T, true> : evict_kernel<T, false>, p, cs_log2,
+                            chunks);
 }
 
 }  // namespace
@@ -358,9 +361,11 @@ cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream) {
           (heads << (log2 + 1) <= 4 * sms && p.max_seqlen >> (log2 + 1) >= kLeast)))
     ++log2;
   // Threads of a block: most where there are few blocks; fewer where there are many, which
-  // then pass their barriers side by side (1024 heads of 1088 slots: 29 us with 512, 21 with
-  // 256, 17 with 128; 400 heads: 16.5, 12.5, 14.4; 160 heads of 8192, two blocks each: 88,
-  // 84, 129).
+  // then pass their barriers side by side (1024 heads of 1088 slots: 34 us with 512, 26 with
+  // 256, 23 with 128; 400 heads: 14.0, 10.6, 13.0; 160 heads of 8192, two blocks each: 57,
+  // 49, 75).  Where there are many blocks of many slots the three come close, and 128 is not
+  // always the least: 1024 heads of 4000 133, 137, 136; of 8192, two blocks each, 357, 337,
+  // 336; but 320 heads of 16000, four blocks each, 125, 115, 131.
   const int64_t blocks = heads << log2;
   if (blocks <= 2 * sms || p.max_seqlen >> log2 > kCap<256>) return launch_t<512>(p, log2, stream);
   if (blocks <= 4 * sms) return launch_t<256>(p, log2, stream);
