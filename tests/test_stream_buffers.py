@@ -268,3 +268,34 @@ def test_a_block_in_use_is_not_taken_by_another_stream(call):
     assert all(torch.equal(x, y) for x, y in zip((got, *state), want))
     if call in ("rope", "append"):
         assert got.data_ptr() != at
+
+
+@pytest.mark.gpu
+def test_calls_on_a_forked_stream_are_captured_with_their_buffers():
+    batch, hq, hk, d, page, n = 4, 8, 2, 64, 16, 800
+    per = n // page
+    kc, vc = (torch.randn(batch * per, page, hk, d, device="cuda").half() for _ in range(2))
+    table = torch.arange(batch * per, dtype=torch.int32, device="cuda").view(batch, per)
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    q = torch.randn(batch, hq, d, device="cuda").half()
+    pos, inv = torch.arange(batch, dtype=torch.int32, device="cuda"), torch.rand(d // 2, device="cuda")
+
+    def step(**kw):
+        r, _ = ab.attn_rope(q, None, pos, inv, **kw)
+        return ab.attn_decode(r, kc, vc, table, lens, **kw)
+
+    step()  # loads the kernels
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        first = step(stream=side)
+        second = step(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        q.normal_()
+        want = step()
+        g.replay()
+        torch.cuda.synchronize()
+        for got in (first, second):
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ab.check_device_status()
