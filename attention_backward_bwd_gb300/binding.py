@@ -189,8 +189,10 @@ def _side(stream, index):
     None for the current stream."""
     if stream is None or isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                     device=index)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle in (0, 1):  # NULL and cudaStreamLegacy, of which torch would make a new stream
+        return torch.cuda.default_stream(index)
+    return torch.cuda.ExternalStream(handle, device=index)
 
 
 def _new(side, make, *args, **kw):

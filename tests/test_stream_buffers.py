@@ -64,7 +64,9 @@ class FakeTorch:
     def __init__(self):
         self.made, self.now = [], FakeStream(7)
         self.cuda = SimpleNamespace(
-            Stream=FakeStream, ExternalStream=lambda h, device=None: FakeStream(h), stream=self._stream,
+            Stream=FakeStream, stream=self._stream, default_stream=lambda device=None: FakeStream(0),
+            # a handle of 0 gives a new stream there
+            ExternalStream=lambda h, device=None: FakeStream(h if h > 1 else 555),
             current_stream=lambda device=None: self.now, current_device=lambda: 0,
             is_available=lambda: False)
 
@@ -191,7 +193,31 @@ def test_buffers_of_calls_on_the_current_stream(fake, call, allocated):
     assert lib.streams == [7] and [x.owner for x in t.made] == [7] * allocated
 
 
+@pytest.mark.parametrize("handle", [0, 1])
+@pytest.mark.parametrize("call,allocated", CALLS)
+def test_handles_of_the_default_stream(fake, call, allocated, handle):
+    t, lib = fake
+    call(stream=handle)
+    assert lib.streams == [handle] and [x.owner for x in t.made] == [0] * allocated
+
+
 # ------------------------------------------------------------------ on the GPU
+
+@pytest.mark.gpu
+def test_the_default_stream_by_its_handle():
+    side, main = torch.cuda.Stream(), torch.cuda.default_stream()
+    q = torch.randn(300, 4, 64, device="cuda").half()
+    pos, inv = torch.arange(300, dtype=torch.int32, device="cuda"), torch.rand(32, device="cuda")
+    want = ab.attn_rope(q, None, pos, inv)[0]
+    assert binding._side(0, 0) == binding._side(1, 0) == main
+    assert binding._side(side.cuda_stream, 0).cuda_stream == side.cuda_stream
+    side.wait_stream(main)
+    with torch.cuda.stream(side):
+        for handle in (0, 1):
+            got = ab.attn_rope(q, None, pos, inv, stream=handle)[0]
+            side.wait_stream(main)
+            assert torch.equal(got, want)
+
 
 def _busy_block(nbytes, stream):
     """A block of ``nbytes`` that the current stream still has to read: its address, where it is
