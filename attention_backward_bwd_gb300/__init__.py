@@ -13,6 +13,8 @@ from .binding import (AttnError, alloc_workspace, attn_bwd, attn_bwd_host, attn_
 from .cache import (alloc_decode_workspace, alloc_evict_workspace, attn_cache_append,
                     attn_cache_evict, attn_decode, attn_rope, decode_workspace_size,
                     evict_workspace_size)
+from .cache8 import attn_cache_append8, attn_cache_load8, attn_decode8
+from .pages import attn_cache_copy, attn_cache_fork, fork_workspace_size
 
 __all__ = ["AttnError", "alloc_workspace", "attn_bwd", "attn_bwd_host", "attn_bwd_host_varlen",
            "attn_fwd",
@@ -20,4 +22,6 @@ __all__ = ["AttnError", "alloc_workspace", "attn_bwd", "attn_bwd_host", "attn_bw
            "host_buffer_size", "lib", "set_wait_timeout_ns", "version", "workspace_layout",
            "workspace_size", "alloc_decode_workspace", "alloc_evict_workspace",
            "attn_cache_append", "attn_cache_evict", "attn_decode", "attn_rope",
-           "decode_workspace_size", "evict_workspace_size"]
+           "decode_workspace_size", "evict_workspace_size", "attn_cache_append8",
+           "attn_cache_load8", "attn_decode8", "attn_cache_copy", "attn_cache_fork",
+           "fork_workspace_size"]

@@ -68,7 +68,8 @@ EXPORTS = ("attn_fwd", "attn_bwd", "attn_bwd_preprocess", "attn_bwd_main", "attn
            "attn_set_wait_timeout_ns", "attn_last_error", "attn_version", "attn_diag_mma",
            "attn_diag_wait_timeout", "attn_diag_tanh", "attn_rope", "attn_cache_append",
            "attn_decode", "attn_decode_workspace_size", "attn_cache_evict",
-           "attn_cache_evict_workspace_size")
+           "attn_cache_evict_workspace_size", "attn_cache_append8", "attn_cache_load8",
+           "attn_decode8", "attn_cache_fork", "attn_cache_fork_workspace_size", "attn_cache_copy")
 
 
 def lib() -> ctypes.CDLL:
@@ -147,6 +148,21 @@ def lib() -> ctypes.CDLL:
         L.attn_cache_evict.restype = _I
         L.attn_cache_evict_workspace_size.argtypes = [_I, _I, _I, _I]
         L.attn_cache_evict_workspace_size.restype = ctypes.c_size_t
+        # the cache in 8 bits (cache8.py) and shared pages (pages.py)
+        L.attn_cache_append8.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]
+        L.attn_cache_append8.restype = _I
+        L.attn_cache_load8.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]
+        L.attn_cache_load8.restype = _I
+        L.attn_decode8.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, f32, _P, _P, _I, _P, _P,
+                                   ctypes.c_size_t, _P]
+        L.attn_decode8.restype = _I
+        L.attn_cache_fork.argtypes = [_P, q64, _P, q64, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I,
+                                      _I, _P, _P, _P, ctypes.c_size_t, _P]
+        L.attn_cache_fork.restype = _I
+        L.attn_cache_fork_workspace_size.argtypes = [_I, _I, _I]
+        L.attn_cache_fork_workspace_size.restype = ctypes.c_size_t
+        L.attn_cache_copy.argtypes = [_P, _I, _I, _I, _P, _P, _I, _P]
+        L.attn_cache_copy.restype = _I
         _lib = L
         return L
 

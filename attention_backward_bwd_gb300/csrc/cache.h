@@ -1,8 +1,8 @@
 // Parameter blocks, launchers and the device-side page lookup of the serving
-// operators (include/attn_cache.h).  Not part of the public C ABI.
+// operators (include/attn_cache.h, attn_cache8.h).  Not part of the public C ABI.
 #pragma once
 
-#include "../../include/attn_cache.h"
+#include "../../include/attn_cache8.h"
 #include "internal.h"
 
 namespace attn {
@@ -27,6 +27,8 @@ struct FastDiv {
 constexpr unsigned int kBadLength = 1u;   // seqlens / slots out of range
 constexpr unsigned int kBadPage = 2u;     // block_table entry outside [0, num_pages)
 constexpr unsigned int kBadOffsets = 4u;  // cu_seqlens of an append
+constexpr unsigned int kBadParent = 8u;   // parents of a fork
+constexpr unsigned int kNoPage = 16u;     // no free page left for a fork
 
 // Longest sequence of a decode or an eviction.  Their kernels count slots in 32 bits and step past
 // the last one by up to 8 * 512 slots (evict.cu: a head's threads) or a tile.
@@ -111,9 +113,106 @@ struct EvictParams {
   unsigned int* status;
 };
 
+// Codes of 8 bits and their factors.
+struct Cache8Arg {
+  PagedArg pages;              // strides in bytes
+  float *k_scale, *v_scale;
+  int64_t ks[3], vs[3];        // strides of page, block of tokens, head
+  FastDiv block;               // by the tokens of a block
+  int int8;                    // 0: e4m3
+};
+
+struct Append8Params {
+  TensorArg q, oq, k, v;
+  RotaryArg rot;
+  int bf16;
+  int tokens, batch, h_q, h_k, head_dim;
+  Cache8Arg cache;
+  const int* seqlens;
+  const int* cu;               // nullptr: token t is sequence t
+  unsigned int* status;
+};
+
+struct Load8Params {
+  TensorArg k, v;              // outputs, ss and sh used
+  int bf16;
+  int tokens, batch, h_k, head_dim;
+  Cache8Arg cache;
+  const int* starts;
+  const int* cu;
+  unsigned int* status;
+};
+
+struct Decode8Params : DecodeParams {
+  float *k_scale, *v_scale;
+  int64_t ks[3], vs[3];
+  FastDiv block;
+  int bf16;
+};
+
+struct ForkParams {
+  const int* table;            // may be table_out
+  int64_t table_stride;
+  int* table_out;
+  int64_t out_stride;
+  const int* seqlens;
+  int* seqlens_out;
+  const int* refs;
+  int* refs_out;
+  int num_pages, rows, max_pages, page_size;
+  const int* parents;          // nullptr: every row its own
+  const int* room;             // nullptr: room_all for every row
+  int room_all;
+  int share;
+  int* copies;                 // pairs of pages
+  int* counts;                 // copies made, pages left free
+  int* ws;                     // fork_ws() bytes
+  unsigned int* status;
+};
+
+struct CopyParams {
+  TensorArg k, v;              // strides in bytes: page, the rows of rows[0], those of rows[1]
+  int rows[2], chunks;         // a page is rows[0] x rows[1] rows of 16-byte pieces
+  float *k_scale, *v_scale;
+  int64_t ks[3], vs[3];
+  int blocks, heads;
+  const int* pairs;
+  const int* count;            // nullptr: all
+  int num_pairs, num_pages;
+  unsigned int* status;
+};
+
+cudaError_t launch_append8(const Append8Params& p, cudaStream_t stream);
+cudaError_t launch_load8(const Load8Params& p, cudaStream_t stream);
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
+cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream);
+size_t fork_ws(int rows, int max_pages, int num_pages);
+cudaError_t launch_decode8(const Decode8Params& p, int int8, cudaStream_t stream);
+
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool append, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream);
+
+// Geometry of a decode with tiles of 1 << tile_log2 keys: how the groups are cut into head
+// tiles, the lines, their runs (0: no keys) and whether segments are taken whole.
+cudaError_t shape_decode(DecodeParams& p, int tile_log2, int blocks_per_sm, int* runs);
+// Joins the partials that a decode's `runs` blocks left (not after whole segments).
+cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, cudaStream_t stream);
+
+// ---- checks of arguments (cache_api.cu)
+
+inline TensorArg arg(const attn_tensor* t) { return TensorArg{t->ptr, t->stride_b, t->stride_s, t->stride_h}; }
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// A tensor with `n` entries along batch / sequence / head: strides of dimensions longer than one
+// are positive multiples of `unit` elements (16 bytes).
+int check_rows(const attn_tensor* t, const char* name, int64_t nb, int64_t ns, int64_t nh, int unit = 8);
+int check_heads(int dtype, int batch, int h_q, int h_k, int head_dim);
+int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out, int unit = 8);
+int check_length(const attn_paged_kv* c, int max_seqlen);
+int check_rotary(const attn_rotary* r, int64_t tokens, int head_dim, RotaryArg* out);
+// The operators' device status word (separate from the one that stops later varlen calls).
+int status_of(unsigned int** out);
+int check_workspace(const void* ws, size_t given, size_t need);
 
 // Moves of one head are at most the slots above the budget, and at most the budget.
 inline int evict_move_cap(int budget, int max_seqlen) {

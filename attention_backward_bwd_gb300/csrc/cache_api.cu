@@ -10,36 +10,28 @@
 
 namespace attn {
 
-namespace {
-
-// A tensor with `n` entries along batch / sequence / head: strides of
-// dimensions longer than one are positive multiples of 8 elements.
-int check_rows(const attn_tensor* t, const char* name, int64_t nb, int64_t ns, int64_t nh) {
+int check_rows(const attn_tensor* t, const char* name, int64_t nb, int64_t ns, int64_t nh, int unit) {
   if (t == nullptr || t->ptr == nullptr) return fail(ATTN_ERR_NULL, "%s is NULL", name);
   if (reinterpret_cast<uintptr_t>(t->ptr) % 16 != 0)
     return fail(ATTN_ERR_ALIGN, "%s: base pointer must be 16-byte aligned", name);
   const int64_t n[3] = {nb, ns, nh};
   const int64_t st[3] = {t->stride_b, t->stride_s, t->stride_h};
   for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && (st[i] <= 0 || st[i] % 8 != 0))
+    if (n[i] > 1 && (st[i] <= 0 || st[i] % unit != 0))
       return fail(ATTN_ERR_STRIDE,
-                  "%s: strides must be positive multiples of 8 elements (got b=%lld s=%lld h=%lld)",
-                  name, static_cast<long long>(t->stride_b), static_cast<long long>(t->stride_s),
+                  "%s: strides must be positive multiples of %d elements (got b=%lld s=%lld h=%lld)",
+                  name, unit, static_cast<long long>(t->stride_b), static_cast<long long>(t->stride_s),
                   static_cast<long long>(t->stride_h));
   if (nh > 1 && t->stride_h > INT32_MAX)
     return fail(ATTN_ERR_STRIDE, "%s: the head stride must stay below 2^31 elements", name);
   return ATTN_OK;
 }
 
-TensorArg arg(const attn_tensor* t) { return TensorArg{t->ptr, t->stride_b, t->stride_s, t->stride_h}; }
-
 int check_heads(int dtype, int batch, int h_q, int h_k, int head_dim) {
   return check_common(dtype, batch, 0, 0, h_q, h_k, head_dim, 1.f, nullptr, nullptr, 0, 0);
 }
 
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out) {
+int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out, int unit) {
   if (c == nullptr) return fail(ATTN_ERR_NULL, "cache is NULL");
   if (c->num_pages <= 0 || c->page_size <= 0 || c->max_pages <= 0)
     return fail(ATTN_ERR_SHAPE, "num_pages (%d), page_size (%d) and max_pages (%d) must be positive",
@@ -47,13 +39,13 @@ int check_cache(const attn_paged_kv* c, int batch, int h_k, PagedArg* out) {
   if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX)
     return fail(ATTN_ERR_SHAPE, "max_pages * page_size must stay below 2^31");
   int rc;
-  if ((rc = check_rows(&c->k, "k cache", c->num_pages, c->page_size, h_k))) return rc;
-  if ((rc = check_rows(&c->v, "v cache", c->num_pages, c->page_size, h_k))) return rc;
+  if ((rc = check_rows(&c->k, "k cache", c->num_pages, c->page_size, h_k, unit))) return rc;
+  if ((rc = check_rows(&c->v, "v cache", c->num_pages, c->page_size, h_k, unit))) return rc;
   // the kernels hold page and slot strides in 16-byte units of 32 bits (64 GiB a page)
   for (const attn_tensor* t : {&c->k, &c->v})
-    if ((c->num_pages > 1 && t->stride_b / 8 > UINT32_MAX) ||
-        (c->page_size > 1 && t->stride_s / 8 > UINT32_MAX))
-      return fail(ATTN_ERR_STRIDE, "page and slot strides must stay below 2^35 elements");
+    if ((c->num_pages > 1 && t->stride_b / unit > UINT32_MAX) ||
+        (c->page_size > 1 && t->stride_s / unit > UINT32_MAX))
+      return fail(ATTN_ERR_STRIDE, "page and slot strides must stay below 2^%d elements", unit == 8 ? 35 : 36);
   if (c->block_table == nullptr) return fail(ATTN_ERR_NULL, "block_table is NULL");
   if (!aligned(c->block_table, 4)) return fail(ATTN_ERR_ALIGN, "block_table must be 4-byte aligned");
   if (batch > 1 && c->table_stride < c->max_pages)
@@ -111,8 +103,6 @@ int check_rotary(const attn_rotary* r, int64_t tokens, int head_dim, RotaryArg* 
   return ATTN_OK;
 }
 
-// The operators' device status word (separate from the one that stops later
-// varlen calls).
 int status_of(unsigned int** out) {
   unsigned int* st = status_word();
   if (st == nullptr) return fail(ATTN_ERR_CUDA, "cannot resolve the device status word");
@@ -128,6 +118,8 @@ int check_workspace(const void* ws, size_t given, size_t need) {
     return fail(ATTN_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", given, need);
   return ATTN_OK;
 }
+
+namespace {
 
 struct EvictWs {
   size_t off_to, total;

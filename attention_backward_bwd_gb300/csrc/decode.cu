@@ -52,8 +52,7 @@
 // without the factor.
 #include <atomic>
 
-#include "cache.h"
-#include "common.cuh"
+#include "decode.cuh"
 
 namespace attn {
 
@@ -65,14 +64,7 @@ constexpr int kCopy = 64;       // copying threads
 constexpr int kThreads = kCompute + kCopy;
 constexpr int kJoin = 128;      // threads of a join block
 constexpr int kAhead = 8;       // partials of a lane in flight there
-constexpr int kMaxRows = 16;    // query heads of a block
-constexpr int kLens = 256;      // lengths kept in shared memory
 constexpr int kBlocks = 2;      // of an SM
-// Runs at most: sizes the partials without asking a device.
-constexpr int kMaxRuns = 320;
-// Up to this length, and while the blocks suffice, sequences are taken whole (5.5 us against
-// 6.9 for one of 128 keys; but 2048 segments of 63 to 256 keys 39.7 us against 31.5).
-constexpr int kWholeKeys = 256;
 
 // Factor of P in shared memory and of O until it is written (a power of two: exact).
 template <typename T>
@@ -104,100 +96,7 @@ struct __align__(16) TileDesc {
   uint32_t valid[4];  // bit per key of the tile
   int pad[4];
 };
-enum { kBegin = 1, kEnd = 2, kFull = 4, kSecond = 8, kNone = 16 };
 
-// Keys that sequence length n leaves to attend: [first, n).
-__device__ __forceinline__ int first_key(const DecodeParams& p, int n) {
-  return p.win_left >= 0 ? max(0, n - 1 - p.win_left) : 0;
-}
-__device__ __forceinline__ int clean_len(const DecodeParams& p, int n, bool tell) {
-  if (n >= 0 && n <= p.max_seqlen) return n;
-  if (tell) report(p.status, kBadLength);
-  return 0;
-}
-__device__ __forceinline__ int tiles_of(const DecodeParams& p, int n) {
-  return (n - first_key(p, n) + (1 << p.tile_log2) - 1) >> p.tile_log2;
-}
-
-// Where a line of tiles is cut.  Run i of `runs` is [i * total / runs, (i + 1) * total / runs).
-struct Cut {
-  long long total;
-  int runs;
-  __device__ __forceinline__ long long start(int i) const { return total * i / runs; }
-  __device__ __forceinline__ int run_of(long long tile) const {
-    return static_cast<int>(((tile + 1) * runs - 1) / total);
-  }
-};
-
-// Block-wide exclusive prefix of the tiles of the sequences: every thread owns `per`
-// neighbouring ones.  Returns this thread's prefix.  Ends with a barrier.  (The launch
-// checks that the sum stays below 2^31.)
-template <int N>
-__device__ __forceinline__ int scan_tiles(const DecodeParams& p, bool tell, int* lens,
-                                          int* warp_sums, int per, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    if (b >= p.batch) break;
-    const int n = clean_len(p, p.seqlens[b], tell);
-    if (lens != nullptr && b < kLens) lens[b] = n;
-    mine += tiles_of(p, n);
-  }
-  int x = mine;
-#pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, i);
-    if (lane >= i) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < N / 32; ++w) {
-    before += w < warp ? warp_sums[w] : 0;
-    total += warp_sums[w];
-  }
-  return before + x - mine;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, long long src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "l"(policy)
-               : "memory");
-}
-// 16 bytes, or 16 zeros.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0), "l"(policy)
-               : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -213,12 +112,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Partial of a block (of its run's first or second cut segment): rows of O, then maxima
-// and sums.
-__device__ __forceinline__ float* partial(const DecodeParams& p, int block, int second) {
-  return p.parts + (static_cast<int64_t>(block) * 2 + second) * p.part_stride;
 }
 
 // What a row's chunk numbers are permuted by (exclusive or): eight rows, four of them where a
@@ -269,37 +162,6 @@ __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t*
       cp_async16_or_zero(at(i) + kTile * kPitch, v, ok, policy);
     }
   }
-}
-
-// The sequence that tile `r0` of the line lies in, and the tiles (of one head) before it.
-template <int N, typename Len>
-__device__ __forceinline__ int find_sequence(const DecodeParams& p, const int* pre, int per, int hv_n,
-                                             long long r0, Len len_of, int& before) {
-  int lo = 0, hi = N - 1;  // the last thread whose sequences start at or before r0
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(pre[mid]) * hv_n <= r0) lo = mid; else hi = mid - 1;
-  }
-  before = pre[lo];
-  for (int b = lo * per;; ++b) {
-    const int t = tiles_of(p, len_of(b));
-    if (b + 1 >= p.batch || r0 < static_cast<long long>(before + t) * hv_n) return b;
-    before += t;
-  }
-}
-
-// Rows of head tile hv of a sequence without keys.
-template <typename T>
-__device__ __forceinline__ void no_keys(const DecodeParams& p, int b, int hv) {
-  const int g = hv / p.head_tiles, ht = hv - g * p.head_tiles;
-  const int h0 = g * p.group + ht * kMaxRows, hn = min(kMaxRows, p.group - ht * kMaxRows);
-  T* out = static_cast<T*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + h0 * p.o.sh;
-  const int chunks = p.head_dim / 8;
-  for (int i = threadIdx.x; i < hn * chunks; i += blockDim.x)
-    *reinterpret_cast<uint4*>(out + (i / chunks) * p.o.sh + (i % chunks) * 8) = make_uint4(0, 0, 0, 0);
-  if (p.lse != nullptr)
-    for (int i = threadIdx.x; i < hn; i += blockDim.x)
-      p.lse[static_cast<int64_t>(b) * p.h_q + h0 + i] = INFINITY;
 }
 
 // O and what P's remainders add to it.  Of an infinite value a remainder of 0 or below makes
@@ -980,8 +842,6 @@ __global__ void __launch_bounds__(kJoin) weights_kernel(DecodeParams p, int bloc
   }
 }
 
-int pad_dim(int d) { return d <= 64 ? 64 : (d <= 96 ? 96 : (d <= 128 ? 128 : (d <= 192 ? 192 : 256))); }
-
 // One block a segment, without partials.
 bool takes_whole(int batch, int h_k, int group, int max_seqlen, bool weights) {
   return !weights && max_seqlen <= kWholeKeys &&
@@ -1014,15 +874,48 @@ cudaError_t launch_main(const DecodeParams& p, int runs, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
   const int dp = pad_dim(p.head_dim);
+  p.chunks = p.head_dim / 8;
+  int r;
+  cudaError_t e = shape_decode(p, tile_log2(dp), kBlocks, &r);
+  if (e != cudaSuccess) return e;
+  if (r > 0) {
+    if (dp == 64) e = launch_main<T, 64>(p, r, stream);
+    else if (dp == 96) e = launch_main<T, 96>(p, r, stream);
+    else if (dp == 128) e = launch_main<T, 128>(p, r, stream);
+    else if (dp == 192) e = launch_main<T, 192>(p, r, stream);
+    else e = launch_main<T, 256>(p, r, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.whole) return cudaSuccess;
+  e = launch_join(p, Pack<T>::kIsBf16 ? ATTN_BF16 : ATTN_FP16, r, stream);
+  if (e != cudaSuccess || p.w_in == nullptr || p.max_seqlen == 0) return e;
+  // 16 blocks fit an SM
+  const int64_t bg = static_cast<int64_t>(p.batch) * p.h_k, fit = (16 * static_cast<int64_t>(num_sms()) + bg - 1) / bg;
+  const int chunks = ceil_div(p.max_seqlen, kKeys), blocks = chunks < fit ? chunks : static_cast<int>(fit);
+  if (bg * blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchAttribute early;  // starts while the kernel before it drains, and waits for it
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(bg * blocks));
+  cfg.blockDim = dim3(kJoin);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_kernel, p, blocks);
+}
+
+}  // namespace
+
+cudaError_t shape_decode(DecodeParams& p, int tile_log2, int blocks_per_sm, int* runs_out) {
   p.head_tiles = ceil_div(p.group, kMaxRows);
   p.part_rows = p.group < kMaxRows ? p.group : kMaxRows;
-  p.part_stride = static_cast<int64_t>(p.part_rows) * dp + 2 * kMaxRows;
-  p.chunks = p.head_dim / 8;
-  p.tile_log2 = tile_log2(dp);
+  p.part_stride = static_cast<int64_t>(p.part_rows) * pad_dim(p.head_dim) + 2 * kMaxRows;
+  p.tile_log2 = tile_log2;
   const int most_tiles = ceil_div(p.max_seqlen, 1 << p.tile_log2);
   if (static_cast<int64_t>(p.batch) * most_tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t most = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles * most_tiles;
-  int64_t runs = static_cast<int64_t>(num_sms()) * kBlocks;
+  int64_t runs = static_cast<int64_t>(num_sms()) * blocks_per_sm;
   if (runs > kMaxRuns) runs = kMaxRuns;
   const int64_t heads = static_cast<int64_t>(p.h_k) * p.head_tiles;
   // A line a head when that leaves at most a quarter of the blocks idle (64 heads of 64, 256
@@ -1038,43 +931,29 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     runs = p.batch * heads;
     p.lines = 1;
   }
-  cudaError_t e = cudaSuccess;
-  if (runs > 0) {
-    const int r = static_cast<int>(runs);
-    if (dp == 64) e = launch_main<T, 64>(p, r, stream);
-    else if (dp == 96) e = launch_main<T, 96>(p, r, stream);
-    else if (dp == 128) e = launch_main<T, 128>(p, r, stream);
-    else if (dp == 192) e = launch_main<T, 192>(p, r, stream);
-    else e = launch_main<T, 256>(p, r, stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.whole) return cudaSuccess;
+  *runs_out = static_cast<int>(runs);
+  return cudaSuccess;
+}
+
+cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, cudaStream_t stream) {
   cudaLaunchAttribute early;  // starts while the kernel before it drains, and waits for it
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // few segments have many partials each: then four warps share a row's
-  const int64_t segments = p.batch * heads;
+  const int64_t segments = static_cast<int64_t>(p.batch) * p.h_k * p.head_tiles;
   const int by_segment = segments <= runs;
-  const int rows_per = segments * p.part_rows <= 2 * runs ? 1 : (p.part_rows > 2 ? 4 : p.part_rows);
+  const int rows_per = segments * p.part_rows <= 2 * static_cast<int64_t>(runs) ? 1 : (p.part_rows > 2 ? 4 : p.part_rows);
   cfg.gridDim = dim3(static_cast<unsigned>(
       runs > 0 ? (by_segment ? segments : runs) * ceil_div(p.part_rows, rows_per) : 1));
   cfg.blockDim = dim3(kJoin);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = runs > 0 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T>, p, static_cast<int>(runs), by_segment, rows_per, dp);
-  if (e != cudaSuccess || p.w_in == nullptr || p.max_seqlen == 0) return e;
-  // 16 blocks fit an SM
-  const int64_t bg = static_cast<int64_t>(p.batch) * p.h_k, fit = (16 * static_cast<int64_t>(num_sms()) + bg - 1) / bg;
-  const int chunks = ceil_div(p.max_seqlen, kKeys), blocks = chunks < fit ? chunks : static_cast<int>(fit);
-  if (bg * blocks > INT32_MAX) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3(static_cast<unsigned>(bg * blocks));
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_kernel, p, blocks);
+  const int dp = pad_dim(p.head_dim);
+  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, p, runs, by_segment, rows_per, dp)
+                            : cudaLaunchKernelEx(&cfg, join_kernel<__half>, p, runs, by_segment, rows_per, dp);
 }
-
-}  // namespace
 
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights) {
   DecodeWs w = {};
