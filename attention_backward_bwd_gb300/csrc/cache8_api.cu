@@ -10,7 +10,8 @@ namespace attn {
 
 namespace {
 
-// Strides of factors: positive wherever a dimension is longer than one.
+// Strides of factors: positive wherever a dimension is longer than one; those of pages and blocks
+// are held in 32 bits.
 int check_factors(const float* s, const char* name, const int64_t (&st)[3], int64_t pages, int64_t blocks,
                   int64_t heads) {
   if (s == nullptr) return fail(ATTN_ERR_NULL, "%s is NULL", name);
@@ -20,6 +21,9 @@ int check_factors(const float* s, const char* name, const int64_t (&st)[3], int6
     if (n[i] > 1 && st[i] <= 0)
       return fail(ATTN_ERR_STRIDE, "%s: strides must be positive (got page=%lld block=%lld head=%lld)", name,
                   static_cast<long long>(st[0]), static_cast<long long>(st[1]), static_cast<long long>(st[2]));
+  for (int i = 0; i < 2; ++i)
+    if (n[i] > 1 && st[i] > UINT32_MAX)
+      return fail(ATTN_ERR_STRIDE, "%s: page and block strides must stay below 2^32", name);
   return ATTN_OK;
 }
 

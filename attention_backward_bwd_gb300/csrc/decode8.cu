@@ -21,12 +21,12 @@
 // attn_decode, and so is the kernel that joins them.
 //
 // Numbers.  q enters as fp16: bf16 rows are divided by the power of two of their largest element,
-// which is exact down to 2^-17 of it and off by 2^-25 of it below.  The weights of a key in O are
-// p_j vs_j.  vs_j = 2^e r with 1 <= r < 2, and the running maximum is that of s_j log2(e) + e, so
-// that the weight 2^(s + e - max) r stays within [0, 2] whatever the factors of the blocks are;
-// it enters the product as two fp16 numbers, its rounded value and the rounded remainder, times
-// 2^14, so that it is right to 2^-22 or 2^-39 of the largest.  The sum of the p_j has the same
-// maximum (its terms are 2^-e times as large: e is kept within +-60).  All sums are fp32.
+// which is exact down to 2^-17 of it and off by 2^-25 of it below.  The weight of a code in O is
+// p_j vs_j, and the running maximum M is that of s_j log2(e) + floor(log2 vs_j), so that the weight
+// 2^(s - M) vs stays below 2 whatever the factors of the blocks are.  It enters the product as two
+// fp16 numbers, its rounded value and the rounded remainder, times 2^14, so that it is right to
+// 2^-22 of itself or 2^-38 of the largest.  V's factors are kept within 2^+-60, so that the
+// 2^(s - M) of the sum have room in fp32.  All sums are fp32.
 #include <atomic>
 
 #include "decode.cuh"
@@ -38,27 +38,29 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kWeight = 16384.f;  // factor of the weights and of O until it is written
-constexpr int kExp = 60;            // exponents of V's factors lie within +-kExp
+constexpr int kKeys = 32;           // of a warp and tile
+constexpr float kLeast = 8.673617379884035e-19f, kMost = 1.152921504606847e18f;  // factors of V: 2^-60, 2^60
 
 template <int DP, int HN>
 struct Cfg {
   static constexpr int kBlocks = DP <= 128 && HN == 1 ? 2 : (DP == 64 ? 2 : 1);  // of an SM
-  static constexpr int kGroups = DP == 64 ? 2 : 1;       // groups of 16 keys of a warp and tile
-  static constexpr int kKeys = 16 * kGroups;
-  static constexpr int kTileLog2 = kGroups == 2 ? 8 : 7;
-  static constexpr int kTile = 1 << kTileLog2;
+  // a warp's 32 keys of a tile are copied and worked on in kSubs parts of kGroups times 16
+  static constexpr int kGroups = DP == 64 ? 2 : 1, kSubs = 2 / kGroups, kSubKeys = 16 * kGroups;
+  static constexpr int kStageBytes = 2 * kSubKeys * DP;  // of a part, of a warp
   static constexpr int kHeads = 8 * HN;
-  static constexpr int kStageBytes = 2 * kKeys * DP;     // of a warp
-  static constexpr int kMergeCols = 32 / HN;             // columns of O that the warps add up at a time
+  static constexpr int kMergeCols = 16;                  // columns of O that the warps add up at a time
   static constexpr int kMerge = kWarps * kHeads * (kMergeCols + 4) * 4;
-  // stages that fit beside the rest, at most six
+  // tiles that are copied ahead: as fit beside the rest, at most three
   static constexpr int kRest = 1024 + kWarps * (kHeads * 8 + 4) + kMerge + kLens * 4;
-  static constexpr int kFit = ((228 * 1024 / kBlocks - kRest) / kWarps - kKeys * 16 - 32) / (kStageBytes + kKeys * 8 + 16);
-  static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr int kSlots = kStages + 2;             // descriptors
-  static constexpr int kWarpBytes = kStages * (kStageBytes + kKeys * 8) + kKeys * 16 + kSlots * 16;
+  static constexpr int kFit = (228 * 1024 / kBlocks - kRest) / kWarps;
+  static constexpr int warp_bytes(int ahead) {  // stages, addresses, descriptors, factors
+    return (ahead * kSubs + 1) * kStageBytes + (ahead + 1) * kKeys * 8 + kKeys * 16 + 128;
+  }
+  static constexpr int kAhead = warp_bytes(3) <= kFit ? 3 : (warp_bytes(2) <= kFit ? 2 : 1);
+  static constexpr int kStages = kAhead * kSubs + 1, kSlots = kAhead + 1;
+  static constexpr int kWarpBytes = warp_bytes(kAhead);
   static constexpr int kSmem = kWarps * kWarpBytes + kMerge + kLens * 4;
-  static_assert(kWarpBytes % 16 == 0 && kStages >= 2, "");
+  static_assert(kWarpBytes % 128 == 0 && kSlots * 16 <= 128, "");
   static_assert((kSmem + kRest - kMerge - kLens * 4) * kBlocks <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -67,6 +69,14 @@ struct Cfg {
 template <int DP>
 __host__ __device__ constexpr int perm8(int row) {
   return DP % 128 == 0 ? row & 7 : (DP == 96 ? (row >> 2) & 1 : (row >> 1) & 3);
+}
+
+// The address of chunks k and k + 1 (k even) in a row, from that of chunks 0 and 1: rows start at
+// multiples of 32 bytes and more, so that the permutation acts on the address.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t row, int k) {
+  constexpr int kMask = DP % 128 == 0 ? 6 : (DP == 96 ? 0 : 2);
+  return (row ^ ((k & kMask) << 4)) + (k & ~(kMask | 1)) * 16;
 }
 
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const float* src, bool real) {
@@ -118,16 +128,16 @@ __device__ __forceinline__ void halves_across(uint32_t x, uint32_t& even, uint32
 template <int DP, int HN, bool INT8>
 __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel(Decode8Params p) {
   using C = Cfg<DP, HN>;
-  constexpr int S = C::kStages, kSlots = C::kSlots, kKeys = C::kKeys, kGroups = C::kGroups, kTile = C::kTile;
+  constexpr int S = C::kStages, kSlots = C::kSlots, kSubs = C::kSubs, kSubKeys = C::kSubKeys, kGroups = C::kGroups;
   constexpr int kSteps = DP / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_sums[kWarps];
   __shared__ float s_max[kWarps][C::kHeads], s_sum[kWarps][C::kHeads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned char* mine = smem + warp * C::kWarpBytes;  // ring, factors, addresses, descriptors
-  float2* factors = reinterpret_cast<float2*>(mine + S * C::kStageBytes);
-  longlong2* rows = reinterpret_cast<longlong2*>(factors + S * kKeys);
+  unsigned char* mine = smem + warp * C::kWarpBytes;  // stages, addresses, descriptors, factors
+  longlong2* rows = reinterpret_cast<longlong2*>(mine + S * C::kStageBytes);
   int4* desc = reinterpret_cast<int4*>(rows + kKeys);  // sequence, head tile, flags, valid keys
+  float2* factors = reinterpret_cast<float2*>(desc + 8);
   float* merge = reinterpret_cast<float*>(smem + kWarps * C::kWarpBytes);
   int* s_pre = reinterpret_cast<int*>(merge);  // until the first O is added up
   int* lens = reinterpret_cast<int*>(smem + kWarps * C::kWarpBytes + C::kMerge);
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   // columns that no copy writes stay zero
   if (p.chunks < DP / 16) {
     const int nc = DP / 16 - p.chunks;
-    for (int i = lane; i < S * 2 * kKeys * nc; i += 32)
+    for (int i = lane; i < S * 2 * kSubKeys * nc; i += 32)
       *reinterpret_cast<uint4*>(mine + (i / nc) * DP + (((p.chunks + i % nc) ^ perm8<DP>(i / nc)) << 4)) =
           make_uint4(0, 0, 0, 0);
   }
@@ -175,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   auto load_seq = [&](int n) {
     cn = n;
     cfirst = first_key(p, cn);
-    cnt = (cn - cfirst + kTile - 1) >> C::kTileLog2;
+    cnt = tiles_of(p, cn);
     table = p.cache.table + cb * p.cache.table_stride;
   };
   auto load_head = [&]() {
@@ -208,11 +218,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     seg_from_start = ct == 0;
   }
   load_head();
-  // strides in 16-byte units: a page's offset is one 32 x 32 bit product
+  // strides in 16-byte units: a page's offset is one 32 x 32 bit product; of factors, 32 bits
   const uint32_t kp = static_cast<uint32_t>(p.cache.k.sb / 16), kslot = static_cast<uint32_t>(p.cache.k.ss / 16);
   const uint32_t vp = static_cast<uint32_t>(p.cache.v.sb / 16), vslot = static_cast<uint32_t>(p.cache.v.ss / 16);
-  const int key = lane & (kKeys - 1);  // of this warp's keys the one that the lane looks up
-  int pend_page = 0, pend_within = 0, pend_flags = 0, pend_b = 0, pend_hv = 0;
+  const uint32_t fkp = static_cast<uint32_t>(p.ks[0]), fkb = static_cast<uint32_t>(p.ks[1]);
+  const uint32_t fvp = static_cast<uint32_t>(p.vs[0]), fvb = static_cast<uint32_t>(p.vs[1]);
+  // this lane's key of the first tile: of tiles of 128 keys a warp has 16
+  const bool lane_on = lane < (4 << (p.tile_log2 - 5));
+  const int key0 = (warp << (p.tile_log2 - 3)) + lane;
+  uint32_t pend_page = 0, pend_within = 0;
+  int pend_flags = 0, pend_b = 0, pend_hv = 0;
   bool pend_live = false;
   const char *pend_k = nullptr, *pend_v = nullptr;
   const float *pend_ks = nullptr, *pend_vs = nullptr;
@@ -226,12 +241,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     pend_v = vhead;
     pend_ks = ksh;
     pend_vs = vsh;
-    const int j = cfirst + ct * kTile + warp * kKeys + key;
-    pend_live = j < cn;
+    const int j = cfirst + (ct << p.tile_log2) + key0;
+    pend_live = lane_on && j < cn;
     if (pend_live) {
-      const int n = static_cast<int>(p.cache.page.div(static_cast<uint32_t>(j)));
-      pend_within = j - n * static_cast<int>(p.cache.page.d);
-      pend_page = table[n];
+      const uint32_t n = p.cache.page.div(static_cast<uint32_t>(j));
+      pend_within = static_cast<uint32_t>(j) - n * p.cache.page.d;
+      pend_page = static_cast<uint32_t>(table[n]);
     }
     const bool at_end = ct == cnt - 1;
     pend_b = cb;
@@ -261,99 +276,107 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   // Keys and values are read once, unless a group has several head tiles: they leave the L2 first.
   const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
   // Writes a tile's addresses and descriptor down and asks for its factors.
-  auto store_plan = [&](int slot, int stage) {
+  auto store_plan = [&](int slot) {
     bool ok = pend_live;
-    if (ok && static_cast<unsigned>(pend_page) >= static_cast<unsigned>(p.cache.num_pages)) {
+    if (ok && pend_page >= static_cast<uint32_t>(p.cache.num_pages)) {
       report(p.status, kBadPage);
       ok = false;
     }
     longlong2 o = make_longlong2(0, 0);  // addresses of the key's row of k and of v
     const float *fk = p.k_scale, *fv = p.v_scale;
     if (ok) {
-      const uint64_t page = static_cast<uint32_t>(pend_page), in = static_cast<uint32_t>(pend_within);
+      const uint64_t page = pend_page, in = pend_within;
       o.x = reinterpret_cast<long long>(pend_k + ((page * kp + in * kslot) << 4));
       o.y = reinterpret_cast<long long>(pend_v + ((page * vp + in * vslot) << 4));
-      const int64_t blk = p.block.div(static_cast<uint32_t>(pend_within));
-      fk = pend_ks + static_cast<int64_t>(pend_page) * p.ks[0] + blk * p.ks[1];
-      fv = pend_vs + static_cast<int64_t>(pend_page) * p.vs[0] + blk * p.vs[1];
+      const uint64_t blk = p.block.div(pend_within);
+      fk = pend_ks + (page * fkp + blk * fkb);
+      fv = pend_vs + (page * fvp + blk * fvb);
     }
-    const uint32_t at = factors_u + (stage * kKeys + key) * 8;
-    if (kKeys == 32) {
-      cp_async4_or_zero(at, fk, ok);
-      cp_async4_or_zero(at + 4, fv, ok);
-    } else {
-      cp_async4_or_zero(at + (lane >> 4) * 4, lane < 16 ? fk : fv, ok);
-    }
-    if (lane < kKeys) rows[key] = o;
+    const uint32_t at = factors_u + (slot * kKeys + lane) * 8;
+    cp_async4_or_zero(at, fk, ok);
+    cp_async4_or_zero(at + 4, fv, ok);
+    rows[lane] = o;
     const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0)
-      desc[slot] = make_int4(pend_b, pend_hv, pend_flags, static_cast<int>(kKeys == 32 ? bits : bits & 0xffffu));
+    if (lane == 0) desc[slot] = make_int4(pend_b, pend_hv, pend_flags, static_cast<int>(bits));
   };
-  // Issues the copies of the tile whose plan was stored last, if there is one.
-  auto fetch = [&](int slot, int stage) {
-    constexpr int kLanes = DP == 64 ? 4 : (DP <= 128 ? 8 : 16), kStep = 32 / kLanes, kIter = kKeys / kStep;
-    const int4 d = desc[slot];
-    const int c = lane % kLanes, r0 = lane / kLanes;
-    if (!(d.z & kNone) && d.w != 0 && c < p.chunks) {
-      const uint32_t dst = ring_u + stage * C::kStageBytes;
+  // Issues the copies of part `sub` of the tile whose plan was stored last, if there is one.
+  constexpr int kLanes = DP == 64 ? 4 : (DP <= 128 ? 8 : 16), kStep = 32 / kLanes, kIter = kSubKeys / kStep;
+  const int cc = lane % kLanes, cr = lane / kLanes;
+  const uint32_t copy_u = ring_u + cr * DP + ((cc ^ perm8<DP>(cr)) << 4);
+  auto fetch = [&](int slot, int sub, int stage) {
+    const uint32_t live = static_cast<uint32_t>(desc[slot].w) >> (sub * kSubKeys);
+    constexpr uint32_t kAll = kSubKeys == 32 ? 0xffffffffu : 0xffffu;
+    if ((live & kAll) != 0 && cc < p.chunks) {
+      const uint32_t dst = copy_u + stage * C::kStageBytes;
+      const longlong2* from = rows + sub * kSubKeys + cr;
+      auto to = [&](int i) { return (dst ^ (perm8<DP>(i * kStep) << 4)) + i * kStep * DP; };
+      if ((live & kAll) == kAll) {
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int r = r0 + i * kStep;
-        const longlong2 a = rows[r];
-        const bool ok = a.x != 0;
-        const uint32_t to = dst + r * DP + ((c ^ perm8<DP>(r)) << 4);
-        cp_async16_or_zero(to, ok ? a.x + c * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok, policy);
-        cp_async16_or_zero(to + kKeys * DP, ok ? a.y + c * 16 : reinterpret_cast<long long>(p.cache.v.ptr), ok, policy);
+        for (int i = 0; i < kIter; ++i) {
+          const longlong2 a = from[i * kStep];
+          cp_async16(to(i), a.x + cc * 16, policy);
+          cp_async16(to(i) + kSubKeys * DP, a.y + cc * 16, policy);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const longlong2 a = from[i * kStep];
+          const bool ok = a.x != 0;
+          cp_async16_or_zero(to(i), ok ? a.x + cc * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok, policy);
+          cp_async16_or_zero(to(i) + kSubKeys * DP, ok ? a.y + cc * 16 : reinterpret_cast<long long>(p.cache.v.ptr), ok,
+                             policy);
+        }
       }
     }
     cp_commit();
   };
   plan();
-  int slot_w = 0, stage_w = 0;  // of the next tile to store and fetch
-  auto next_w = [&]() {
-    slot_w = slot_w + 1 == kSlots ? 0 : slot_w + 1;
-    stage_w = stage_w + 1 == S ? 0 : stage_w + 1;
-  };
-  for (int t = 0; t < S - 1; ++t) {
-    store_plan(slot_w, stage_w);
+  int slot_w = 0, stage_w = 0;  // of the next tile to store, of the next part to fetch
+  auto next_stage = [&]() { stage_w = stage_w + 1 == S ? 0 : stage_w + 1; };
+  for (int t = 0; t < C::kAhead; ++t) {
+    store_plan(slot_w);
     plan();
     __syncwarp();
-    fetch(slot_w, stage_w);
-    next_w();
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub) {
+      fetch(slot_w, sub, stage_w);
+      next_stage();
+    }
+    ++slot_w;  // kAhead < kSlots
     __syncwarp();
   }
 
   // ================================================== attention
   uint32_t qf[HN][kSteps][2];
-  float qscale[HN][2];  // of heads 2 (lane % 4) and the next: times s_j ks_j the base-2 logit
+  float qscale[HN][2];  // of heads 2 (lane % 4) and the next: times s_j ks_j the logit (base 2, or under the cap)
   float o[kSteps][HN][4];
-  float m[HN][2], l[HN][2];
+  float m[HN][2], base[HN][2], l[HN][2];  // base: m, or 0 without keys so far
   const int g8 = lane >> 2, q4 = lane & 3;
   int b = 0, h0 = 0, hn = 0;
-  const uint32_t lrow = (lane & 7) + ((lane >> 3) & 1) * 8;  // of ldmatrix: key and chunk
-  const int lchunk = lane >> 4;
+  // ldmatrix: this lane's key and chunk 0 or 1
+  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+  const uint32_t load_u = ring_u + lrow * DP + (((lane >> 4) ^ perm8<DP>(lrow)) << 4);
   int slot = 0, stage = 0;
   for (;;) {
     cp_wait<S - 2>();
-    __syncwarp();  // the copies of all lanes are there, and the last tile's stage is free
+    __syncwarp();  // the copies of all lanes are there, and the last part's stage is free
     const int4 d = desc[slot];
     if (d.z & kNone) break;
-    const int stage_now = stage;
+    const float2* factor = factors + slot * kKeys + g8;
     slot = slot + 1 == kSlots ? 0 : slot + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
-    // the tile S - 1 ahead
-    store_plan(slot_w, stage_w);
+    // the tile kAhead ahead
+    store_plan(slot_w);
     plan();
     __syncwarp();
-    fetch(slot_w, stage_w);
-    next_w();
+    fetch(slot_w, 0, stage_w);
+    next_stage();
 
     if (d.z & kBegin) {
       const int g = d.y / p.head_tiles, ht = d.y - g * p.head_tiles;
       b = d.x;
       h0 = g * p.group + ht * kMaxRows;
       hn = min(kMaxRows, p.group - ht * kMaxRows);
-      float mul[HN];
+      const float unit = p.softcap > 0.f ? p.cap_in : p.scale_log2;
 #pragma unroll
       for (int n = 0; n < HN; ++n) {
         const int head = g8 + n * 8;
@@ -367,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
           top = max(top, max(max((x.x & 0x7fffu) << 16, x.x & 0x7fff0000u),
                              max((x.y & 0x7fffu) << 16, x.y & 0x7fff0000u)));
         }
-        mul[n] = 1.f;
+        float mul = 1.f;
         if (p.bf16) {  // divided by the power of two of the row's largest element
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int e = min(max(static_cast<int>(top >> 23) - 127, -126), 126);
           const float down = __int_as_float((127 - e) << 23);
-          mul[n] = __int_as_float((127 + e) << 23);
+          mul = __int_as_float((127 + e) << 23);
 #pragma unroll
           for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -383,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) qscale[n][i] = __shfl_sync(0xffffffffu, mul[n], (2 * q4 + i) * 4);
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
+        for (int c = 0; c < 2; ++c) {
+          qscale[n][c] = __shfl_sync(0xffffffffu, mul, (2 * q4 + c) * 4) * unit;
+          m[n][c] = -INFINITY;
+          base[n][c] = l[n][c] = 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -393,10 +418,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
       }
     }
 
-    if (d.w != 0) {
-      const uint32_t kst = ring_u + stage_now * C::kStageBytes + lrow * DP;
-      // ---- base-2 logits of this warp's keys, plus the exponents of V's factors
-      float z[kGroups][HN][4], r[kGroups][2], down[kGroups][2];
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub) {
+      if (sub > 0) {
+        cp_wait<S - 2>();
+        __syncwarp();
+        fetch(slot_w, sub, stage_w);
+        next_stage();
+      }
+      const uint32_t kst = load_u + stage * C::kStageBytes;
+      stage = stage + 1 == S ? 0 : stage + 1;
+      const uint32_t live = static_cast<uint32_t>(d.w) >> (sub * kSubKeys);
+      if ((live & (kSubKeys == 32 ? 0xffffffffu : 0xffffu)) == 0) continue;
+
+      // ---- base-2 logits of this warp's keys; V's factors and their exponents
+      float y[kGroups][HN][4], e[kGroups][2], fv[kGroups][2];
+      bool moved = false;
 #pragma unroll
       for (int gr = 0; gr < kGroups; ++gr) {
         float s[HN][2][4];
@@ -407,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
         for (int k = 0; k < kSteps; k += 2) {
           uint32_t x[4], a[8];
-          ldsm4(kst + gr * 16 * DP + (((k + lchunk) ^ perm8<DP>(lrow)) << 4), x);
+          ldsm4(chunk_at<DP>(kst, k) + gr * 16 * DP, x);
           halves<INT8>(x[0], a[0], a[2]);
           halves<INT8>(x[1], a[1], a[3]);
           halves<INT8>(x[2], a[4], a[6]);
@@ -420,48 +457,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int kk = gr * 16 + g8 + i * 8;
-          const float2 f = factors[stage_now * kKeys + kk];
-          const int e = min(max(static_cast<int>(__float_as_uint(f.y) >> 23) - 127, -kExp), kExp);
-          r[gr][i] = f.y * __int_as_float((127 - e) << 23);
-          down[gr][i] = __int_as_float((127 - e) << 23);
-          const bool valid = (static_cast<uint32_t>(d.w) >> kk) & 1u;
+          const int kk = gr * 16 + i * 8;
+          const float2 f = factor[sub * kSubKeys + kk];
+          const float v = fminf(fmaxf(f.y, kLeast), kMost);
+          e[gr][i] = __uint_as_float(0x4b000000u | (__float_as_uint(v) >> 23)) - 8388735.f;  // 2^23 + 127
+          fv[gr][i] = f.y == 0.f ? 0.f : v * kWeight;
 #pragma unroll
           for (int n = 0; n < HN; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float x = (s[n][0][i * 2 + c] + s[n][1][i * 2 + c]) * (f.x * qscale[n][c]);
-              const float y = p.softcap > 0.f ? p.cap_out * tanh_exp(x * p.cap_in) : x * p.scale_log2;
-              z[gr][n][i * 2 + c] = valid ? y + static_cast<float>(e) : -INFINITY;
+              float& l2 = y[gr][n][i * 2 + c];
+              l2 = p.softcap > 0.f ? p.cap_out * tanh_exp(x) : x;
+              if (!((live >> (kk + g8)) & 1u)) l2 = -INFINITY;
+              moved |= l2 + e[gr][i] > m[n][c];
             }
         }
       }
       // ---- the running maximum
-      float f[HN][2];
-      bool moved = false;
-#pragma unroll
-      for (int n = 0; n < HN; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(z[0][n][c], z[0][n][c + 2]);
-          if (kGroups == 2) top = fmaxf(top, fmaxf(z[kGroups - 1][n][c], z[kGroups - 1][n][c + 2]));
-#pragma unroll
-          for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-          const float mx = fmaxf(m[n][c], top);
-          f[n][c] = mx == m[n][c] ? 1.f : ex2(m[n][c] - mx);
-          moved |= mx != m[n][c];
-          m[n][c] = mx;
-        }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int n = 0; n < HN; ++n) {
-          l[n][0] *= f[n][0];
-          l[n][1] *= f[n][1];
+        for (int n = 0; n < HN; ++n)
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k)
+          for (int c = 0; c < 2; ++c) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[k][n][i] *= f[n][i & 1];
-        }
+            for (int gr = 0; gr < kGroups; ++gr)
+              top = fmaxf(top, fmaxf(y[gr][n][c] + e[gr][0], y[gr][n][c + 2] + e[gr][1]));
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const float mx = fmaxf(m[n][c], top);
+            const float f = mx == m[n][c] ? 1.f : ex2(m[n][c] - mx);
+            m[n][c] = mx;
+            base[n][c] = mx == -INFINITY ? 0.f : mx;
+            l[n][c] *= f;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              o[k][n][c] *= f;
+              o[k][n][c + 2] *= f;
+            }
+          }
       }
       // ---- weights, and O^T += V^T (weights)
 #pragma unroll
@@ -471,11 +506,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
         for (int n = 0; n < HN; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0], b1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-            const float e0 = ex2(z[gr][n][i * 2] - b0), e1 = ex2(z[gr][n][i * 2 + 1] - b1);
-            l[n][0] += e0 * down[gr][i];
-            l[n][1] += e1 * down[gr][i];
-            const float w0 = e0 * (r[gr][i] * kWeight), w1 = e1 * (r[gr][i] * kWeight);
+            const float p0 = ex2(y[gr][n][i * 2] - base[n][0]), p1 = ex2(y[gr][n][i * 2 + 1] - base[n][1]);
+            l[n][0] += p0;
+            l[n][1] += p1;
+            const float w0 = p0 * fv[gr][i], w1 = p1 * fv[gr][i];
             const uint32_t h = Pack<__half>::two(w0, w1);
             const float2 back = Pack<__half>::unpack(h);
             hi[n][i] = transposed(h);
@@ -484,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
         for (int k = 0; k < kSteps; k += 2) {
           uint32_t x[4], a[8];
-          ldsm4_t(kst + (kKeys + gr * 16) * DP + (((k + lchunk) ^ perm8<DP>(lrow)) << 4), x);
+          ldsm4_t(chunk_at<DP>(kst, k) + (kSubKeys + gr * 16) * DP, x);
           halves_across<INT8>(x[0], a[0], a[1]);
           halves_across<INT8>(x[1], a[2], a[3]);
           halves_across<INT8>(x[2], a[4], a[5]);
@@ -499,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
         }
       }
     }
+    slot_w = slot_w + 1 == kSlots ? 0 : slot_w + 1;
 
     if (d.z & kEnd) {
       // ---- this run's part of the segment is complete: the warps' O are added up
@@ -588,7 +623,7 @@ cudaError_t launch_main(Decode8Params p, cudaStream_t stream) {
   using C = Cfg<DP, HN>;
   static std::atomic<unsigned long long> done{0};  // devices with the attribute set
   int runs;
-  cudaError_t e = shape_decode(p, C::kTileLog2, C::kBlocks, &runs);
+  cudaError_t e = shape_decode(p, 8, C::kBlocks, &runs);
   if (e != cudaSuccess) return e;
   if (runs > 0) {
     int dev = 0;

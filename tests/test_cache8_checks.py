@@ -99,7 +99,8 @@ BAD_CACHE = [
     (dict(c=None), NULL), (dict(d=72), SHAPE), (dict(c=paged8(kind=2)), DTYPE), (dict(c=paged8(block=0)), SHAPE),
     (dict(c=paged8(block=3)), SHAPE), (dict(c=paged8(fk=0)), NULL), (dict(c=paged8(fv=0)), NULL),
     (dict(c=paged8(fk=P + 2)), ALIGN), (dict(c=paged8(st=(0, 2, 1))), STRIDE), (dict(c=paged8(vst=(4, -2, 1))), STRIDE),
-    (dict(c=paged8(vst=(4, 2, 0))), STRIDE), (dict(c=paged8(kh=72)), STRIDE), (dict(c=paged8(ks=136)), STRIDE),
+    (dict(c=paged8(vst=(4, 2, 0))), STRIDE), (dict(c=paged8(st=(1 << 32, 2, 1))), STRIDE),
+    (dict(c=paged8(vst=(4, 1 << 32, 1))), STRIDE), (dict(c=paged8(kh=72)), STRIDE), (dict(c=paged8(ks=136)), STRIDE),
     (dict(c=paged8(kb=-2048)), STRIDE), (dict(c=paged8(kptr=P + 8)), ALIGN), (dict(c=paged8(vptr=0)), NULL),
     (dict(c=paged8(table=0)), NULL), (dict(c=paged8(ts=7)), STRIDE), (dict(c=paged8(pages=0)), SHAPE),
     (dict(c=paged8(kb=1 << 40)), STRIDE), (dict(c=paged8(size=1 << 28, per=8)), SHAPE),

@@ -256,12 +256,13 @@ def test_decode_with_factors_far_apart(dt, kind, exps):
     # V's factors anywhere in their range; K's near 1 and q small, so that the logits are moderate
     lens, d = [600, 90], 64
     kc, vc, ks, vs, table = make_cache8(600, 2, 2, d, 32, 16, kind, 11)
-    vs.copy_(torch.exp2(torch.randint(exps[0], exps[1] + 1, vs.shape).float()))
+    g = torch.Generator().manual_seed(11)
+    vs.copy_(torch.exp2(torch.randint(exps[0], exps[1] + 1, vs.shape, generator=g).float()))
     vs[::7] = 0.0  # blocks of zeros
     if dt == "fp16":  # the output stays within fp16
         vs.mul_(2.0 ** -exps[1])
         vs.copy_(torch.where(vs > 0, vs.clamp(min=2.0 ** -60), vs))
-    q = (torch.randn(2, 4, d) * 0.5).to(DT[dt]).cuda()
+    q = (torch.randn(2, 4, d, generator=g) * 0.5).to(DT[dt]).cuda()
     o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints(lens))
     ab.check_device_status()
     check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, d ** -0.5)
