@@ -48,8 +48,7 @@ struct Cfg {
   static constexpr int kGroups = DP == 64 ? 2 : 1, kSubs = 2 / kGroups, kSubKeys = 16 * kGroups;
   static constexpr int kStageBytes = 2 * kSubKeys * DP;  // of a part, of a warp
   static constexpr int kHeads = 8 * HN;
-  static constexpr int kMergeCols = 16;                  // columns of O that the warps add up at a time
-  static constexpr int kMerge = kWarps * kHeads * (kMergeCols + 4) * 4;
+  static constexpr int kMerge = kWarps * kHeads * 20 * 4;  // 16 columns of O of the warps, more of fewer heads
   // tiles that are copied ahead: as fit beside the rest, at most three
   static constexpr int kRest = 1024 + kWarps * (kHeads * 8 + 4) + kMerge + kLens * 4;
   static constexpr int kFit = (228 * 1024 / kBlocks - kRest) / kWarps;
@@ -178,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   int left = 0;
   int cb = 0, ch = 0, ct = 0, cn = 0, cfirst = 0, cnt = 0;
   bool seg_from_start = true;
-  int nth = 0, begin = 1;
   const int* table = nullptr;
   const char *khead = nullptr, *vhead = nullptr;
   const float *ksh = nullptr, *vsh = nullptr;
@@ -226,21 +224,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   // this lane's key of the first tile: of tiles of 128 keys a warp has 16
   const bool lane_on = lane < (4 << (p.tile_log2 - 5));
   const int key0 = (warp << (p.tile_log2 - 3)) + lane;
+  // The walk stands at the tile that is planned: it moves on when the next one is.
   uint32_t pend_page = 0, pend_within = 0;
-  int pend_flags = 0, pend_b = 0, pend_hv = 0;
-  bool pend_live = false;
-  const char *pend_k = nullptr, *pend_v = nullptr;
-  const float *pend_ks = nullptr, *pend_vs = nullptr;
-  auto plan = [&]() {  // looks one tile up and moves on
+  int flags = kBegin;
+  bool pend_live = false, first = true;
+  auto plan = [&]() {  // moves on and looks the tile up
     pend_live = false;
     if (left == 0) {
-      pend_flags = kNone;
+      flags = kNone;
       return;
     }
-    pend_k = khead;
-    pend_v = vhead;
-    pend_ks = ksh;
-    pend_vs = vsh;
+    if (!first) {
+      flags &= kSecond;
+      if (ct != cnt - 1) {
+        ++ct;
+      } else {
+        ct = 0;
+        flags = kBegin | kSecond;
+        seg_from_start = true;
+        if (++ch == line_heads) {
+          ch = 0;
+          do {
+            ++cb;
+            load_seq(len_of(cb));
+          } while (cnt == 0 && cb + 1 < p.batch);
+        }
+        load_head();
+      }
+    }
+    first = false;
+    --left;
+    if (ct == cnt - 1) flags |= seg_from_start ? kEnd | kFull : kEnd;
+    if (left == 0) flags |= kEnd;
     const int j = cfirst + (ct << p.tile_log2) + key0;
     pend_live = lane_on && j < cn;
     if (pend_live) {
@@ -248,34 +263,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
       pend_within = static_cast<uint32_t>(j) - n * p.cache.page.d;
       pend_page = static_cast<uint32_t>(table[n]);
     }
-    const bool at_end = ct == cnt - 1;
-    pend_b = cb;
-    pend_hv = line + ch;
-    pend_flags = (begin ? kBegin : 0) | (at_end || left == 1 ? kEnd : 0) | (at_end && seg_from_start ? kFull : 0) |
-                 (nth ? kSecond : 0);
-    begin = 0;
-    --left;
-    if (left == 0) return;
-    if (!at_end) {
-      ++ct;
-      return;
-    }
-    ct = 0;
-    begin = 1;
-    nth = 1;
-    seg_from_start = true;
-    if (++ch == line_heads) {
-      ch = 0;
-      do {
-        ++cb;
-        load_seq(len_of(cb));
-      } while (cnt == 0 && cb + 1 < p.batch);
-    }
-    load_head();
   };
   // Keys and values are read once, unless a group has several head tiles: they leave the L2 first.
   const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-  // Writes a tile's addresses and descriptor down and asks for its factors.
+  // Writes the tile's addresses and descriptor down and asks for its factors.
+  uint32_t live_w = 0;  // its keys
   auto store_plan = [&](int slot) {
     bool ok = pend_live;
     if (ok && pend_page >= static_cast<uint32_t>(p.cache.num_pages)) {
@@ -286,25 +278,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     const float *fk = p.k_scale, *fv = p.v_scale;
     if (ok) {
       const uint64_t page = pend_page, in = pend_within;
-      o.x = reinterpret_cast<long long>(pend_k + ((page * kp + in * kslot) << 4));
-      o.y = reinterpret_cast<long long>(pend_v + ((page * vp + in * vslot) << 4));
+      o.x = reinterpret_cast<long long>(khead + ((page * kp + in * kslot) << 4));
+      o.y = reinterpret_cast<long long>(vhead + ((page * vp + in * vslot) << 4));
       const uint64_t blk = p.block.div(pend_within);
-      fk = pend_ks + (page * fkp + blk * fkb);
-      fv = pend_vs + (page * fvp + blk * fvb);
+      fk = ksh + (page * fkp + blk * fkb);
+      fv = vsh + (page * fvp + blk * fvb);
     }
     const uint32_t at = factors_u + (slot * kKeys + lane) * 8;
     cp_async4_or_zero(at, fk, ok);
     cp_async4_or_zero(at + 4, fv, ok);
     rows[lane] = o;
-    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) desc[slot] = make_int4(pend_b, pend_hv, pend_flags, static_cast<int>(bits));
+    live_w = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) desc[slot] = make_int4(cb, line + ch, flags, static_cast<int>(live_w));
   };
   // Issues the copies of part `sub` of the tile whose plan was stored last, if there is one.
   constexpr int kLanes = DP == 64 ? 4 : (DP <= 128 ? 8 : 16), kStep = 32 / kLanes, kIter = kSubKeys / kStep;
   const int cc = lane % kLanes, cr = lane / kLanes;
   const uint32_t copy_u = ring_u + cr * DP + ((cc ^ perm8<DP>(cr)) << 4);
-  auto fetch = [&](int slot, int sub, int stage) {
-    const uint32_t live = static_cast<uint32_t>(desc[slot].w) >> (sub * kSubKeys);
+  auto fetch = [&](int sub, int stage) {
+    const uint32_t live = live_w >> (sub * kSubKeys);
     constexpr uint32_t kAll = kSubKeys == 32 ? 0xffffffffu : 0xffffu;
     if ((live & kAll) != 0 && cc < p.chunks) {
       const uint32_t dst = copy_u + stage * C::kStageBytes;
@@ -339,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     __syncwarp();
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub) {
-      fetch(slot_w, sub, stage_w);
+      fetch(sub, stage_w);
       next_stage();
     }
     ++slot_w;  // kAhead < kSlots
@@ -368,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     store_plan(slot_w);
     plan();
     __syncwarp();
-    fetch(slot_w, 0, stage_w);
+    fetch(0, stage_w);
     next_stage();
 
     if (d.z & kBegin) {
@@ -423,17 +415,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
       if (sub > 0) {
         cp_wait<S - 2>();
         __syncwarp();
-        fetch(slot_w, sub, stage_w);
+        fetch(sub, stage_w);
         next_stage();
       }
       const uint32_t kst = load_u + stage * C::kStageBytes;
       stage = stage + 1 == S ? 0 : stage + 1;
-      const uint32_t live = static_cast<uint32_t>(d.w) >> (sub * kSubKeys);
-      if ((live & (kSubKeys == 32 ? 0xffffffffu : 0xffffu)) == 0) continue;
+      constexpr uint32_t kAllKeys = kSubKeys == 32 ? 0xffffffffu : 0xffffu;
+      const uint32_t live = (static_cast<uint32_t>(d.w) >> (sub * kSubKeys)) & kAllKeys;
+      if (live == 0) continue;
 
       // ---- base-2 logits of this warp's keys; V's factors and their exponents
       float y[kGroups][HN][4], e[kGroups][2], fv[kGroups][2];
-      bool moved = false;
 #pragma unroll
       for (int gr = 0; gr < kGroups; ++gr) {
         float s[HN][2][4];
@@ -465,15 +457,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
           for (int n = 0; n < HN; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float x = (s[n][0][i * 2 + c] + s[n][1][i * 2 + c]) * (f.x * qscale[n][c]);
-              float& l2 = y[gr][n][i * 2 + c];
-              l2 = p.softcap > 0.f ? p.cap_out * tanh_exp(x) : x;
-              if (!((live >> (kk + g8)) & 1u)) l2 = -INFINITY;
-              moved |= l2 + e[gr][i] > m[n][c];
-            }
+            for (int c = 0; c < 2; ++c)
+              y[gr][n][i * 2 + c] = (s[n][0][i * 2 + c] + s[n][1][i * 2 + c]) * (f.x * qscale[n][c]);
         }
       }
+      if (p.softcap > 0.f) {
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+          for (int n = 0; n < HN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[gr][n][i] = p.cap_out * tanh_exp(y[gr][n][i]);
+      }
+      if (live != kAllKeys) {
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!((live >> (gr * 16 + i * 8 + g8)) & 1u))
+#pragma unroll
+              for (int n = 0; n < HN; ++n) y[gr][n][i * 2] = y[gr][n][i * 2 + 1] = -INFINITY;
+      }
+      bool moved = false;
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+        for (int n = 0; n < HN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) moved |= y[gr][n][i] + e[gr][i >> 1] > m[n][i & 1];
       // ---- the running maximum
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -562,28 +573,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
         }
       const bool whole = (d.z & kFull) != 0;
       float* part = partial(p, blockIdx.x, (d.z & kSecond) ? 1 : 0);
-      constexpr int kCols = C::kMergeCols, kPitch = kCols + 4, kRow = C::kHeads * kPitch;  // of a head, of a warp
+      // 16 columns at a time, or as many more as the heads are fewer
+      const int wide = hn > C::kHeads / 2 ? 0 : (hn > C::kHeads / 4 ? 1 : 2);
+      const int cols = 16 << wide, pitch = cols + 4, of_warp = (C::kHeads >> wide) * pitch;
 #pragma unroll
-      for (int k0 = 0; k0 < kSteps; k0 += kCols / 16) {
-        float* to = merge + warp * kRow;
+      for (int k = 0; k < kSteps; ++k) {
+        const int in = k & ((1 << wide) - 1);  // of the round
+        float* to = merge + warp * of_warp + in * 16 + 2 * g8;
 #pragma unroll
         for (int n = 0; n < HN; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int row = n * 8 + 2 * q4 + c;
-#pragma unroll
-            for (int k = 0; k < kCols / 16; ++k)
-              *reinterpret_cast<float2*>(to + row * kPitch + k * 16 + 2 * g8) =
-                  make_float2(o[k0 + k][n][c] * mul[n][c], o[k0 + k][n][c + 2] * mul[n][c]);
+            if (row < hn)
+              *reinterpret_cast<float2*>(to + row * pitch) = make_float2(o[k][n][c] * mul[n][c], o[k][n][c + 2] * mul[n][c]);
           }
+        if (in != (1 << wide) - 1 && k + 1 < kSteps) continue;
+        const int k0 = k - in, some = (in + 1) * 8;  // first step, pairs of columns
         __syncthreads();
-        for (int i = tid; i < hn * (kCols / 2); i += kThreads) {
-          const int row = i / (kCols / 2), col = i % (kCols / 2) * 2;
+        for (int i = tid; i < hn * some; i += kThreads) {
+          const int row = i / some, col = (i - row * some) * 2;
           float2 x = make_float2(0.f, 0.f);
           float top = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 y = *reinterpret_cast<const float2*>(merge + w * kRow + row * kPitch + col);
+            const float2 y = *reinterpret_cast<const float2*>(merge + w * of_warp + row * pitch + col);
             x.x += y.x;
             x.y += y.y;
             top = fmaxf(top, s_max[w][row]);
@@ -611,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
             }
           }
         }
-        if (k0 + kCols / 16 < kSteps) __syncthreads();
+        if (k + 1 < kSteps) __syncthreads();
       }
     }
   }
