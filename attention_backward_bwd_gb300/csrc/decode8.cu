@@ -48,9 +48,8 @@ struct Cfg {
   static constexpr int kGroups = DP == 64 ? 2 : 1, kSubs = 2 / kGroups, kSubKeys = 16 * kGroups;
   static constexpr int kStageBytes = 2 * kSubKeys * DP;  // of a part, of a warp
   static constexpr int kHeads = 8 * HN;
-  static constexpr int kMerge = kWarps * kHeads * 20 * 4;  // 16 columns of O of the warps, more of fewer heads
   // tiles that are copied ahead: as fit beside the rest, at most three
-  static constexpr int kRest = 1024 + kWarps * (kHeads * 8 + 4) + kMerge + kLens * 4;
+  static constexpr int kRest = 1024 + kWarps * (kHeads * 8 + 4) + kThreads * 4 + kLens * 4;
   static constexpr int kFit = (228 * 1024 / kBlocks - kRest) / kWarps;
   static constexpr int warp_bytes(int ahead) {  // stages, addresses, descriptors, factors
     return (ahead * kSubs + 1) * kStageBytes + (ahead + 1) * kKeys * 8 + kKeys * 16 + 128;
@@ -58,9 +57,9 @@ struct Cfg {
   static constexpr int kAhead = warp_bytes(3) <= kFit ? 3 : (warp_bytes(2) <= kFit ? 2 : 1);
   static constexpr int kStages = kAhead * kSubs + 1, kSlots = kAhead + 1;
   static constexpr int kWarpBytes = warp_bytes(kAhead);
-  static constexpr int kSmem = kWarps * kWarpBytes + kMerge + kLens * 4;
+  static constexpr int kSmem = kWarps * kWarpBytes + kThreads * 4 + kLens * 4;
   static_assert(kWarpBytes % 128 == 0 && kSlots * 16 <= 128, "");
-  static_assert((kSmem + kRest - kMerge - kLens * 4) * kBlocks <= 228 * 1024, "shared memory of an SM");
+  static_assert((kWarps * kWarpBytes + kRest) * kBlocks <= 228 * 1024, "shared memory of an SM");
 };
 
 // What a row's 16-byte chunk numbers are permuted by (exclusive or), so that eight neighbouring
@@ -137,9 +136,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   longlong2* rows = reinterpret_cast<longlong2*>(mine + S * C::kStageBytes);
   int4* desc = reinterpret_cast<int4*>(rows + kKeys);  // sequence, head tile, flags, valid keys
   float2* factors = reinterpret_cast<float2*>(desc + 8);
-  float* merge = reinterpret_cast<float*>(smem + kWarps * C::kWarpBytes);
-  int* s_pre = reinterpret_cast<int*>(merge);  // until the first O is added up
-  int* lens = reinterpret_cast<int*>(smem + kWarps * C::kWarpBytes + C::kMerge);
+  int* s_pre = reinterpret_cast<int*>(smem + kWarps * C::kWarpBytes);
+  int* lens = s_pre + kThreads;
   const int hv_n = p.h_k * p.head_tiles;
   const int line_heads = p.lines > 1 ? 1 : hv_n;
   const int run = blockIdx.x / p.lines, line = blockIdx.x - run * p.lines;
@@ -165,12 +163,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
     if (run >= cut.runs) return;
   }
   // columns that no copy writes stay zero
-  if (p.chunks < DP / 16) {
+  auto zero_columns = [&](int first_stage, int stages) {
     const int nc = DP / 16 - p.chunks;
-    for (int i = lane; i < S * 2 * kSubKeys * nc; i += 32)
-      *reinterpret_cast<uint4*>(mine + (i / nc) * DP + (((p.chunks + i % nc) ^ perm8<DP>(i / nc)) << 4)) =
-          make_uint4(0, 0, 0, 0);
-  }
+    for (int i = lane; i < stages * 2 * kSubKeys * nc; i += 32)
+      *reinterpret_cast<uint4*>(mine + first_stage * C::kStageBytes + (i / nc) * DP +
+                                (((p.chunks + i % nc) ^ perm8<DP>(i / nc)) << 4)) = make_uint4(0, 0, 0, 0);
+  };
+  zero_columns(0, S);
   __syncthreads();
 
   // ================================================== tiles: looked up, copied
@@ -548,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 
     if (d.z & kEnd) {
       // ---- this run's part of the segment is complete: the warps' O are added up
-      __syncthreads();  // what the last segment left has been read
 #pragma unroll
       for (int n = 0; n < HN; ++n)
 #pragma unroll
@@ -560,73 +558,62 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
             s_sum[warp][n * 8 + 2 * q4 + c] = l[n][c];
           }
         }
-      __syncthreads();
-      float mul[HN][2];
-#pragma unroll
-      for (int n = 0; n < HN; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w][n * 8 + 2 * q4 + c]);
-          mul[n][c] = ex2(m[n][c] - (top == -INFINITY ? 0.f : top));
-        }
       const bool whole = (d.z & kFull) != 0;
       float* part = partial(p, blockIdx.x, (d.z & kSecond) ? 1 : 0);
-      // 16 columns at a time, or as many more as the heads are fewer
-      const int wide = hn > C::kHeads / 2 ? 0 : (hn > C::kHeads / 4 ? 1 : 2);
-      const int cols = 16 << wide, pitch = cols + 4, of_warp = (C::kHeads >> wide) * pitch;
+      // Eight heads at a time each warp leaves its O in the stage that it worked on last, which
+      // the next copy will take: [head][column], columns permuted by the head.
+      const int done = stage == 0 ? S - 1 : stage - 1;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int in = k & ((1 << wide) - 1);  // of the round
-        float* to = merge + warp * of_warp + in * 16 + 2 * g8;
+      for (int n = 0; n < HN; ++n) {
+        const int heads = min(8, hn - n * 8);
+        if (heads <= 0) break;
+        float* to = reinterpret_cast<float*>(mine + done * C::kStageBytes);
 #pragma unroll
-        for (int n = 0; n < HN; ++n)
+        for (int c = 0; c < 2; ++c)
+          if (2 * q4 + c < heads)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int row = n * 8 + 2 * q4 + c;
-            if (row < hn)
-              *reinterpret_cast<float2*>(to + row * pitch) = make_float2(o[k][n][c] * mul[n][c], o[k][n][c + 2] * mul[n][c]);
-          }
-        if (in != (1 << wide) - 1 && k + 1 < kSteps) continue;
-        const int k0 = k - in, some = (in + 1) * 8;  // first step, pairs of columns
+            for (int k = 0; k < kSteps; ++k)
+              *reinterpret_cast<float2*>(to + (2 * q4 + c) * DP + ((k * 16 + 2 * g8) ^ (q4 * 8))) =
+                  make_float2(o[k][n][c], o[k][n][c + 2]);
         __syncthreads();
-        for (int i = tid; i < hn * some; i += kThreads) {
-          const int row = i / some, col = (i - row * some) * 2;
+        for (int i = tid; i < heads * (DP / 2); i += kThreads) {
+          const int in = i / (DP / 2), col = (i - in * (DP / 2)) * 2, row = n * 8 + in;
+          const unsigned char* from = smem + done * C::kStageBytes + (in * DP + (col ^ ((in >> 1) * 8))) * 4;
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w][row]);
+          const float low = top == -INFINITY ? 0.f : top;
           float2 x = make_float2(0.f, 0.f);
-          float top = -INFINITY, sum = 0.f;
+          float sum = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 y = *reinterpret_cast<const float2*>(merge + w * of_warp + row * pitch + col);
-            x.x += y.x;
-            x.y += y.y;
-            top = fmaxf(top, s_max[w][row]);
+            const float2 y = *reinterpret_cast<const float2*>(from + w * C::kWarpBytes);
+            const float f = ex2(s_max[w][row] - low);
+            x.x = fmaf(y.x, f, x.x);
+            x.y = fmaf(y.y, f, x.y);
+            sum = fmaf(s_sum[w][row], f, sum);
           }
-          const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) sum += s_sum[w][row] * ex2(s_max[w][row] - base);
-          const int at = k0 * 16 + col;
           if (whole) {
             const bool none = sum == 0.f;
             const float inv = none ? 0.f : 1.f / kWeight / sum;
-            const float a = none ? 0.f : x.x * inv, bb = none ? 0.f : x.y * inv;
+            const float u = none ? 0.f : x.x * inv, v = none ? 0.f : x.y * inv;
             uint16_t* out = static_cast<uint16_t*>(const_cast<void*>(p.o.ptr)) + b * p.o.sb + (h0 + row) * p.o.sh;
-            if (at < p.head_dim)
-              *reinterpret_cast<uint32_t*>(out + at) =
-                  p.bf16 ? Pack<__nv_bfloat16>::two(a, bb) : Pack<__half>::two(a, bb);
-            if (k0 == 0 && col == 0 && p.lse != nullptr)
+            if (col < p.head_dim)
+              *reinterpret_cast<uint32_t*>(out + col) = p.bf16 ? Pack<__nv_bfloat16>::two(u, v) : Pack<__half>::two(u, v);
+            if (col == 0 && p.lse != nullptr)
               p.lse[static_cast<int64_t>(b) * p.h_q + h0 + row] =
                   none ? INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
           } else {
-            *reinterpret_cast<float2*>(part + row * DP + at) = make_float2(x.x * (1.f / kWeight), x.y * (1.f / kWeight));
-            if (k0 == 0 && col == 0) {
+            *reinterpret_cast<float2*>(part + row * DP + col) = make_float2(x.x * (1.f / kWeight), x.y * (1.f / kWeight));
+            if (col == 0) {
               part[p.part_rows * DP + row] = top;
               part[p.part_rows * DP + kMaxRows + row] = sum;
             }
           }
         }
-        if (k + 1 < kSteps) __syncthreads();
+        __syncthreads();  // all of it has been read
       }
+      zero_columns(done, 1);
     }
   }
   cp_wait<0>();
