@@ -7,12 +7,15 @@
 // changes then where it leaves the normal range, and x / s is exact, so that a code is off by one
 // rounding of x.
 //
-// Append.  A block of threads takes the new tokens of one block of the cache: they lie in one page
-// (its tokens' block divides the page).  It computes the turns of a few rows at a time once for
-// all heads; its warps take a head of q, of k or of v each, a lane eight neighbouring elements of a
-// row.  Up to kHeld rows a lane stay in registers between the maximum and the rounding, so that
-// k and v are read once; blocks with more new tokens are read a second time, from the L2.
+// Append.  A block of threads takes the new tokens of one block of the cache, which lie in one page
+// (its tokens' block divides the page), and eight rows of heads of q, k or v, one a warp.  A warp
+// asks for its rows first (up to kHeld 16-byte chunks of a lane), then the block's threads compute
+// the turns of the tokens, and the rows stay in registers as they came: they are turned once for
+// their largest value and once more when they are rounded, so that k and v are read once.  Tokens
+// beyond kHeld chunks a lane are read a second time, from the L2.
 // Read-back.  A warp takes a token: 16 codes a lane, 32 bytes out.
+#include <type_traits>
+
 #include "cache.h"
 #include "common.cuh"
 
@@ -22,19 +25,18 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeld = 8;       // rows of a lane in registers
-constexpr int kTurns = 1024;   // turns of the rows that a block takes at once
+constexpr int kHeld = 16;      // chunks of a lane in registers
+constexpr int kTurns = 2048;   // turns of the rows that a block takes at once
 constexpr int kBlocks = 2;     // of an SM
 constexpr float kLargest = 1.152921504606847e18f;    // 2^60
 
-// The order in which a lane finds the other element of a pair: kHalves in the chunk n_freq
-// elements away (n_freq a multiple of 8), kPairs in its own chunk, kMixed element by element.
+// Where the other element of a pair is: kHalves in the lane n_freq / 8 further (n_freq a multiple
+// of 8), kPairs in the lane's own chunk, kMixed anywhere, read once more.
 enum RopeMode { kNoTurn = 0, kHalves = 1, kPairs = 2, kMixed = 3 };
 
 struct Append8Grid {
   int lanes_log2;        // lanes of a row
-  int mode;
-  int parts;             // blocks that share the heads of a block of tokens
+  FastDiv parts;         // blocks that share the heads of a block of tokens
 };
 
 // Smallest power of two that `top` is at most 448 (127) times, within the bounds; exact.
@@ -47,15 +49,20 @@ __device__ __forceinline__ float factor_of(float top) {
   return __int_as_float((min(max(e, -60), 60) + 127) << 23);
 }
 
-template <bool INT8>
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+// The codes of x inv.  kClean: all x are finite and none is beyond the largest code.
+template <bool INT8, bool kClean = false>
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float inv) {
   if (INT8) {
-    auto one = [](float x) { return static_cast<uint32_t>(min(max(__float2int_rn(x), -127), 127)) & 0xffu; };
-    return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+    // 1.5 2^23 more: the sum's last bits are the rounded number
+    auto one = [&](float x) {
+      if (kClean) return __float_as_uint(fmaf(x, inv, 12582912.f));
+      return static_cast<uint32_t>(min(max(__float2int_rn(x * inv), -127), 127));
+    };
+    return __byte_perm(__byte_perm(one(a), one(b), 0x0040), __byte_perm(one(c), one(d), 0x0040), 0x5410);
   }
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
@@ -106,15 +113,15 @@ __device__ __forceinline__ int blocks_of(const Append8Params& p, const Fresh& f)
   return n <= rest ? 1 : 2 + static_cast<int>(p.cache.block.div(n - rest - 1));
 }
 
-template <typename T, bool INT8>
+template <typename T, bool INT8, int MODE>
 __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Params p, Append8Grid g) {
-  __shared__ float2 cs[kTurns];                  // (cos, sin) of [row][frequency]
+  __shared__ float2 cs[MODE == kNoTurn ? 1 : kTurns];  // (cos, sin) of [row][frequency]
   __shared__ unsigned long long turns[128];
-  __shared__ int64_t s_pre[kThreads];            // (offsets that do not ascend may name a token often)
+  __shared__ int64_t s_pre[kThreads];  // (offsets that do not ascend may name a token often)
   __shared__ int64_t s_sums[kWarps];
-  extern __shared__ float s_top[];               // largest values of the heads of k and of v
+  __shared__ int4 s_fresh[kThreads];   // of the first sequence of each thread: first, n, len, bad
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nf = g.mode == kNoTurn ? 0 : p.rot.n_freq;
+  const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq;
 
   // fraction of a turn that one position adds at each frequency, times 2^64
   for (int i = tid; i < nf; i += kThreads) {
@@ -124,8 +131,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   // ---- blocks of the sequences before this thread's
   const int per = (p.batch + kThreads - 1) / kThreads;
   int64_t mine = 0;
-  for (int i = 0; i < per && tid * per + i < p.batch; ++i)
-    mine += blocks_of(p, fresh_of(p, tid * per + i, blockIdx.x == 0));
+  for (int i = 0; i < per && tid * per + i < p.batch; ++i) {
+    const Fresh f = fresh_of(p, tid * per + i, blockIdx.x == 0);
+    if (i == 0) s_fresh[tid] = make_int4(f.first, f.n, f.len, f.bad);
+    mine += blocks_of(p, f);
+  }
   int64_t x = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -147,12 +157,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   const int c = lane & (lanes - 1), r0 = lane >> g.lanes_log2, at = 8 * c;
   const bool on = at < p.head_dim;
   const int jobs = p.h_q + 2 * p.h_k;
-  const int64_t items = total * g.parts;
+  const int64_t items = total * g.parts.d;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t u = item / g.parts;
-    const int part = static_cast<int>(item - u * g.parts);
-    const int j0 = static_cast<int>(static_cast<int64_t>(jobs) * part / g.parts);
-    const int j1 = static_cast<int>(static_cast<int64_t>(jobs) * (part + 1) / g.parts);
+    const int64_t u = items <= INT32_MAX ? g.parts.div(static_cast<uint32_t>(item)) : item / g.parts.d;
+    const int part = static_cast<int>(item - u * g.parts.d);
     // ---- the sequence and the block of tokens
     int lo = 0, hi = kThreads - 1;
     while (lo < hi) {
@@ -160,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       if (s_pre[mid] <= u) lo = mid; else hi = mid - 1;
     }
     int b = lo * per, at_block = static_cast<int>(u - s_pre[lo]);
-    Fresh f = fresh_of(p, b, false);
+    const int4 held_fresh = s_fresh[lo];
+    Fresh f{held_fresh.x, held_fresh.y, held_fresh.z, held_fresh.w != 0};
     for (int n = blocks_of(p, f); at_block >= n; n = blocks_of(p, f)) {
       at_block -= n;
       f = fresh_of(p, ++b, false);
@@ -170,6 +179,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
     const int64_t from = base > f.len ? base : f.len, end = min(base + size, static_cast<int64_t>(f.len) + f.n);
     const int token0 = f.first + static_cast<int>(from - f.len), n = static_cast<int>(end - from);
     const int old = static_cast<int>(from - base);  // earlier tokens of the block
+
+    // ---- this warp's row of heads, on its way
+    const int j = part * kWarps + warp;
+    const bool is_q = j < p.h_q, is_v = j >= p.h_q + p.h_k, turned = MODE != kNoTurn && !is_v;
+    const int head = is_q ? j : j - p.h_q - (is_v ? p.h_k : 0);
+    const TensorArg& in = is_q ? p.q : (is_v ? p.v : p.k);
+    const int64_t row_step = in.ss * rpw;
+    const T* src = static_cast<const T*>(in.ptr) + static_cast<int64_t>(token0 + r0) * in.ss + head * in.sh + at;
+    uint4 raw[kHeld];
+    auto ask = [&](int t0) {
+      const int rows = on && j < jobs ? n - t0 - r0 : 0;
+      const T* s = src + t0 * in.ss;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        raw[i] = i * rpw < rows ? *reinterpret_cast<const uint4*>(s + i * row_step) : make_uint4(0, 0, 0, 0);
+    };
+    ask(0);
+
     const int64_t cap = static_cast<int64_t>(p.cache.pages.max_pages) * p.cache.pages.page.d;
     bool stored = !f.bad;
     int page = 0, within = 0;
@@ -186,14 +213,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         stored = false;
       }
     }
-    const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
 
-    // The rows [t0, t0 + chunk_rows) of the block's new tokens: their turns.
+    // The turns of the rows [t0, t0 + chunk_rows), where the block has rows that turn.
+    const bool any_turns = MODE != kNoTurn && part * kWarps < p.h_q + p.h_k;
     auto turn_rows = [&](int t0) {
+      if (MODE == kNoTurn || !any_turns) return;
       __syncthreads();
       const int rows = min(chunk_rows, n - t0);
       for (int i = tid; i < rows * nf; i += kThreads) {
-        const int r = i / nf, fr = i - r * nf;
+        const int r = i / max(nf, 1), fr = i - r * nf;
         int axis = 0;
 #pragma unroll
         for (int a = 0; a < 3; ++a) axis += fr >= p.rot.end[a] ? 1 : 0;
@@ -205,72 +233,136 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       }
       __syncthreads();
     };
-    // This lane's elements of row r (of the chunk from t0 on), turned.
-    auto take = [&](const TensorArg& in, int head, bool turn, int t0, int r, float (&v)[8]) {
-      const T* row = static_cast<const T*>(in.ptr) + static_cast<int64_t>(token0 + t0 + r) * in.ss + head * in.sh;
-      uint4 raw = *reinterpret_cast<const uint4*>(row + at);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+    // The elements of chunk i of this lane (of the rows from t0 on), turned.
+    const int f0 = MODE == kPairs ? at / 2 : (at >= nf ? at - nf : at);
+    const bool turns_here = turned && at < 2 * nf;
+    const int other_lane = MODE != kHalves || !turns_here ? lane : (at >= nf ? lane - nf / 8 : lane + nf / 8);
+    const float side = at >= nf ? 1.f : -1.f;
+    auto take = [&](int i, int t0, float (&v)[8]) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = Pack<T>::unpack(w[i]);
-        v[2 * i] = y.x;
-        v[2 * i + 1] = y.y;
+      for (int k = 0; k < 4; ++k) {
+        const float2 y = Pack<T>::unpack(w[k]);
+        v[2 * k] = y.x;
+        v[2 * k + 1] = y.y;
       }
-      if (!turn || at >= 2 * nf) return;
+      if (MODE == kNoTurn || !turned) return;
+      const int r = r0 + i * rpw;  // stays within the turns' room; what is not a row is not used
       const float2* t = cs + r * nf;
-      if (g.mode == kPairs) {
+      if (MODE == kHalves) {
+        uint32_t ow[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (at / 2 + i < nf) {
-            const float2 a = t[at / 2 + i];
-            const float x0 = v[2 * i], x1 = v[2 * i + 1];
-            v[2 * i] = x0 * a.x - x1 * a.y;
-            v[2 * i + 1] = x0 * a.y + x1 * a.x;
+        for (int k = 0; k < 4; ++k) ow[k] = __shfl_sync(0xffffffffu, w[k], other_lane);
+        if (turns_here) {
+          const float4* t4 = reinterpret_cast<const float4*>(t + f0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 y = Pack<T>::unpack(ow[k]);
+            const float4 a = t4[k];
+            v[2 * k] = v[2 * k] * a.x + y.x * (side * a.y);
+            v[2 * k + 1] = v[2 * k + 1] * a.z + y.y * (side * a.w);
           }
-      } else if (g.mode == kHalves) {
-        const bool second = at >= nf;
-        const uint4 other = *reinterpret_cast<const uint4*>(row + at + (second ? -nf : nf));
-        const uint32_t* ow = reinterpret_cast<const uint32_t*>(&other);
-        const int f0 = second ? at - nf : at;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = Pack<T>::unpack(ow[i]);
-          const float2 a = t[f0 + 2 * i], bb = t[f0 + 2 * i + 1];
-          v[2 * i] = v[2 * i] * a.x + y.x * (second ? a.y : -a.y);
-          v[2 * i + 1] = v[2 * i + 1] * bb.x + y.y * (second ? bb.y : -bb.y);
         }
-      } else {
-        float o[8];
+      } else if (MODE == kPairs) {
+        if (turns_here)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = at + i;
-          const uint16_t y = e < 2 * nf ? reinterpret_cast<const uint16_t*>(row)[e < nf ? e + nf : e - nf] : 0;
-          o[i] = Pack<T>::unpack(y).x;
-        }
+          for (int k = 0; k < 4; ++k)
+            if (f0 + k < nf) {
+              const float2 a = t[f0 + k];
+              const float x0 = v[2 * k], x1 = v[2 * k + 1];
+              v[2 * k] = x0 * a.x - x1 * a.y;
+              v[2 * k + 1] = x0 * a.y + x1 * a.x;
+            }
+      } else if (turns_here && t0 + r < n) {
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(src + t0 * in.ss + i * row_step) - at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = at + i;
+        for (int k = 0; k < 8; ++k) {
+          const int e = at + k;
           if (e < 2 * nf) {
+            const float y = Pack<T>::unpack(static_cast<uint32_t>(row[e < nf ? e + nf : e - nf])).x;
             const float2 a = t[e < nf ? e : e - nf];
-            v[i] = v[i] * a.x + o[i] * (e < nf ? -a.y : a.y);
+            v[k] = v[k] * a.x + y * (e < nf ? -a.y : a.y);
           }
         }
       }
     };
-    auto largest = [&](const float (&v)[8], float top) {  // of the finite ones
+
+    const bool held = n <= chunk_rows;
+    if (is_q) {
+      for (int t0 = 0; t0 < n; t0 += chunk_rows) {
+        if (t0 > 0) ask(t0);
+        turn_rows(t0);
+        const int rows = on ? n - t0 - r0 : 0;
+        T* to = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + static_cast<int64_t>(token0 + t0 + r0) * p.oq.ss + head * p.oq.sh + at;
+        if (MODE == kMixed) {  // every lane reads its pairs' other elements before one is written: oq may be q
+          uint4 done[kHeld];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = fabsf(v[i]);
-        top = y < INFINITY ? fmaxf(top, y) : top;
+          for (int i = 0; i < kHeld; ++i) {
+            float v[8];
+            take(i, t0, v);
+            done[i] = make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]), Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i)
+            if (i * rpw < rows) *reinterpret_cast<uint4*>(to + i * p.oq.ss * rpw) = done[i];
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          if (i * rpw >= n - t0) break;
+          float v[8];
+          take(i, t0, v);
+          if (i * rpw < rows)
+            *reinterpret_cast<uint4*>(to + i * p.oq.ss * rpw) =
+                make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]), Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
+        }
       }
-      return top;
-    };
-    // A head's factor, from its new tokens' largest value; its earlier codes follow it.
-    auto settle = [&](const TensorArg& pages, float* scales, const int64_t (&st)[3], int head, float top) {
+      if (!held)
+        for (int t0 = 0; t0 < n; t0 += chunk_rows) turn_rows(t0);  // with the block's other warps
+      continue;
+    }
+
+    // ---- the largest value of the new tokens, by their bits; what is not finite lies above kInf
+    constexpr uint32_t kInf = 0x7f800000u;
+    uint32_t top = 0, most = 0;  // of the finite ones, of all
+    auto compare = [&](int t0, bool finite) {
 #pragma unroll
-      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-      float* s = scales + page * st[0] + blk * st[1] + head * st[2];
-      float now = factor_of<INT8>(top);
+      for (int i = 0; i < kHeld; ++i) {
+        if (i * rpw >= n - t0) break;
+        float v[8];
+        take(i, t0, v);
+        if (on && t0 + r0 + i * rpw < n)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t y = __float_as_uint(v[k]) & 0x7fffffffu;
+            if (finite) top = y < kInf ? max(top, y) : top;
+            else most = max(most, y);
+          }
+      }
+    };
+    for (int t0 = 0; t0 < n; t0 += chunk_rows) {
+      if (t0 > 0) ask(t0);
+      turn_rows(t0);
+      compare(t0, false);
+      if (!held) compare(t0, true);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (held) {
+      if (most < kInf) top = most;
+      else compare(0, true);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+
+    // ---- the head's factor; its earlier codes follow it
+    const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
+    char* to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
+    float now = factor_of<INT8>(__uint_as_float(top));
+    if (j >= jobs) stored = false;
+    if (stored) {
+      const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
+      const int64_t* st = is_v ? p.cache.vs : p.cache.ks;
+      float* s = (is_v ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1] + head * st[2];
       if (old > 0) {
         float was = *s;
         was = was > 0.f ? fminf(was, kLargest) : 0.f;
@@ -278,108 +370,48 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         if (now > was) {
           const float ratio = was / now;
           const int per_row = p.head_dim / 16;
-          char* rows = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
           for (int i = lane; i < old * per_row; i += 32) {
             const int r = i / per_row;
-            uint4* to = reinterpret_cast<uint4*>(rows + r * pages.ss) + (i - r * per_row);
-            uint4 codes = *to;
+            uint4* at16 = reinterpret_cast<uint4*>(to + r * pages.ss) + (i - r * per_row);
+            uint4 codes = *at16;
             uint32_t* w = reinterpret_cast<uint32_t*>(&codes);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float4 y = value4<INT8>(w[k]);
-              w[k] = code4<INT8>(y.x * ratio, y.y * ratio, y.z * ratio, y.w * ratio);
+              w[k] = code4<INT8>(y.x, y.y, y.z, y.w, ratio);
             }
-            *to = codes;
+            *at16 = codes;
           }
         } else {
           now = was;
         }
       }
       if (lane == 0) *s = now;
-      return 1.f / now;
-    };
-    auto put8 = [&](const TensorArg& pages, int head, int r, const float (&v)[8], float inv) {
-      char* to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb +
-                 static_cast<int64_t>(within + old + r) * pages.ss + head * pages.sh + at;
-      *reinterpret_cast<uint2*>(to) = make_uint2(code4<INT8>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                                                 code4<INT8>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    };
-    auto put16 = [&](int head, int r, const float (&v)[8]) {
-      T* to = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + static_cast<int64_t>(token0 + r) * p.oq.ss + head * p.oq.sh + at;
-      *reinterpret_cast<uint4*>(to) = make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]),
-                                                 Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
-    };
-
-    const bool turns_any = nf > 0 && j0 < p.h_q + p.h_k;
-    const bool held = n <= chunk_rows;
-    if (!held && j1 > p.h_q && stored) {
-      // ---- more rows than the registers hold: their largest values first
-      for (int j = j0 + warp; j < j1; j += kWarps)
-        if (lane == 0 && j >= p.h_q) s_top[j - p.h_q] = 0.f;
-      for (int t0 = 0; t0 < n; t0 += chunk_rows) {
-        if (turns_any) turn_rows(t0);
-        for (int j = j0 + warp; j < j1; j += kWarps) {
-          if (j < p.h_q) continue;
-          const bool is_v = j >= p.h_q + p.h_k;
-          const int head = j - p.h_q - (is_v ? p.h_k : 0);
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < kHeld; ++i) {
-            const int r = r0 + i * rpw;
-            float v[8];
-            if (on && t0 + r < n) {
-              take(is_v ? p.v : p.k, head, !is_v && nf > 0, t0, r, v);
-              top = largest(v, top);
-            }
-          }
-#pragma unroll
-          for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-          if (lane == 0) s_top[j - p.h_q] = fmaxf(s_top[j - p.h_q], top);
-          __syncwarp();
-        }
-      }
     }
-    for (int t0 = 0; t0 < n; t0 += chunk_rows) {
-      if (turns_any) turn_rows(t0);
-      for (int j = j0 + warp; j < j1; j += kWarps) {
-        const bool is_q = j < p.h_q, is_v = j >= p.h_q + p.h_k;
-        const int head = is_q ? j : j - p.h_q - (is_v ? p.h_k : 0);
-        if (!is_q && !stored) continue;
-        const TensorArg& in = is_q ? p.q : (is_v ? p.v : p.k);
-        float v[kHeld][8];
-        float top = 0.f;
+
+    // ---- codes
+    const float inv = 1.f / now;
+    to += old * pages.ss + at;
+    auto put = [&](int t0, auto clean) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          const int r = r0 + i * rpw;
-          if (on && t0 + r < n) {
-            take(in, head, !is_v && nf > 0, t0, r, v[i]);
-            top = largest(v[i], top);
-          }
-        }
-        if (is_q) {
-          __syncwarp();  // every lane has read its pairs' other elements: oq may be q
-#pragma unroll
-          for (int i = 0; i < kHeld; ++i)
-            if (on && t0 + r0 + i * rpw < n) put16(head, t0 + r0 + i * rpw, v[i]);
-          continue;
-        }
-        const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
-        float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
-        float inv;
-        if (t0 == 0) {
-          inv = settle(pages, scales, is_v ? p.cache.vs : p.cache.ks, head, held ? top : s_top[j - p.h_q]);
-          if (!held) {
-            __syncwarp();
-            if (lane == 0) s_top[j - p.h_q] = inv;
-            __syncwarp();
-          }
-        } else {
-          inv = s_top[j - p.h_q];
-        }
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-          if (on && t0 + r0 + i * rpw < n) put8(pages, head, t0 + r0 + i * rpw, v[i], inv);
+      for (int i = 0; i < kHeld; ++i) {
+        if (i * rpw >= n - t0) break;
+        float v[8];
+        take(i, t0, v);
+        const int r = t0 + r0 + i * rpw;
+        if (on && r < n && stored)
+          *reinterpret_cast<uint2*>(to + r * pages.ss) =
+              make_uint2(code4<INT8, clean.value>(v[0], v[1], v[2], v[3], inv), code4<INT8, clean.value>(v[4], v[5], v[6], v[7], inv));
       }
+    };
+    for (int t0 = 0; t0 < n; t0 += chunk_rows) {
+      if (!held) {
+        ask(t0);
+        turn_rows(t0);
+      }
+      // (a factor at its upper bound leaves values beyond the largest code)
+      if (INT8 && most < kInf && now < kLargest) put(t0, std::true_type());
+      else put(t0, std::false_type());
     }
   }
 }
@@ -455,20 +487,21 @@ cudaError_t launch_append(const Append8Params& p, cudaStream_t stream) {
   const int chunks = p.head_dim / 8, nf = p.rot.n_freq;
   g.lanes_log2 = 0;
   while ((1 << g.lanes_log2) < chunks) ++g.lanes_log2;
-  g.mode = p.rot.positions == nullptr ? kNoTurn : (p.rot.interleaved ? kPairs : (nf % 8 == 0 ? kHalves : kMixed));
+  const int mode = p.rot.positions == nullptr ? kNoTurn : (p.rot.interleaved ? kPairs : (nf % 8 == 0 ? kHalves : kMixed));
   const int64_t most = static_cast<int64_t>(num_sms()) * kBlocks;
   const int64_t seqs = p.batch < p.tokens ? p.batch : p.tokens;
   int64_t units = p.tokens / static_cast<int64_t>(p.cache.block.d) + 2 * seqs;
   if (units > p.tokens) units = p.tokens;
-  // few blocks of tokens: several blocks share the heads of each, down to one for each warp
   const int64_t jobs = static_cast<int64_t>(p.h_q) + 2 * static_cast<int64_t>(p.h_k);
-  const int64_t fit = (jobs + kWarps - 1) / kWarps;
-  int64_t parts = most / units;
-  parts = parts < 1 ? 1 : (parts > fit ? fit : parts);
-  g.parts = static_cast<int>(parts);
-  const int64_t grid = units * parts;
-  const size_t smem = static_cast<size_t>(p.h_k) * 2 * sizeof(float);
-  append8_kernel<T, INT8><<<static_cast<unsigned>(grid < most ? grid : most), kThreads, smem, stream>>>(p, g);
+  g.parts.set(static_cast<uint32_t>((jobs + kWarps - 1) / kWarps));
+  const int64_t items = units * g.parts.d;
+  const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  switch (mode) {
+    case kNoTurn: append8_kernel<T, INT8, kNoTurn><<<grid, kThreads, 0, stream>>>(p, g); break;
+    case kHalves: append8_kernel<T, INT8, kHalves><<<grid, kThreads, 0, stream>>>(p, g); break;
+    case kPairs: append8_kernel<T, INT8, kPairs><<<grid, kThreads, 0, stream>>>(p, g); break;
+    default: append8_kernel<T, INT8, kMixed><<<grid, kThreads, 0, stream>>>(p, g); break;
+  }
   return cudaGetLastError();
 }
 

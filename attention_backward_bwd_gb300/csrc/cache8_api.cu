@@ -78,7 +78,8 @@ int attn_cache_append8(const attn_tensor* q, const attn_tensor* oq, const attn_t
     return fail(ATTN_ERR_ARG, "q is only taken to be rotated: give rotary, or no q");
   int rc = check_heads(dtype, batch, with_q ? h_q : h_k, h_k, head_dim);
   if (rc) return rc;
-  if (h_k > 4096) return fail(ATTN_ERR_SHAPE, "at most 4096 key/value heads, got %d", h_k);
+  if (static_cast<int64_t>(h_q) + 2 * static_cast<int64_t>(h_k) > INT32_MAX / 2)
+    return fail(ATTN_ERR_SHAPE, "h_q + 2 h_k must stay below 2^30");
   if (tokens < 0) return fail(ATTN_ERR_SHAPE, "tokens must be >= 0, got %d", tokens);
   if (cu_seqlens == nullptr && tokens != batch)
     return fail(ATTN_ERR_ARG, "without cu_seqlens there is one token a sequence: got %d tokens, %d "

@@ -43,7 +43,7 @@ typedef struct {
  * the nearest ones, ties to even; what lies beyond the largest code becomes it, a NaN stays one
  * in e4m3 and becomes 0 in int8.  k is rounded once, from its rotation in fp32.  Tokens whose
  * slot or page is bad are left out and reported as there.  cu_seqlens that do not ascend are
- * reported and their sequences left out.  At most 4096 key/value heads.
+ * reported and their sequences left out.
  */
 int attn_cache_append8(const attn_tensor* q, const attn_tensor* oq, const attn_tensor* k,
                        const attn_tensor* v, int dtype, int tokens, int batch, int h_q, int h_k,

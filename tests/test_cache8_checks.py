@@ -111,7 +111,7 @@ CASES = [(f, kw, code) for f in (append, load, decode) for kw, code in BAD_CACHE
     (append, dict(rot=rotary(inverse=1)), ARG), (append, dict(rot=rotary(n=33, sec=(33, 0, 0, 0))), SHAPE),
     (append, dict(n=None), NULL), (append, dict(n=P + 1), ALIGN), (append, dict(k=T(s=60)), STRIDE),
     (append, dict(v=T(ptr=0)), NULL), (append, dict(q=T(ptr=P + 4)), ALIGN),
-    (append, dict(hk=4097, hq=4097), SHAPE),
+    (append, dict(hk=1 << 29, hq=1 << 29), SHAPE),
     (load, dict(dt=3), DTYPE), (load, dict(t=-1), SHAPE), (load, dict(at=None), NULL), (load, dict(cu=None), NULL),
     (load, dict(cu=P + 2), ALIGN), (load, dict(k=T(ptr=0)), NULL), (load, dict(v=T(h=20)), STRIDE),
     (decode, dict(hq=3), SHAPE), (decode, dict(most=129), ARG), (decode, dict(most=-1), ARG),
