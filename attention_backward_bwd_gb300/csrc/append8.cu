@@ -115,13 +115,14 @@ __device__ __forceinline__ int blocks_of(const Append8Params& p, const Fresh& f)
 
 template <typename T, bool INT8, int MODE>
 __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Params p, Append8Grid g) {
-  __shared__ float2 cs[MODE == kNoTurn ? 1 : kTurns];  // (cos, sin) of [row][frequency]
+  __shared__ __align__(16) float2 cs[MODE == kNoTurn ? 1 : kTurns];  // (cos, sin) of [row][frequency]
   __shared__ unsigned long long turns[128];
   __shared__ int64_t s_pre[kThreads];  // (offsets that do not ascend may name a token often)
   __shared__ int64_t s_sums[kWarps];
   __shared__ int4 s_fresh[kThreads];   // of the first sequence of each thread: first, n, len, bad
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq;
+  // turns of a row: the last ones, up to a multiple of 4, turn by nothing
+  const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq, pitch = MODE == kNoTurn ? 4 : (nf + 3) / 4 * 4;
 
   // fraction of a turn that one position adds at each frequency, times 2^64
   for (int i = tid; i < nf; i += kThreads) {
@@ -220,15 +221,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       if (MODE == kNoTurn || !any_turns) return;
       __syncthreads();
       const int rows = min(chunk_rows, n - t0);
-      for (int i = tid; i < rows * nf; i += kThreads) {
-        const int r = i / max(nf, 1), fr = i - r * nf;
-        int axis = 0;
+      for (int i = tid; i < rows * pitch; i += kThreads) {
+        const int r = i / pitch, fr = i - r * pitch;
+        float sn = 0.f, cn = 1.f;
+        if (fr < nf) {
+          int axis = 0;
 #pragma unroll
-        for (int a = 0; a < 3; ++a) axis += fr >= p.rot.end[a] ? 1 : 0;
-        const long long pos = p.rot.positions[axis * p.rot.axis_stride + token0 + t0 + r];
-        const unsigned long long phase = static_cast<unsigned long long>(pos) * turns[fr];
-        float sn, cn;
-        sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &sn, &cn);
+          for (int a = 0; a < 3; ++a) axis += fr >= p.rot.end[a] ? 1 : 0;
+          const long long pos = p.rot.positions[axis * p.rot.axis_stride + token0 + t0 + r];
+          const unsigned long long phase = static_cast<unsigned long long>(pos) * turns[fr];
+          sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &sn, &cn);
+        }
         cs[i] = make_float2(cn, sn);
       }
       __syncthreads();
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       }
       if (MODE == kNoTurn || !turned) return;
       const int r = r0 + i * rpw;  // stays within the turns' room; what is not a row is not used
-      const float2* t = cs + r * nf;
+      const float2* t = cs + r * pitch;
       if (MODE == kHalves) {
         uint32_t ow[4];
 #pragma unroll
@@ -264,15 +267,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
           }
         }
       } else if (MODE == kPairs) {
-        if (turns_here)
+        if (turns_here) {
+          const float4* t4 = reinterpret_cast<const float4*>(t + f0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (f0 + k < nf) {
-              const float2 a = t[f0 + k];
-              const float x0 = v[2 * k], x1 = v[2 * k + 1];
-              v[2 * k] = x0 * a.x - x1 * a.y;
-              v[2 * k + 1] = x0 * a.y + x1 * a.x;
-            }
+          for (int k = 0; k < 2; ++k) {
+            const float4 a = t4[k];
+            const float x0 = v[4 * k], x1 = v[4 * k + 1], x2 = v[4 * k + 2], x3 = v[4 * k + 3];
+            v[4 * k] = x0 * a.x - x1 * a.y;
+            v[4 * k + 1] = x0 * a.y + x1 * a.x;
+            v[4 * k + 2] = x2 * a.z - x3 * a.w;
+            v[4 * k + 3] = x2 * a.w + x3 * a.z;
+          }
+        }
       } else if (turns_here && t0 + r < n) {
         const uint16_t* row = reinterpret_cast<const uint16_t*>(src + t0 * in.ss + i * row_step) - at;
 #pragma unroll
@@ -323,41 +329,59 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       continue;
     }
 
-    // ---- the largest value of the new tokens, by their bits; what is not finite lies above kInf
-    constexpr uint32_t kInf = 0x7f800000u;
-    uint32_t top = 0, most = 0;  // of the finite ones, of all
-    auto compare = [&](int t0, bool finite) {
+    // ---- the largest value of the new tokens (rows that are none are zeros)
+    constexpr uint32_t kInf = 0x7f800000u, kInf16 = Pack<T>::kIsBf16 ? 0x7f80u : 0x7c00u;
+    float top = 0.f;
+    bool clean = true;  // all are finite
+    auto compare = [&](int t0) {
+      if (!turned) {  // two at a time, as bits: as numbers that are not negative they have the same order
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          if (i * rpw >= n - t0) break;
+          most = __vmaxu2(__vmaxu2(most, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu)),
+                          __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+        }
+        const uint32_t one = max(most & 0xffffu, most >> 16);
+        if (one >= kInf16) clean = false;
+        else top = fmaxf(top, Pack<T>::unpack(one).x);
+      } else {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          if (i * rpw >= n - t0) break;
+          float v[8];
+          take(i, t0, v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
+        }
+        if (most >= kInf) clean = false;
+        else top = fmaxf(top, __uint_as_float(most));
+      }
+    };
+    auto compare_finite = [&](int t0) {  // one by one
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
         if (i * rpw >= n - t0) break;
         float v[8];
         take(i, t0, v);
-        if (on && t0 + r0 + i * rpw < n)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t y = __float_as_uint(v[k]) & 0x7fffffffu;
-            if (finite) top = y < kInf ? max(top, y) : top;
-            else most = max(most, y);
-          }
+        for (int k = 0; k < 8; ++k) top = fabsf(v[k]) < INFINITY ? fmaxf(top, fabsf(v[k])) : top;
       }
     };
     for (int t0 = 0; t0 < n; t0 += chunk_rows) {
       if (t0 > 0) ask(t0);
       turn_rows(t0);
-      compare(t0, false);
-      if (!held) compare(t0, true);
+      compare(t0);
+      clean = __all_sync(0xffffffffu, clean);
+      if (!clean) compare_finite(t0);
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (held) {
-      if (most < kInf) top = most;
-      else compare(0, true);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 
     // ---- the head's factor; its earlier codes follow it
     const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
     char* to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
-    float now = factor_of<INT8>(__uint_as_float(top));
+    float now = factor_of<INT8>(top);
     if (j >= jobs) stored = false;
     if (stored) {
       const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
@@ -392,16 +416,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
     // ---- codes
     const float inv = 1.f / now;
     to += old * pages.ss + at;
-    auto put = [&](int t0, auto clean) {
+    auto put = [&](int t0, auto fits) {
+      const int rows = on && stored ? n - t0 - r0 : 0;
+      char* out = to + (t0 + r0) * pages.ss;
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
         if (i * rpw >= n - t0) break;
         float v[8];
         take(i, t0, v);
-        const int r = t0 + r0 + i * rpw;
-        if (on && r < n && stored)
-          *reinterpret_cast<uint2*>(to + r * pages.ss) =
-              make_uint2(code4<INT8, clean.value>(v[0], v[1], v[2], v[3], inv), code4<INT8, clean.value>(v[4], v[5], v[6], v[7], inv));
+        if (i * rpw < rows)
+          *reinterpret_cast<uint2*>(out) =
+              make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], inv), code4<INT8, fits.value>(v[4], v[5], v[6], v[7], inv));
+        out += pages.ss * rpw;
       }
     };
     for (int t0 = 0; t0 < n; t0 += chunk_rows) {
@@ -410,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         turn_rows(t0);
       }
       // (a factor at its upper bound leaves values beyond the largest code)
-      if (INT8 && most < kInf && now < kLargest) put(t0, std::true_type());
+      if (INT8 && clean && now < kLargest) put(t0, std::true_type());
       else put(t0, std::false_type());
     }
   }
