@@ -12,8 +12,10 @@
 // asks for its rows first (up to kHeld 16-byte chunks of a lane), then the block's threads compute
 // the turns of the tokens, and the rows stay in registers as they came: they are turned once for
 // their largest value and once more when they are rounded, so that k and v are read once.  Tokens
-// beyond kHeld chunks a lane are read a second time, from the L2.
+// Warps share the tokens of a row of heads where they are more; what is beyond that, too, is read a
+// second time, from the L2.
 // Read-back.  A warp takes a token: 16 codes a lane, 32 bytes out.
+#include <atomic>
 #include <type_traits>
 
 #include "cache.h"
@@ -26,8 +28,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeld = 16;      // chunks of a lane in registers
-constexpr int kTurns = 2048;   // turns of the rows that a block takes at once
+constexpr int kTurns = 2048;   // turns of the rows that a warp takes at once
 constexpr int kBlocks = 2;     // of an SM
+constexpr int kMostShares = 2; // log2 of the warps that share tokens
 constexpr float kLargest = 1.152921504606847e18f;    // 2^60
 
 // Where the other element of a pair is: kHalves in the lane n_freq / 8 further (n_freq a multiple
@@ -36,7 +39,8 @@ enum RopeMode { kNoTurn = 0, kHalves = 1, kPairs = 2, kMixed = 3 };
 
 struct Append8Grid {
   int lanes_log2;        // lanes of a row
-  FastDiv parts;         // blocks that share the heads of a block of tokens
+  int share_log2;        // warps that share the tokens of a row of heads
+  int parts;             // blocks that share the heads of a block of tokens
 };
 
 // Smallest power of two that `top` is at most 448 (127) times, within the bounds; exact.
@@ -113,13 +117,19 @@ __device__ __forceinline__ int blocks_of(const Append8Params& p, const Fresh& f)
   return n <= rest ? 1 : 2 + static_cast<int>(p.cache.block.div(n - rest - 1));
 }
 
+// Barrier of the warps that share a row of heads.
+__device__ __forceinline__ void share_barrier(int which, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(which + 1), "r"(threads) : "memory");
+}
+
 template <typename T, bool INT8, int MODE>
 __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Params p, Append8Grid g) {
-  __shared__ __align__(16) float2 cs[MODE == kNoTurn ? 1 : kTurns];  // (cos, sin) of [row][frequency]
+  extern __shared__ __align__(16) float2 cs[];  // (cos, sin) of [row][frequency]
   __shared__ unsigned long long turns[128];
   __shared__ int64_t s_pre[kThreads];  // (offsets that do not ascend may name a token often)
   __shared__ int64_t s_sums[kWarps];
   __shared__ int4 s_fresh[kThreads];   // of the first sequence of each thread: first, n, len, bad
+  __shared__ float2 s_top[2][kWarps];  // largest value and whether all are finite, of every other row of heads
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // turns of a row: the last ones, up to a multiple of 4, turn by nothing
   const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq, pitch = MODE == kNoTurn ? 4 : (nf + 3) / 4 * 4;
@@ -154,14 +164,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   s_pre[tid] = before + x - mine;
   __syncthreads();
 
-  const int lanes = 1 << g.lanes_log2, rpw = 32 >> g.lanes_log2, chunk_rows = kHeld * rpw;
-  const int c = lane & (lanes - 1), r0 = lane >> g.lanes_log2, at = 8 * c;
+  const int lanes = 1 << g.lanes_log2, rpw = 32 >> g.lanes_log2, chunk_rows = (kHeld * rpw) << g.share_log2;
+  // this warp's first row of a chunk, and this lane's
+  const int member = warp & ((1 << g.share_log2) - 1), w0 = member * kHeld * rpw;
+  const int c = lane & (lanes - 1), r0 = w0 + (lane >> g.lanes_log2), at = 8 * c;
+  int parity = 0;
   const bool on = at < p.head_dim;
-  const int jobs = p.h_q + 2 * p.h_k;
-  const int64_t items = total * g.parts.d;
+  const int jobs = p.h_q + 2 * p.h_k, at_once = kWarps >> g.share_log2;
+  const int64_t items = total * g.parts;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t u = items <= INT32_MAX ? g.parts.div(static_cast<uint32_t>(item)) : item / g.parts.d;
-    const int part = static_cast<int>(item - u * g.parts.d);
+    const int64_t u = g.parts == 1 ? item : item / g.parts;
+    const int part = static_cast<int>(item - u * g.parts);
+    const int j0 = static_cast<int>(static_cast<int64_t>(jobs) * part / g.parts);
+    const int j1 = static_cast<int>(static_cast<int64_t>(jobs) * (part + 1) / g.parts);
     // ---- the sequence and the block of tokens
     int lo = 0, hi = kThreads - 1;
     while (lo < hi) {
@@ -180,43 +195,45 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
     const int64_t from = base > f.len ? base : f.len, end = min(base + size, static_cast<int64_t>(f.len) + f.n);
     const int token0 = f.first + static_cast<int>(from - f.len), n = static_cast<int>(end - from);
     const int old = static_cast<int>(from - base);  // earlier tokens of the block
-
-    // ---- this warp's row of heads, on its way
-    const int j = part * kWarps + warp;
-    const bool is_q = j < p.h_q, is_v = j >= p.h_q + p.h_k, turned = MODE != kNoTurn && !is_v;
-    const int head = is_q ? j : j - p.h_q - (is_v ? p.h_k : 0);
-    const TensorArg& in = is_q ? p.q : (is_v ? p.v : p.k);
-    const int64_t row_step = in.ss * rpw;
-    const T* src = static_cast<const T*>(in.ptr) + static_cast<int64_t>(token0 + r0) * in.ss + head * in.sh + at;
-    uint4 raw[kHeld];
-    auto ask = [&](int t0) {
-      const int rows = on && j < jobs ? n - t0 - r0 : 0;
-      const T* s = src + t0 * in.ss;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        raw[i] = i * rpw < rows ? *reinterpret_cast<const uint4*>(s + i * row_step) : make_uint4(0, 0, 0, 0);
-    };
-    ask(0);
-
     const int64_t cap = static_cast<int64_t>(p.cache.pages.max_pages) * p.cache.pages.page.d;
-    bool stored = !f.bad;
+    bool stored = !f.bad && base < cap;
     int page = 0, within = 0;
-    if (stored && base >= cap) {
-      if (tid == 0 && part == 0) report(p.status, kBadLength);
-      stored = false;
-    }
     if (stored) {
       const int pg = static_cast<int>(p.cache.pages.page.div(static_cast<uint32_t>(base)));
       within = static_cast<int>(base) - pg * static_cast<int>(p.cache.pages.page.d);
       page = p.cache.pages.table[b * p.cache.pages.table_stride + pg];
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.cache.pages.num_pages)) {
-        if (tid == 0 && part == 0) report(p.status, kBadPage);
-        stored = false;
-      }
     }
+    const bool held = n <= chunk_rows;
+
+    // ---- rows of heads, one a warp (or a part of it) at a time
+    int j = j0 + (warp >> g.share_log2), head;
+    bool is_q, is_v, turned;
+    const T* src;      // this lane's element of the row of heads, of its first token
+    int64_t row_step;
+    uint4 raw[kHeld];
+    auto ask = [&](int t0) {
+      const int rows = on && j < j1 ? n - t0 - r0 : 0;
+      const T* s = src + t0 * (row_step >> (5 - g.lanes_log2));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        raw[i] = i * rpw < rows ? *reinterpret_cast<const uint4*>(s) : make_uint4(0, 0, 0, 0);
+        s += row_step;
+      }
+    };
+    auto begin = [&]() {
+      is_q = j < p.h_q;
+      is_v = j >= p.h_q + p.h_k;
+      turned = MODE != kNoTurn && !is_v;
+      head = is_q ? j : j - p.h_q - (is_v ? p.h_k : 0);
+      const TensorArg& in = is_q ? p.q : (is_v ? p.v : p.k);
+      row_step = in.ss * rpw;
+      src = static_cast<const T*>(in.ptr) + static_cast<int64_t>(token0 + r0) * in.ss + head * in.sh + at;
+      ask(0);
+    };
+    begin();
 
     // The turns of the rows [t0, t0 + chunk_rows), where the block has rows that turn.
-    const bool any_turns = MODE != kNoTurn && part * kWarps < p.h_q + p.h_k;
+    const bool any_turns = MODE != kNoTurn && j0 < p.h_q + p.h_k;
     auto turn_rows = [&](int t0) {
       if (MODE == kNoTurn || !any_turns) return;
       __syncthreads();
@@ -236,11 +253,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
       }
       __syncthreads();
     };
+    if (held) turn_rows(0);
+    if (stored && static_cast<unsigned>(page) >= static_cast<unsigned>(p.cache.pages.num_pages)) {
+      if (tid == 0 && part == 0) report(p.status, kBadPage);
+      stored = false;
+    } else if (!stored && !f.bad) {
+      if (tid == 0 && part == 0) report(p.status, kBadLength);
+    }
+    const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
+
     // The elements of chunk i of this lane (of the rows from t0 on), turned.
     const int f0 = MODE == kPairs ? at / 2 : (at >= nf ? at - nf : at);
-    const bool turns_here = turned && at < 2 * nf;
-    const int other_lane = MODE != kHalves || !turns_here ? lane : (at >= nf ? lane - nf / 8 : lane + nf / 8);
     const float side = at >= nf ? 1.f : -1.f;
+    const bool in_turns = at < 2 * nf;
+    const int other_lane = MODE != kHalves || !in_turns ? lane : (at >= nf ? lane - nf / 8 : lane + nf / 8);
     auto take = [&](int i, int t0, float (&v)[8]) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
 #pragma unroll
@@ -250,13 +276,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         v[2 * k + 1] = y.y;
       }
       if (MODE == kNoTurn || !turned) return;
-      const int r = r0 + i * rpw;  // stays within the turns' room; what is not a row is not used
+      const int r = min(r0 + i * rpw, n - t0 - 1);  // (what is not a row is zeros)
       const float2* t = cs + r * pitch;
       if (MODE == kHalves) {
         uint32_t ow[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) ow[k] = __shfl_sync(0xffffffffu, w[k], other_lane);
-        if (turns_here) {
+        if (in_turns) {
           const float4* t4 = reinterpret_cast<const float4*>(t + f0);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -267,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
           }
         }
       } else if (MODE == kPairs) {
-        if (turns_here) {
+        if (in_turns) {
           const float4* t4 = reinterpret_cast<const float4*>(t + f0);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -279,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             v[4 * k + 3] = x2 * a.w + x3 * a.z;
           }
         }
-      } else if (turns_here && t0 + r < n) {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(src + t0 * in.ss + i * row_step) - at;
+      } else if (in_turns && t0 + r0 + i * rpw < n) {
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(src + t0 * (row_step >> (5 - g.lanes_log2)) + i * row_step) - at;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int e = at + k;
@@ -292,152 +318,166 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         }
       }
     };
+    auto pack16 = [&](const float (&v)[8]) {
+      return make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]), Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
+    };
 
-    const bool held = n <= chunk_rows;
-    if (is_q) {
-      for (int t0 = 0; t0 < n; t0 += chunk_rows) {
-        if (t0 > 0) ask(t0);
-        turn_rows(t0);
-        const int rows = on ? n - t0 - r0 : 0;
-        T* to = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + static_cast<int64_t>(token0 + t0 + r0) * p.oq.ss + head * p.oq.sh + at;
-        if (MODE == kMixed) {  // every lane reads its pairs' other elements before one is written: oq may be q
-          uint4 done[kHeld];
-#pragma unroll
-          for (int i = 0; i < kHeld; ++i) {
-            float v[8];
-            take(i, t0, v);
-            done[i] = make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]), Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
+    const int rounds = (j1 - j0 + at_once - 1) / at_once;  // the same for all warps: some steps are block-wide
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+      if (round > 0) {
+        j += at_once;
+        begin();
+      }
+      // of k and v: the factor of the block's earlier tokens
+      float* factor = nullptr;
+      float was = 0.f;
+      if (stored && !is_q && j < j1) {
+        const int64_t* st = is_v ? p.cache.vs : p.cache.ks;
+        factor = (is_v ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1] + head * st[2];
+        if (old > 0) was = *factor;
+      }
+      float top = 0.f, inv = 0.f;
+      bool clean = true;  // all are finite
+      char* to = nullptr;
+      int64_t step = 0;
+      // Tokens that are not held pass twice: for their largest value, and to be rounded.
+      const int passes = held ? 1 : 2;
+#pragma unroll 1
+      for (int pass = 0; pass < passes; ++pass) {
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += chunk_rows) {
+          if (!held) {
+            if (pass > 0 || t0 > 0) ask(t0);
+            turn_rows(t0);
           }
-          __syncwarp();
+          const int left = n - t0 - w0;            // rows from this warp's first on
+          const int rows = on && j < j1 ? n - t0 - r0 : 0;  // from this lane's
+          if (is_q) {
+            if (pass > 0) continue;
+            T* out = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + static_cast<int64_t>(token0 + t0 + r0) * p.oq.ss +
+                     head * p.oq.sh + at;
+            const int64_t out_step = p.oq.ss * rpw;
+            if (MODE == kMixed) {  // every lane reads its pairs' other elements before one is written: oq may be q
 #pragma unroll
-          for (int i = 0; i < kHeld; ++i)
-            if (i * rpw < rows) *reinterpret_cast<uint4*>(to + i * p.oq.ss * rpw) = done[i];
-          continue;
-        }
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          if (i * rpw >= n - t0) break;
-          float v[8];
-          take(i, t0, v);
-          if (i * rpw < rows)
-            *reinterpret_cast<uint4*>(to + i * p.oq.ss * rpw) =
-                make_uint4(Pack<T>::two(v[0], v[1]), Pack<T>::two(v[2], v[3]), Pack<T>::two(v[4], v[5]), Pack<T>::two(v[6], v[7]));
-        }
-      }
-      if (!held)
-        for (int t0 = 0; t0 < n; t0 += chunk_rows) turn_rows(t0);  // with the block's other warps
-      continue;
-    }
-
-    // ---- the largest value of the new tokens (rows that are none are zeros)
-    constexpr uint32_t kInf = 0x7f800000u, kInf16 = Pack<T>::kIsBf16 ? 0x7f80u : 0x7c00u;
-    float top = 0.f;
-    bool clean = true;  // all are finite
-    auto compare = [&](int t0) {
-      if (!turned) {  // two at a time, as bits: as numbers that are not negative they have the same order
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          if (i * rpw >= n - t0) break;
-          most = __vmaxu2(__vmaxu2(most, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu)),
-                          __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
-        }
-        const uint32_t one = max(most & 0xffffu, most >> 16);
-        if (one >= kInf16) clean = false;
-        else top = fmaxf(top, Pack<T>::unpack(one).x);
-      } else {
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          if (i * rpw >= n - t0) break;
-          float v[8];
-          take(i, t0, v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
-        }
-        if (most >= kInf) clean = false;
-        else top = fmaxf(top, __uint_as_float(most));
-      }
-    };
-    auto compare_finite = [&](int t0) {  // one by one
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (i * rpw >= n - t0) break;
-        float v[8];
-        take(i, t0, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fabsf(v[k]) < INFINITY ? fmaxf(top, fabsf(v[k])) : top;
-      }
-    };
-    for (int t0 = 0; t0 < n; t0 += chunk_rows) {
-      if (t0 > 0) ask(t0);
-      turn_rows(t0);
-      compare(t0);
-      clean = __all_sync(0xffffffffu, clean);
-      if (!clean) compare_finite(t0);
-    }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-
-    // ---- the head's factor; its earlier codes follow it
-    const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
-    char* to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
-    float now = factor_of<INT8>(top);
-    if (j >= jobs) stored = false;
-    if (stored) {
-      const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
-      const int64_t* st = is_v ? p.cache.vs : p.cache.ks;
-      float* s = (is_v ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1] + head * st[2];
-      if (old > 0) {
-        float was = *s;
-        was = was > 0.f ? fminf(was, kLargest) : 0.f;
-        __syncwarp();
-        if (now > was) {
-          const float ratio = was / now;
-          const int per_row = p.head_dim / 16;
-          for (int i = lane; i < old * per_row; i += 32) {
-            const int r = i / per_row;
-            uint4* at16 = reinterpret_cast<uint4*>(to + r * pages.ss) + (i - r * per_row);
-            uint4 codes = *at16;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&codes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float4 y = value4<INT8>(w[k]);
-              w[k] = code4<INT8>(y.x, y.y, y.z, y.w, ratio);
+              for (int i = 0; i < kHeld; ++i) {
+                float v[8];
+                take(i, t0, v);
+                raw[i] = pack16(v);
+              }
+              __syncwarp();
             }
-            *at16 = codes;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+              if (i * rpw >= left) break;
+              if (MODE != kMixed) {
+                float v[8];
+                take(i, t0, v);
+                raw[i] = pack16(v);
+              }
+              if (i * rpw < rows) *reinterpret_cast<uint4*>(out) = raw[i];
+              out += out_step;
+            }
+            continue;
           }
-        } else {
-          now = was;
+          if (pass == 0) {
+            // ---- the largest value of the new tokens (rows that are none are zeros)
+            constexpr uint32_t kInf = 0x7f800000u, kInf16 = Pack<T>::kIsBf16 ? 0x7f80u : 0x7c00u;
+            uint32_t most = 0;
+            bool fine;
+            if (!turned) {  // two at a time, as bits: as numbers that are not negative they have the same order
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i) {
+                if (i * rpw >= left) break;
+                most = __vmaxu2(__vmaxu2(most, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu)),
+                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+              }
+              most = max(most & 0xffffu, most >> 16);
+              fine = most < kInf16;
+              if (fine) top = fmaxf(top, Pack<T>::unpack(most).x);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i) {
+                if (i * rpw >= left) break;
+                float v[8];
+                take(i, t0, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
+              }
+              fine = most < kInf;
+              if (fine) top = fmaxf(top, __uint_as_float(most));
+            }
+            if (__any_sync(0xffffffffu, !fine)) {  // the finite ones, one by one
+              clean = false;
+#pragma unroll
+              for (int i = 0; i < kHeld; ++i) {
+                if (i * rpw >= left) break;
+                float v[8];
+                take(i, t0, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fabsf(v[k]) < INFINITY ? fmaxf(top, fabsf(v[k])) : top;
+              }
+            }
+            if (!held) continue;
+          }
+          if (held || t0 == 0) {
+            // ---- the head's factor; its earlier codes follow it
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            if (g.share_log2 > 0) {
+              if (lane == 0) s_top[parity][warp] = make_float2(top, clean ? 1.f : 0.f);
+              share_barrier(warp >> g.share_log2, 32 << g.share_log2);
+              for (int i = 0; i < 1 << g.share_log2; ++i) {
+                const float2 other = s_top[parity][warp - member + i];
+                top = fmaxf(top, other.x);
+                clean = clean && other.y != 0.f;
+              }
+              parity ^= 1;
+            }
+            const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
+            to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
+            was = was > 0.f ? fminf(was, kLargest) : 0.f;
+            float now = factor_of<INT8>(top);
+            if (factor != nullptr && now > was && was > 0.f) {
+              const float ratio = was / now;
+              const int per_row = p.head_dim / 16;
+              for (int i = lane + 32 * member; i < old * per_row; i += 32 << g.share_log2) {
+                const int r = i / per_row;
+                uint4* at16 = reinterpret_cast<uint4*>(to + r * pages.ss) + (i - r * per_row);
+                uint4 codes = *at16;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&codes);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float4 y = value4<INT8>(w[k]);
+                  w[k] = code4<INT8>(y.x, y.y, y.z, y.w, ratio);
+                }
+                *at16 = codes;
+              }
+            }
+            now = fmaxf(now, was);
+            if (factor != nullptr && lane == 0 && member == 0) *factor = now;
+            inv = 1.f / now;
+            clean = clean && now < kLargest;  // a factor at its upper bound leaves values beyond the largest code
+            to += (old + r0) * pages.ss + at;
+            step = pages.ss * rpw;
+          }
+          // ---- codes
+          char* out = to + t0 * (step >> (5 - g.lanes_log2));
+          auto put = [&](auto fits) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+              if (i * rpw >= left) break;
+              float v[8];
+              take(i, t0, v);
+              if (i * rpw < rows && factor != nullptr)
+                *reinterpret_cast<uint2*>(out) = make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], inv),
+                                                            code4<INT8, fits.value>(v[4], v[5], v[6], v[7], inv));
+              out += step;
+            }
+          };
+          if (INT8 && clean) put(std::true_type());
+          else put(std::false_type());
         }
       }
-      if (lane == 0) *s = now;
-    }
-
-    // ---- codes
-    const float inv = 1.f / now;
-    to += old * pages.ss + at;
-    auto put = [&](int t0, auto fits) {
-      const int rows = on && stored ? n - t0 - r0 : 0;
-      char* out = to + (t0 + r0) * pages.ss;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (i * rpw >= n - t0) break;
-        float v[8];
-        take(i, t0, v);
-        if (i * rpw < rows)
-          *reinterpret_cast<uint2*>(out) =
-              make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], inv), code4<INT8, fits.value>(v[4], v[5], v[6], v[7], inv));
-        out += pages.ss * rpw;
-      }
-    };
-    for (int t0 = 0; t0 < n; t0 += chunk_rows) {
-      if (!held) {
-        ask(t0);
-        turn_rows(t0);
-      }
-      // (a factor at its upper bound leaves values beyond the largest code)
-      if (INT8 && clean && now < kLargest) put(t0, std::true_type());
-      else put(t0, std::false_type());
     }
   }
 }
@@ -507,6 +547,23 @@ __global__ void __launch_bounds__(kThreads) load8_kernel(Load8Params p, FastDiv 
   }
 }
 
+template <typename T, bool INT8, int MODE>
+cudaError_t launch_mode(const Append8Params& p, const Append8Grid& g, unsigned grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};  // devices with the attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (MODE != kNoTurn && (!(done.load(std::memory_order_relaxed) & bit) || bit == 0)) {
+    e = cudaFuncSetAttribute(append8_kernel<T, INT8, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTurns * static_cast<int>(sizeof(float2)) << kMostShares);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  append8_kernel<T, INT8, MODE><<<grid, kThreads, smem, stream>>>(p, g);
+  return cudaGetLastError();
+}
+
 template <typename T, bool INT8>
 cudaError_t launch_append(const Append8Params& p, cudaStream_t stream) {
   Append8Grid g;
@@ -518,17 +575,27 @@ cudaError_t launch_append(const Append8Params& p, cudaStream_t stream) {
   const int64_t seqs = p.batch < p.tokens ? p.batch : p.tokens;
   int64_t units = p.tokens / static_cast<int64_t>(p.cache.block.d) + 2 * seqs;
   if (units > p.tokens) units = p.tokens;
+  // Warps share the tokens of a row of heads where a block of the cache gets more of them than one
+  // holds (as many as a sequence has on average).
+  const int64_t rows = p.tokens / seqs < p.cache.block.d ? (p.tokens + seqs - 1) / seqs : p.cache.block.d;
+  g.share_log2 = 0;
+  while (g.share_log2 < kMostShares && ((kHeld << 5 >> g.lanes_log2) << g.share_log2) < rows) ++g.share_log2;
+  // few blocks of tokens: several blocks share the heads of each, down to one for each warp
   const int64_t jobs = static_cast<int64_t>(p.h_q) + 2 * static_cast<int64_t>(p.h_k);
-  g.parts.set(static_cast<uint32_t>((jobs + kWarps - 1) / kWarps));
-  const int64_t items = units * g.parts.d;
+  const int at_once = kWarps >> g.share_log2;
+  const int64_t fit = (jobs + at_once - 1) / at_once;
+  int64_t parts = 4 * most / units;
+  parts = parts < 1 ? 1 : (parts > fit ? fit : parts);
+  g.parts = static_cast<int>(parts);
+  const int64_t items = units * parts;
   const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  const size_t smem = mode == kNoTurn ? 0 : (kTurns * sizeof(float2)) << g.share_log2;
   switch (mode) {
-    case kNoTurn: append8_kernel<T, INT8, kNoTurn><<<grid, kThreads, 0, stream>>>(p, g); break;
-    case kHalves: append8_kernel<T, INT8, kHalves><<<grid, kThreads, 0, stream>>>(p, g); break;
-    case kPairs: append8_kernel<T, INT8, kPairs><<<grid, kThreads, 0, stream>>>(p, g); break;
-    default: append8_kernel<T, INT8, kMixed><<<grid, kThreads, 0, stream>>>(p, g); break;
+    case kNoTurn: return launch_mode<T, INT8, kNoTurn>(p, g, grid, smem, stream);
+    case kHalves: return launch_mode<T, INT8, kHalves>(p, g, grid, smem, stream);
+    case kPairs: return launch_mode<T, INT8, kPairs>(p, g, grid, smem, stream);
+    default: return launch_mode<T, INT8, kMixed>(p, g, grid, smem, stream);
   }
-  return cudaGetLastError();
 }
 
 template <typename T, bool INT8>
