@@ -1,6 +1,7 @@
-"""Builds libattn_gb300.so in place from csrc/*.cu with nvcc for sm_103a.
+"""Builds libattn_gb300.so in place from csrc/*.cu with nvcc for sm_103a, and _native.so, the
+marshalling of the calls that last a few microseconds, from csrc/native.cpp with the host compiler.
 
-Each translation unit compiles in its own nvcc process (in parallel), then
+Each translation unit compiles in its own process (in parallel), then
 one link step produces the shared library next to this file.  The CUDA
 runtime is linked statically, so loading the library needs no GPU driver;
 the driver is reached at run time through the runtime's entry-point query.
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_gb300.so")
+NATIVE = os.path.join(HERE, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--threads", "2"]
@@ -34,14 +36,33 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps += [os.path.join(HERE, "..", "include", f)
              for f in os.listdir(os.path.join(HERE, "..", "include"))]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _native() -> None:
+    """_native.so against the torch that imports it."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           *(a for i in include for a in ("-isystem", i)), os.path.join(CSRC, "native.cpp"), "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for native.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
@@ -63,7 +84,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
+        native = ex.submit(_native)
         objs = list(ex.map(compile_one, sources()))
+        native.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

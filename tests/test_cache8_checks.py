@@ -14,13 +14,13 @@ import torch
 
 import attention_backward_bwd_gb300 as ab
 from attention_backward_bwd_gb300 import cache as binding_cache
-from attention_backward_bwd_gb300 import cache8 as binding_cache8
 from tests.test_abi_host import _c_kind, _ctypes_kind
 from tests.test_cache_checks import T, rotary
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DTYPE, SHAPE, STRIDE, ALIGN, NULL, WS, ARG = -1, -2, -3, -4, -5, -6, -9
 P = 1 << 20
+FACTORS = struct.Struct("@PPqqqqqqii")  # attn_paged_kv8 behind its attn_paged_kv
 
 
 @pytest.fixture(scope="module")
@@ -54,7 +54,7 @@ def test_packed_structure_matches_the_header(tmp_path):
     subprocess.run([cc, "-std=c11", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
     at = {x.split()[0]: int(x.split()[1]) for x in out.splitlines()}
-    b = binding_cache._PAGED.pack(*range(1, 14)) + binding_cache8._FACTORS.pack(*range(21, 31))
+    b = binding_cache._PAGED.pack(*range(1, 14)) + FACTORS.pack(*range(21, 31))
     assert len(b) == at["size"]
     assert at["kv"] == 0 and binding_cache._PAGED.size == at["k_scale"]
     for name, fmt, want in (("k_scale", "@P", 21), ("v_scale", "@P", 22), ("k_scale_page", "@q", 23),
@@ -66,7 +66,7 @@ def test_packed_structure_matches_the_header(tmp_path):
 def paged8(kptr=P, vptr=P, kh=64, ks=128, kb=2048, table=P, ts=8, pages=10, size=16, per=8, fk=P, fv=P, st=(4, 2, 1),
            vst=(4, 2, 1), block=8, kind=0):
     return binding_cache._PAGED.pack(kptr, kb, ks, kh, vptr, 2048, 128, 64, table, ts, pages, size, per) + \
-        binding_cache8._FACTORS.pack(fk, fv, *st, *vst, block, kind)
+        FACTORS.pack(fk, fv, *st, *vst, block, kind)
 
 
 def append(lib, q=T(), oq=T(), k=T(), v=T(), dt=1, t=4, b=4, hq=2, hk=2, d=64, c=paged8(), n=P, cu=None, rot=rotary()):
