@@ -1,13 +1,19 @@
 // Pages that sequences share: forking, freeing and room for new tokens (attn_cache_fork), and the
 // copy of pages (attn_cache_copy).
 //
-// attn_cache_fork works on the block table and the pages' counts of references alone.  One cluster
-// of blocks takes it in steps that the cluster's barrier parts: who goes on with which row, the
-// references that go and come and what each row needs, prefix sums over rows and the number of free
-// pages in each block's part of the pool, the list of the lowest free pages, the new rows.  Which
-// page a row gets follows from its place alone, so that the result does not depend on timing.  It
-// is bound by the chain of these steps and of loads behind them.
+// attn_cache_fork works on the block table and the pages' counts of references alone, in steps: the
+// references that go and come and what each row needs; prefix sums over the rows and the number of
+// free pages in each block's part of the pool; the list of the lowest free pages; the new rows.
+// Who goes on with which row is worked out by every block for itself, in shared memory.  Which page
+// a row gets follows from its place alone, so that the result does not depend on timing.  A warp
+// takes kChunk entries of a row.  Small tables and pools are one launch of one cluster, whose
+// barrier parts the steps: bound by their chain, each some loads long.  Large ones (kLarge) take a
+// launch a step, with all of the GPU for the references and the rows: a reference is an atomic
+// operation, of which an SM issues one a cycle or so (512 rows of 1025 pages: 84 us in one cluster,
+// see launch_fork).
 // attn_cache_copy moves whole pages, 16 bytes a thread, several in flight: bound by the memory.
+#include <atomic>
+
 #include "cache.h"
 #include "common.cuh"
 
@@ -15,32 +21,44 @@ namespace attn {
 
 namespace {
 
-constexpr int kForkThreads = 1024;
-constexpr int kCluster = 8;
+constexpr int kForkThreads = 512;
+constexpr int kForkWarps = kForkThreads / 32;
+constexpr int kCluster = 8;    // blocks
+constexpr int kEntries = 8;    // of a lane in flight
+constexpr int kChunk = 32 * kEntries;
+// Rows whose state is kept in shared memory: 12 bytes each, and 8 more for the prefix sums.
+constexpr int kRows = 8192;
+constexpr int64_t kLarge = 100000;  // entries and pages
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// Steps of a launch.
+enum { kRefs = 1, kList = 2, kWrite = 4, kAllSteps = 7 };
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
 
-// Workspace of a fork: per row the first row that takes it over, its parent, its length, the
-// pages and copies it needs and their prefix sums; per block its free pages; the sums; then the
-// list of free pages and, where the table is its own output, the old table.
+// Workspace of a fork: per row the pages and copies it needs and their prefix sums (beyond kRows
+// rows also the first row that takes it over, its parent and its length); per block its free
+// pages; the copies made, the pages needed and the free ones; then the list of free pages and,
+// where the table is its own output, the old table.
 struct ForkWs {
-  int *who, *parent, *len, *fresh, *copied, *fresh_before, *copied_before, *free_of, *sums, *list, *old;
+  int *fresh, *copied, *who, *parent, *len, *fresh_before, *copied_before, *free_of, *sums, *list, *old;
 };
 __host__ __device__ inline ForkWs fork_layout(int* ws, int64_t rows, int64_t list) {
   ForkWs w;
-  w.who = ws;
+  w.fresh = ws;
+  w.copied = w.fresh + rows;
+  w.who = w.copied + rows;
   w.parent = w.who + rows;
   w.len = w.parent + rows;
-  w.fresh = w.len + rows;
-  w.copied = w.fresh + rows;
-  w.fresh_before = w.copied + rows;
+  w.fresh_before = w.len + rows;
   w.copied_before = w.fresh_before + rows;
   w.free_of = w.copied_before + rows;
   w.sums = w.free_of + kCluster;
@@ -61,13 +79,13 @@ __device__ __forceinline__ int block_prefix(int mine, int* warp_sums, int& total
   __syncthreads();  // the last call's sums have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int s = warp_sums[lane];
+  int s = lane < kForkWarps ? warp_sums[lane] : 0;
 #pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
+  for (int i = 1; i < kForkWarps; i <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, s, i);
     if (lane >= i) s += y;
   }
-  total = __shfl_sync(0xffffffffu, s, 31);
+  total = __shfl_sync(0xffffffffu, s, kForkWarps - 1);
   const int before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
   return (warp == 0 ? 0 : before) + x - mine;
 }
@@ -79,55 +97,76 @@ struct Row {
   bool heir;          // goes on with its parent's pages
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs w) {
-  __shared__ int s_sums[32];
+template <int STEPS>
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs w, int copy_refs) {
+  __shared__ int s_sums[kForkWarps];
+  extern __shared__ int s_state[];
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_rank());
-  const int at = rank * kForkThreads + tid, step = kCluster * kForkThreads;
-  const int gw = at >> 5, warps = step >> 5;
-  const bool in_place = p.table == p.table_out;
+  const int rank = static_cast<int>(cluster_rank()), blocks = static_cast<int>(cluster_blocks());
+  const int at = blockIdx.x * kForkThreads + tid, step = gridDim.x * kForkThreads;
+  auto sync = [&]() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  const bool in_place = p.table == p.table_out, few = p.rows <= kRows;
+  int* const saved_len = w.len;  // from the references' launch to the rows': seqlens may be its own output
+  if (STEPS == kRefs || STEPS == kList) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (STEPS == kList || STEPS == kWrite) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (few) {
+    w.who = s_state;
+    w.parent = w.who + p.rows;
+    w.len = w.parent + p.rows;
+    if (STEPS == kAllSteps) {
+      w.fresh_before = w.len + p.rows;
+      w.copied_before = w.fresh_before + p.rows;
+    }
+  }
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   auto valid = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages); };
 
-  // ---- lengths, the old table out of the way, the counts where they will be
-  for (int b = at; b < p.rows; b += step) {
-    int n = p.seqlens[b];
-    if (n < 0 || n > cap) {
-      report(p.status, kBadLength);
-      n = 0;
+  if (STEPS != kList) {
+    // ---- lengths and parents; the first row of each parent goes on with its pages.  Of few rows
+    // every block sets all up.
+    const bool tell = STEPS & kRefs && (!few || blockIdx.x == 0);
+    const int b0 = few ? tid : at, bs = few ? kForkThreads : step;
+    for (int b = b0; b < p.rows; b += bs) {
+      int n = STEPS == kWrite ? __ldcg(saved_len + b) : p.seqlens[b], s = p.parents == nullptr ? b : p.parents[b];
+      if (n < 0 || n > cap) {
+        if (tell) report(p.status, kBadLength);
+        n = 0;
+      }
+      if (s >= p.rows) {
+        if (tell) report(p.status, kBadParent);
+        s = b;
+      }
+      w.len[b] = n;
+      if (STEPS == kRefs && blockIdx.x == 0) saved_len[b] = n;
+      w.parent[b] = s;
+      w.who[b] = p.rows;
     }
-    w.len[b] = n;
-    w.who[b] = p.rows;
+    if (STEPS & kRefs && copy_refs)
+      for (int i0 = at; i0 < p.num_pages; i0 += step * kEntries) {
+        int x[kEntries];
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k)
+          if (i0 + k * step < p.num_pages) x[k] = p.refs[i0 + k * step];
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k)
+          if (i0 + k * step < p.num_pages) p.refs_out[i0 + k * step] = x[k];
+      }
+    if (STEPS & kRefs && at == 0) w.sums[0] = 0;
+    if (few) __syncthreads();
+    else sync();
+    for (int b = b0; b < p.rows; b += bs)
+      if (w.parent[b] >= 0) atomicMin(w.who + w.parent[b], b);
+    if (STEPS == kAllSteps) sync();  // the references are where they will be, too
+    else __syncthreads();
   }
-  if (in_place)
-    for (int b = gw; b < p.rows; b += warps)
-      for (int i = lane; i < p.max_pages; i += 32)
-        w.old[static_cast<int64_t>(b) * p.max_pages + i] = p.table[b * p.table_stride + i];
-  if (p.refs != p.refs_out)
-    for (int i = at; i < p.num_pages; i += step) p.refs_out[i] = p.refs[i];
-  if (at == 0) w.sums[2] = 0;
-  cluster_sync();
 
-  // ---- the first row of each parent goes on with its pages
-  for (int b = at; b < p.rows; b += step) {
-    int s = p.parents == nullptr ? b : p.parents[b];
-    if (s >= p.rows) {
-      report(p.status, kBadParent);
-      s = b;
-    }
-    w.parent[b] = s;
-    if (s >= 0) atomicMin(w.who + s, b);
-  }
-  cluster_sync();
-
-  auto old_row = [&](int b) -> const int* {
-    return in_place ? w.old + static_cast<int64_t>(b) * p.max_pages : p.table + b * p.table_stride;
-  };
   auto row_of = [&](int b, bool tell) {
     Row r;
-    r.parent = __ldcg(w.parent + b);
-    r.n = r.parent < 0 ? 0 : __ldcg(w.len + r.parent);
-    r.heir = r.parent >= 0 && __ldcg(w.who + r.parent) == b;
+    r.parent = w.parent[b];
+    r.n = r.parent < 0 ? 0 : w.len[r.parent];
+    r.heir = r.parent >= 0 && w.who[r.parent] == b;
     r.full = r.n / p.page_size;
     r.used = r.full + (r.n % p.page_size != 0 ? 1 : 0);
     const int room = r.parent < 0 ? 0 : (p.room == nullptr ? p.room_all : p.room[b]);
@@ -139,15 +178,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kForkThreads)
     r.need = static_cast<int>((slots + p.page_size - 1) / p.page_size);
     return r;
   };
-  // Entry i of a row: the parent's page, whether it is shared, copied, or a fresh one is needed.
+  // Entry i of a row: its page, whether that is the parent's shared one, one to be copied, missing.
   struct Entry {
     int page;
     bool shared, copied, fresh, bad;
   };
-  auto entry_of = [&](const Row& r, const int* old, int i) {
+  auto entry_of = [&](const Row& r, int page, int i) {
     Entry e{-1, false, false, false, false};
     if (r.parent < 0 || i >= p.max_pages) return e;
-    const int page = __ldcg(old + i);
     if (r.heir) {
       e.page = valid(page) ? page : -1;
       e.fresh = e.page < 0 && i >= r.used && i < r.need;
@@ -161,119 +199,206 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kForkThreads)
     }
     return e;
   };
-
-  // ---- references that go and come; what each row needs
-  for (int b = gw; b < p.rows; b += warps) {
-    const int* own = old_row(b);
-    if (__ldcg(w.who + b) == p.rows)
-      for (int i = lane; i < p.max_pages; i += 32) {
-        const int page = __ldcg(own + i);
-        if (valid(page)) atomicSub(p.refs_out + page, 1);
-      }
-    const Row r = row_of(b, lane == 0);
-    const int* old = r.parent < 0 ? own : old_row(r.parent);
-    int fresh = 0, copied = 0;
-    const int from = r.heir ? r.used : 0, end = max(r.used, r.need);
-    for (int i = from + lane; i < end; i += 32) {
-      const Entry e = entry_of(r, old, i);
-      if (e.bad) report(p.status, kBadPage);
-      if (e.shared) atomicAdd(p.refs_out + e.page, 1);
-      fresh += e.fresh;
-      copied += e.copied;
+  // Where a row's missing entries start (and end: at max(used, need)).
+  auto lack_from = [&](const Row& r) { return r.heir ? r.used : (p.share ? r.full : 0); };
+  // Entries i0 + 32 k + lane below `end`, as they are.
+  auto load = [&](const int* row, int i0, int end, int (&page)[kEntries]) {
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+      const int i = i0 + 32 * k + lane;
+      page[k] = i < end ? __ldcg(row + i) : -1;
+    }
+  };
+  // Missing entries and copies of [from, end), by a warp.
+  auto count = [&](const Row& r, const int* old, int from, int end, int& fresh, int& copied) {
+    fresh = copied = 0;
+    for (int i0 = from; i0 < end; i0 += kChunk) {
+      int page[kEntries];
+      load(old, i0, end, page);
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k)
+        if (i0 + 32 * k + lane < end) {
+          const Entry e = entry_of(r, page[k], i0 + 32 * k + lane);
+          fresh += e.fresh;
+          copied += e.copied;
+        }
     }
     fresh = __reduce_add_sync(0xffffffffu, fresh);
     copied = __reduce_add_sync(0xffffffffu, copied);
-    if (lane == 0) {
-      w.fresh[b] = fresh;
-      w.copied[b] = copied;
-    }
-  }
-  cluster_sync();
+  };
+  const int chunks = (p.max_pages + kChunk - 1) / kChunk;
+  const int64_t items = static_cast<int64_t>(p.rows) * chunks;
 
-  // ---- prefix sums over the rows (the first block); free pages of each block's part
-  if (rank == 0) {
-    int fresh0 = 0, copied0 = 0;
-    for (int b0 = 0; b0 < p.rows; b0 += kForkThreads) {
-      const int b = b0 + tid;
-      int total;
-      const int fresh = b < p.rows ? __ldcg(w.fresh + b) : 0, copied = b < p.rows ? __ldcg(w.copied + b) : 0;
-      const int f = block_prefix(fresh, s_sums, total);
-      if (b < p.rows) w.fresh_before[b] = fresh0 + f;
-      fresh0 += total;
-      const int c = block_prefix(copied, s_sums, total);
-      if (b < p.rows) w.copied_before[b] = copied0 + c;
-      copied0 += total;
-    }
-    if (tid == 0) w.sums[0] = fresh0;
-  }
-  const int page0 = static_cast<int>(static_cast<int64_t>(p.num_pages) * rank / kCluster);
-  const int page1 = static_cast<int>(static_cast<int64_t>(p.num_pages) * (rank + 1) / kCluster);
-  int free_here = 0;
-  for (int i = page0 + tid; i < page1; i += kForkThreads) free_here += __ldcg(p.refs_out + i) == 0;
-  int total;
-  block_prefix(free_here, s_sums, total);
-  if (tid == 0) w.free_of[rank] = total;
-  cluster_sync();
-
-  // ---- the lowest free pages, as many as are needed
-  const int wanted = __ldcg(w.sums);
-  int first = 0, all = 0;
+  if (STEPS & kRefs) {
+    // ---- references that go and come; what each row needs (the table is as it was until the last step)
+    for (int64_t item = at >> 5; item < items; item += step >> 5) {
+      const int b = static_cast<int>(item / chunks), i0 = static_cast<int>(item - static_cast<int64_t>(b) * chunks) * kChunk;
+      const bool left = w.who[b] == p.rows;
+      const Row r = row_of(b, lane == 0 && i0 == 0);
+      const int* old = p.table + (r.parent < 0 ? b : r.parent) * p.table_stride;
+      int own[kEntries], page[kEntries];
+      if (left || in_place) load(p.table + b * p.table_stride, i0, p.max_pages, own);
+      const int shared = r.heir || !p.share ? 0 : r.full;
+      if (i0 < shared) load(old, i0, shared, page);
+      if (left || in_place)
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) {
-    const int n = __ldcg(w.free_of + c);
-    first += c < rank ? n : 0;
-    all += n;
-  }
-  const int granted = min(wanted, all);
-  for (int i0 = page0; i0 < page1 && first < granted; i0 += kForkThreads) {
-    const int i = i0 + tid;
-    const bool is_free = i < page1 && __ldcg(p.refs_out + i) == 0;
-    int n;
-    const int k = first + block_prefix(is_free, s_sums, n);
-    if (is_free && k < granted) w.list[k] = i;
-    first += n;
-  }
-  cluster_sync();
-
-  // ---- the new rows
-  for (int b = gw; b < p.rows; b += warps) {
-    const Row r = row_of(b, false);
-    const int* old = old_row(r.parent < 0 ? b : r.parent);
-    int* out = p.table_out + b * p.out_stride;
-    int fresh0 = __ldcg(w.fresh_before + b), copied0 = __ldcg(w.copied_before + b), made = 0;
-    for (int i0 = 0; i0 < p.max_pages; i0 += 32) {
-      const int i = i0 + lane;
-      const Entry e = entry_of(r, old, i);
-      const uint32_t fresh = __ballot_sync(0xffffffffu, e.fresh), copied = __ballot_sync(0xffffffffu, e.copied);
-      const uint32_t below = (1u << lane) - 1;
-      int page = e.page;
-      if (e.fresh) {
-        const int k = fresh0 + __popc(fresh & below);
-        page = k < granted ? __ldcg(w.list + k) : -1;
-        if (page >= 0) p.refs_out[page] = 1;
-        else report(p.status, kNoPage);
-        if (e.copied && page >= 0) {
-          int* pair = p.copies + 2 * static_cast<int64_t>(copied0 + __popc(copied & below));
-          pair[0] = e.page;
-          pair[1] = page;
-          ++made;
+        for (int k = 0; k < kEntries; ++k) {
+          const int i = i0 + 32 * k + lane;
+          if (in_place && i < p.max_pages) w.old[static_cast<int64_t>(b) * p.max_pages + i] = own[k];
+          if (left && valid(own[k])) atomicSub(p.refs_out + own[k], 1);
+        }
+      if (i0 < shared)
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k) {
+          const int i = i0 + 32 * k + lane;
+          if (i < shared) {
+            if (valid(page[k])) atomicAdd(p.refs_out + page[k], 1);
+            else report(p.status, kBadPage);
+          }
+        }
+      if (i0 == 0) {
+        int fresh, copied;
+        count(r, old, lack_from(r), max(r.used, r.need), fresh, copied);
+        if (lane == 0) {
+          w.fresh[b] = fresh;
+          w.copied[b] = copied;
+          // pages of slots that cannot be copied: what is neither copied nor the room's
+          if (r.parent >= 0 && !r.heir && copied < r.used - lack_from(r)) report(p.status, kBadPage);
         }
       }
-      if (i < p.max_pages) out[i] = page;
-      fresh0 += __popc(fresh);
-      copied0 += __popc(copied);
-    }
-    made = __reduce_add_sync(0xffffffffu, made);
-    if (lane == 0) {
-      p.seqlens_out[b] = r.n;
-      if (made > 0) atomicAdd(w.sums + 2, made);
     }
   }
-  cluster_sync();
-  if (at == 0) {
-    p.counts[0] = __ldcg(w.sums + 2);
-    p.counts[1] = all - granted;
+  if (STEPS == kAllSteps) sync();
+
+  int all = 0, granted = 0;
+  if (STEPS & kList) {
+    // ---- free pages of each block's part; prefix sums over the rows
+    const int page0 = static_cast<int>(static_cast<int64_t>(p.num_pages) * rank / blocks);
+    const int page1 = static_cast<int>(static_cast<int64_t>(p.num_pages) * (rank + 1) / blocks);
+    int free_here = 0;
+    for (int i0 = page0 + tid; i0 < page1; i0 += kForkThreads * kEntries) {
+      int x[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) x[k] = i0 + k * kForkThreads < page1 ? __ldcg(p.refs_out + i0 + k * kForkThreads) : 1;
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) free_here += x[k] == 0;
+    }
+    int total, wanted = 0;
+    const bool here = STEPS == kAllSteps && few;  // the prefix sums are each block's own
+    if (here || rank == 0) {
+      int copied0 = 0;
+      for (int r0 = 0; r0 < p.rows; r0 += kForkThreads) {
+        const int b = r0 + tid;
+        const int fresh = b < p.rows ? __ldcg(w.fresh + b) : 0, copied = b < p.rows ? __ldcg(w.copied + b) : 0;
+        const int f = block_prefix(fresh, s_sums, total);
+        if (b < p.rows) w.fresh_before[b] = wanted + f;
+        wanted += total;
+        const int c = block_prefix(copied, s_sums, total);
+        if (b < p.rows) w.copied_before[b] = copied0 + c;
+        copied0 += total;
+      }
+      if (!here && tid == 0) w.sums[1] = wanted;
+    }
+    block_prefix(free_here, s_sums, total);
+    if (tid == 0) w.free_of[rank] = total;
+    sync();
+
+    // ---- the lowest free pages, as many as are needed
+    if (!here) wanted = __ldcg(w.sums + 1);
+    int first = 0;
+    for (int c = 0; c < blocks; ++c) {
+      const int n = __ldcg(w.free_of + c);
+      first += c < rank ? n : 0;
+      all += n;
+    }
+    granted = min(wanted, all);
+    for (int i0 = page0; i0 < page1 && first < granted; i0 += kForkThreads * 4) {
+      int x[4], n, mine = 0;  // four neighbouring pages a thread
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + tid * 4 + k;
+        x[k] = i < page1 ? __ldcg(p.refs_out + i) : 1;
+        mine += x[k] == 0;
+      }
+      int k0 = first + block_prefix(mine, s_sums, n);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x[k] == 0) {
+          if (k0 < granted) w.list[k0] = i0 + tid * 4 + k;
+          ++k0;
+        }
+      first += n;
+    }
+    if (STEPS == kList && rank == 0 && tid == 0) {
+      w.sums[2] = granted;
+      p.counts[0] = 0;
+      p.counts[1] = all - granted;
+    }
   }
+  if (STEPS == kAllSteps) sync();
+
+  if (STEPS & kWrite) {
+    // ---- the new rows
+    if (STEPS == kWrite) granted = __ldcg(w.sums + 2);
+    for (int64_t item = at >> 5; item < items; item += step >> 5) {
+      const int b = static_cast<int>(item / chunks), i0 = static_cast<int>(item - static_cast<int64_t>(b) * chunks) * kChunk;
+      const Row r = row_of(b, false);
+      const int from = r.parent < 0 ? b : r.parent;
+      const int* old = in_place ? w.old + static_cast<int64_t>(from) * p.max_pages : p.table + from * p.table_stride;
+      int* out = p.table_out + b * p.out_stride;
+      int page[kEntries];
+      load(old, i0, r.heir ? p.max_pages : r.used, page);  // entries that the parent has a say in
+      int fresh0 = w.fresh_before[b], copied0 = w.copied_before[b], made = 0;
+      if (i0 > lack_from(r) && i0 < max(r.used, r.need)) {
+        int fresh, copied;
+        count(r, old, lack_from(r), i0, fresh, copied);
+        fresh0 += fresh;
+        copied0 += copied;
+      }
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        const int i = i0 + 32 * k + lane;
+        if (i - lane >= p.max_pages) break;
+        const Entry e = entry_of(r, page[k], i);
+        int now = e.page;
+        const uint32_t fresh = __ballot_sync(0xffffffffu, e.fresh);
+        if (fresh != 0) {
+          const uint32_t copied = __ballot_sync(0xffffffffu, e.copied), below = (1u << lane) - 1;
+          if (e.fresh) {
+            const int nth = fresh0 + __popc(fresh & below);
+            now = nth < granted ? __ldcg(w.list + nth) : -1;
+            if (now >= 0) p.refs_out[now] = 1;
+            else report(p.status, kNoPage);
+            if (e.copied && now >= 0) {
+              int* pair = p.copies + 2 * static_cast<int64_t>(copied0 + __popc(copied & below));
+              pair[0] = e.page;
+              pair[1] = now;
+              ++made;
+            }
+          }
+          fresh0 += __popc(fresh);
+          copied0 += __popc(copied);
+        }
+        if (i < p.max_pages) out[i] = now;
+      }
+      made = __reduce_add_sync(0xffffffffu, made);
+      if (lane == 0) {
+        if (i0 == 0) p.seqlens_out[b] = r.n;
+        if (made > 0) atomicAdd(STEPS == kWrite ? p.counts : w.sums, made);
+      }
+    }
+  }
+  if (STEPS == kAllSteps) {
+    sync();
+    if (at == 0) {
+      p.counts[0] = __ldcg(w.sums);
+      p.counts[1] = all - granted;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kForkThreads) copy_refs_kernel(const int* from, int* to, int n) {
+  for (int i = blockIdx.x * kForkThreads + threadIdx.x; i < n; i += gridDim.x * kForkThreads) to[i] = from[i];
 }
 
 constexpr int kCopyThreads = 256;
@@ -336,11 +461,61 @@ size_t fork_ws(int rows, int max_pages, int num_pages) {
   return align256((7 * static_cast<int64_t>(rows) + kCluster + 8 + list + entries) * sizeof(int));
 }
 
-cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
+namespace {
+
+template <int STEPS>
+cudaError_t launch_steps(const ForkParams& p, int cluster, int blocks, cudaStream_t stream) {
   const int64_t entries = static_cast<int64_t>(p.rows) * p.max_pages;
   const int64_t list = entries < p.num_pages ? entries : p.num_pages;
-  fork_kernel<<<kCluster, kForkThreads, 0, stream>>>(p, fork_layout(p.ws, p.rows, list));
-  return cudaGetLastError();
+  const size_t smem = STEPS == kList || p.rows > kRows ? 0 : static_cast<size_t>(p.rows) * (STEPS == kAllSteps ? 20 : 12);
+  static std::atomic<unsigned long long> done{0};  // devices with the attribute set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit) || bit == 0) {
+    e = cudaFuncSetAttribute(fork_kernel<STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows * 20);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchAttribute attrs[2];
+  int n = 0;
+  if (cluster > 1) {
+    attrs[n].id = cudaLaunchAttributeClusterDimension;
+    attrs[n].val.clusterDim.x = cluster;
+    attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (STEPS == kList || STEPS == kWrite) {  // launched early, waits for the launch before it
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kForkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attrs;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, fork_kernel<STEPS>, p, fork_layout(p.ws, p.rows, list),
+                            STEPS == kAllSteps && p.refs != p.refs_out ? 1 : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
+  const int64_t entries = static_cast<int64_t>(p.rows) * p.max_pages;
+  if (entries + p.num_pages < kLarge || p.rows > kRows) return launch_steps<kAllSteps>(p, kCluster, kCluster, stream);
+  const int64_t items = static_cast<int64_t>(p.rows) * ceil_div(p.max_pages, kChunk);
+  const int64_t fit = (items + kForkWarps - 1) / kForkWarps, most = 2 * static_cast<int64_t>(num_sms());
+  const int blocks = static_cast<int>(fit < most ? fit : most);
+  if (p.refs != p.refs_out)
+    copy_refs_kernel<<<static_cast<unsigned>(most), kForkThreads, 0, stream>>>(p.refs, p.refs_out, p.num_pages);
+  cudaError_t e = launch_steps<kRefs>(p, 1, blocks, stream);
+  if (e == cudaSuccess) e = launch_steps<kList>(p, kCluster, kCluster, stream);
+  if (e == cudaSuccess) e = launch_steps<kWrite>(p, 1, blocks, stream);
+  return e;
 }
 
 cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream) {

@@ -48,6 +48,8 @@ CASES = [
     (64, 700, 7, 9000, 3, True, 0), (9, 300, 32, 400, 1, False, 2), (40, 64, 64, 100, 100, False, 0),
     (300, 500, 16, 20000, 1, True, 1), (3, 9000, 1, 40000, 5, False, 0),
     (2100, 60, 16, 9001, 1, True, 2),   # more rows than a block has threads
+    (700, 2000, 16, 90001, 20, True, 3), (40, 9000, 3, 121000, 2, False, 0), (1, 100000, 1, 100000, 1, True, 0),
+    (8200, 20, 16, 20000, 1, True, 1),   # more rows than shared memory keeps
 ]
 
 
