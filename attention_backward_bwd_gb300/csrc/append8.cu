@@ -14,7 +14,9 @@
 // their largest value and once more when they are rounded, so that k and v are read once.  Tokens
 // Warps share the tokens of a row of heads where they are more; what is beyond that, too, is read a
 // second time, from the L2.
-// Read-back.  A warp takes a token: 16 codes a lane, 32 bytes out.
+// Read-back.  A warp takes a token: 8 codes a lane, 16 bytes out, so that a warp's stores are whole
+// lines (with 16 codes a lane, two half-written sectors of 32 bytes at a time, 8 sequences up to 8192
+// tokens of 8 heads of 128 took 50 us).
 #include <atomic>
 #include <type_traits>
 
@@ -31,6 +33,7 @@ constexpr int kHeld = 16;      // chunks of a lane in registers
 constexpr int kTurns = 2048;   // turns of the rows that a warp takes at once
 constexpr int kBlocks = 2;     // of an SM
 constexpr int kMostShares = 2; // log2 of the warps that share tokens
+constexpr int kLoads = 4;      // of a lane and of each of k and v, in a read-back
 constexpr float kLargest = 1.152921504606847e18f;    // 2^60
 
 // Where the other element of a pair is: kHalves in the lane n_freq / 8 further (n_freq a multiple
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   }
 }
 
-// A warp a token: rows of k and v of all heads, 16 codes a lane.
+// A warp a token: rows of k and v of all heads, 8 codes a lane and kLoads of these on their way.
 template <typename T, bool INT8>
 __global__ void __launch_bounds__(kThreads) load8_kernel(Load8Params p, FastDiv per_row) {
   const int lane = threadIdx.x & 31;
@@ -515,33 +518,45 @@ __global__ void __launch_bounds__(kThreads) load8_kernel(Load8Params p, FastDiv 
       page = -1;
     }
     const int64_t blk = p.cache.block.div(static_cast<uint32_t>(within));
+    const char* rows[2];
+    const float* scales[2];
+    T* to[2];
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const TensorArg& in = kind ? p.cache.pages.v : p.cache.pages.k;
       const TensorArg& out = kind ? p.v : p.k;
       const int64_t* st = kind ? p.cache.vs : p.cache.ks;
-      const float* scales = (kind ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1];
-      const char* rows = static_cast<const char*>(in.ptr) + page * in.sb + within * in.ss;
-      T* to = static_cast<T*>(const_cast<void*>(out.ptr)) + t * out.ss;
-      for (int i = lane; i < chunks; i += 32) {
-        const int head = static_cast<int>(per_row.div(i)), c = i - head * static_cast<int>(per_row.d);
-        uint4 codes = make_uint4(0, 0, 0, 0);
-        float s = 0.f;
-        if (page >= 0) {
-          codes = *reinterpret_cast<const uint4*>(rows + head * in.sh + c * 16);
-          s = scales[head * st[2]];
-        }
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&codes);
-        uint32_t o[8];
+      scales[kind] = (kind ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1];
+      rows[kind] = static_cast<const char*>(in.ptr) + page * in.sb + within * in.ss;
+      to[kind] = static_cast<T*>(const_cast<void*>(out.ptr)) + t * out.ss;
+    }
+    for (int i0 = lane; i0 < chunks; i0 += 32 * kLoads) {
+      uint2 codes[kLoads][2];
+      float s[kLoads][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 y = value4<INT8>(w[k]);
-          o[2 * k] = Pack<T>::two(y.x * s, y.y * s);
-          o[2 * k + 1] = Pack<T>::two(y.z * s, y.w * s);
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = i0 + 32 * k, head = static_cast<int>(per_row.div(i)), c = i - head * static_cast<int>(per_row.d);
+        codes[k][0] = codes[k][1] = make_uint2(0, 0);
+        s[k][0] = s[k][1] = 0.f;
+        if (i < chunks && page >= 0) {
+          codes[k][0] = __ldcs(reinterpret_cast<const uint2*>(rows[0] + head * p.cache.pages.k.sh + c * 8));
+          codes[k][1] = __ldcs(reinterpret_cast<const uint2*>(rows[1] + head * p.cache.pages.v.sh + c * 8));
+          s[k][0] = scales[0][head * p.cache.ks[2]];
+          s[k][1] = scales[1][head * p.cache.vs[2]];
         }
-        uint4* dst = reinterpret_cast<uint4*>(to + head * out.sh + c * 16);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int i = i0 + 32 * k, head = static_cast<int>(per_row.div(i)), c = i - head * static_cast<int>(per_row.d);
+        if (i >= chunks) break;
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          const float f = s[k][kind];
+          const float4 x = value4<INT8>(codes[k][kind].x), y = value4<INT8>(codes[k][kind].y);
+          *reinterpret_cast<uint4*>(to[kind] + head * (kind ? p.v.sh : p.k.sh) + c * 8) =
+              make_uint4(Pack<T>::two(x.x * f, x.y * f), Pack<T>::two(x.z * f, x.w * f), Pack<T>::two(y.x * f, y.y * f),
+                         Pack<T>::two(y.z * f, y.w * f));
+        }
       }
     }
   }
@@ -601,7 +616,7 @@ cudaError_t launch_append(const Append8Params& p, cudaStream_t stream) {
 template <typename T, bool INT8>
 cudaError_t launch_load(const Load8Params& p, cudaStream_t stream) {
   FastDiv per_row;
-  per_row.set(static_cast<uint32_t>(p.head_dim / 16));
+  per_row.set(static_cast<uint32_t>(p.head_dim / 8));
   const int64_t grid = (static_cast<int64_t>(p.tokens) + kWarps - 1) / kWarps, most = static_cast<int64_t>(num_sms()) * 8;
   load8_kernel<T, INT8><<<static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, stream>>>(p, per_row);
   return cudaGetLastError();
