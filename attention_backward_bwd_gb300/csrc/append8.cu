@@ -120,6 +120,21 @@ __device__ __forceinline__ int blocks_of(const Append8Params& p, const Fresh& f)
   return n <= rest ? 1 : 2 + static_cast<int>(p.cache.block.div(n - rest - 1));
 }
 
+// The largest of three magnitudes, NaN where one is.
+__device__ __forceinline__ float most_of(float top, float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(top));
+  return y;
+}
+__device__ __forceinline__ uint32_t most_of(uint32_t top, uint32_t w, __nv_bfloat16) {
+  const __nv_bfloat162 y = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t most_of(uint32_t top, uint32_t w, __half) {
+  const __half2 y = __hmax2_nan(*reinterpret_cast<const __half2*>(&top), __habs2(*reinterpret_cast<const __half2*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // Barrier of the warps that share a row of heads.
 __device__ __forceinline__ void share_barrier(int which, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(which + 1), "r"(threads) : "memory");
@@ -354,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             if (pass > 0 || t0 > 0) ask(t0);
             turn_rows(t0);
           }
-          const int left = n - t0 - w0;            // rows from this warp's first on
-          const int rows = on && j < j1 ? n - t0 - r0 : 0;  // from this lane's
+          // chunks of this warp's lanes that hold a row, and of this lane
+          const int left = max(n - t0 - w0 + rpw - 1, 0) >> (5 - g.lanes_log2);
+          const int rows = on && j < j1 ? max(n - t0 - r0 + rpw - 1, 0) >> (5 - g.lanes_log2) : 0;
           if (is_q) {
             if (pass > 0) continue;
             T* out = static_cast<T*>(const_cast<void*>(p.oq.ptr)) + static_cast<int64_t>(token0 + t0 + r0) * p.oq.ss +
@@ -372,49 +388,46 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             }
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-              if (i * rpw >= left) break;
+              if (i >= left) break;
               if (MODE != kMixed) {
                 float v[8];
                 take(i, t0, v);
                 raw[i] = pack16(v);
               }
-              if (i * rpw < rows) *reinterpret_cast<uint4*>(out) = raw[i];
+              if (i < rows) *reinterpret_cast<uint4*>(out) = raw[i];
               out += out_step;
             }
             continue;
           }
           if (pass == 0) {
             // ---- the largest value of the new tokens (rows that are none are zeros)
-            constexpr uint32_t kInf = 0x7f800000u, kInf16 = Pack<T>::kIsBf16 ? 0x7f80u : 0x7c00u;
-            uint32_t most = 0;
-            bool fine;
-            if (!turned) {  // two at a time, as bits: as numbers that are not negative they have the same order
+            float most = 0.f;  // NaN where one is
+            if (!turned) {
+              uint32_t two = 0;
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i * rpw >= left) break;
-                most = __vmaxu2(__vmaxu2(most, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu)),
-                                __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+                if (i >= left) break;
+                two = most_of(most_of(most_of(most_of(two, raw[i].x, T()), raw[i].y, T()), raw[i].z, T()), raw[i].w, T());
               }
-              most = max(most & 0xffffu, most >> 16);
-              fine = most < kInf16;
-              if (fine) top = fmaxf(top, Pack<T>::unpack(most).x);
+              const float2 y = Pack<T>::unpack(two);
+              most = most_of(0.f, y.x, y.y);
             } else {
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i * rpw >= left) break;
+                if (i >= left) break;
                 float v[8];
                 take(i, t0, v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(v[k]) & 0x7fffffffu);
+                for (int k = 0; k < 8; k += 2) most = most_of(most, v[k], v[k + 1]);
               }
-              fine = most < kInf;
-              if (fine) top = fmaxf(top, __uint_as_float(most));
             }
+            const bool fine = most < INFINITY;
+            if (fine) top = fmaxf(top, most);
             if (__any_sync(0xffffffffu, !fine)) {  // the finite ones, one by one
               clean = false;
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i * rpw >= left) break;
+                if (i >= left) break;
                 float v[8];
                 take(i, t0, v);
 #pragma unroll
@@ -465,13 +478,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
           }
           // ---- codes
           char* out = to + t0 * (step >> (5 - g.lanes_log2));
+          const int stores = factor != nullptr ? rows : 0;
           auto put = [&](auto fits) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-              if (i * rpw >= left) break;
+              if (i >= left) break;
               float v[8];
               take(i, t0, v);
-              if (i * rpw < rows && factor != nullptr)
+              if (i < stores)
                 *reinterpret_cast<uint2*>(out) = make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], inv),
                                                             code4<INT8, fits.value>(v[4], v[5], v[6], v[7], inv));
               out += step;
