@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   __shared__ int64_t s_sums[kWarps];
   __shared__ int4 s_fresh[kThreads];   // of the first sequence of each thread: first, n, len, bad
   __shared__ float2 s_top[2][kWarps];  // largest value and whether all are finite, of every other row of heads
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = static_cast<int>(warp_id());  // (uniform to the compiler)
   // turns of a row: the last ones, up to a multiple of 4, turn by nothing
   const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq, pitch = MODE == kNoTurn ? 4 : (nf + 3) / 4 * 4;
 
