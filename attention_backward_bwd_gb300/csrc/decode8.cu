@@ -77,6 +77,15 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int k) {
   return (row ^ ((k & kMask) << 4)) + (k & ~(kMask | 1)) * 16;
 }
 
+// (Without a cache policy: with a uniform warp index the compiler keeps the policy in a uniform
+// register, and such a copy ends as an illegal instruction.)
+__device__ __forceinline__ void cp_async16(uint32_t dst, long long src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or 16 zeros.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const float* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_sums[kWarps];
   __shared__ float s_max[kWarps][C::kHeads], s_sum[kWarps][C::kHeads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = static_cast<int>(warp_id());
   unsigned char* mine = smem + warp * C::kWarpBytes;  // stages, addresses, descriptors, factors
   longlong2* rows = reinterpret_cast<longlong2*>(mine + S * C::kStageBytes);
   int4* desc = reinterpret_cast<int4*>(rows + kKeys);  // sequence, head tile, flags, valid keys
@@ -263,10 +272,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
       pend_page = static_cast<uint32_t>(table[n]);
     }
   };
-  // Keys and values are read once: they leave the L2 first, unless a group has several head tiles or
-  // the rows are not whole 64-byte pieces, of which the next head's block then reads the rest
-  // (64 sequences up to 16384 keys, 8 heads of 80: 193 us against 229, of 96 251 and 269).
-  const uint64_t policy = p.head_tiles > 1 || p.head_dim % 64 != 0 ? l2_policy_evict_normal() : l2_policy_evict_first();
   // Writes the tile's addresses and descriptor down and asks for its factors.
   uint32_t live_w = 0;  // its keys
   auto store_plan = [&](int slot) {
@@ -307,17 +312,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
           const longlong2 a = from[i * kStep];
-          cp_async16(to(i), a.x + cc * 16, policy);
-          cp_async16(to(i) + kSubKeys * DP, a.y + cc * 16, policy);
+          cp_async16(to(i), a.x + cc * 16);
+          cp_async16(to(i) + kSubKeys * DP, a.y + cc * 16);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
           const longlong2 a = from[i * kStep];
           const bool ok = a.x != 0;
-          cp_async16_or_zero(to(i), ok ? a.x + cc * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok, policy);
-          cp_async16_or_zero(to(i) + kSubKeys * DP, ok ? a.y + cc * 16 : reinterpret_cast<long long>(p.cache.v.ptr), ok,
-                             policy);
+          cp_async16_or_zero(to(i), ok ? a.x + cc * 16 : reinterpret_cast<long long>(p.cache.k.ptr), ok);
+          cp_async16_or_zero(to(i) + kSubKeys * DP, ok ? a.y + cc * 16 : reinterpret_cast<long long>(p.cache.v.ptr), ok);
         }
       }
     }
