@@ -44,8 +44,10 @@ constexpr float kLeast = 8.673617379884035e-19f, kMost = 1.152921504606847e18f; 
 template <int DP, int HN>
 struct Cfg {
   static constexpr int kBlocks = DP <= 128 && HN == 1 ? 2 : (DP == 64 ? 2 : 1);  // of an SM
-  // a warp's 32 keys of a tile are copied and worked on in kSubs parts of kGroups times 16
-  static constexpr int kGroups = DP == 64 ? 2 : 1, kSubs = 2 / kGroups, kSubKeys = 16 * kGroups;
+  // A warp's 32 keys of a tile are copied and worked on in kSubs parts of kGroups times 16: at once
+  // where registers and shared memory have room for that (64 sequences up to 16384 keys of 8 heads,
+  // 16 query heads each: of 96 columns 246 us at once, 263 in two parts, of 64 columns 228 and 195).
+  static constexpr int kGroups = (DP == 64) == (HN == 1) && DP <= 128 ? 2 : 1, kSubs = 2 / kGroups, kSubKeys = 16 * kGroups;
   static constexpr int kStageBytes = 2 * kSubKeys * DP;  // of a part, of a warp
   static constexpr int kHeads = 8 * HN;
   // tiles that are copied ahead: as fit beside the rest, at most three
