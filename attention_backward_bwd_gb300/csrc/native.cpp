@@ -6,10 +6,12 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContext.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <sstream>
 #include <string>
 
@@ -229,9 +231,14 @@ bool rotary(attn_rotary* r, PyObject* positions, PyObject* inv, PyObject* sectio
   return true;
 }
 
-// An output like x: allocated, or checked against it.
+// A new contiguous tensor beside `like` (without the dispatcher: a microsecond less each).
+at::Tensor fresh(at::IntArrayRef size, at::ScalarType dtype, const at::Tensor& like) {
+  return at::detail::empty_cuda(size, dtype, like.device(), std::nullopt);
+}
+
+// An output of x's shape: allocated, or checked against it.
 at::Tensor output(PyObject* o, const char* name, const at::Tensor& x, int index, int dims, attn_tensor* arg) {
-  at::Tensor out = o == Py_None ? at::empty_like(x) : tensor(o, name);
+  at::Tensor out = o == Py_None ? fresh(x.sizes(), x.scalar_type(), x) : tensor(o, name);
   *arg = rows(out, name, index, x.scalar_type(), dims);
   if (out.sizes() != x.sizes()) refuse(-2, name, " has shape ", shape(out), ", its input ", shape(x));
   if (out.data_ptr() == x.data_ptr() && out.strides() != x.strides() && out.numel() > 0)
@@ -244,7 +251,7 @@ void* workspace(PyObject* o, size_t need, const at::Tensor& like, int index, siz
   *bytes = 0;
   if (o == Py_None) {
     if (need == 0) return nullptr;
-    *held = at::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
+    *held = fresh({static_cast<int64_t>(need)}, at::kByte, like);
   } else {
     const at::Tensor& t = tensor(o, "workspace");
     if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != at::kByte || !t.is_contiguous())
@@ -382,7 +389,7 @@ PyObject* load8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* names[2] = {"out_k", "out_v"};
     for (int i = 0; i < 2; ++i) {
       if (a[8 + i] == Py_None) {
-        out[i] = at::empty({tokens, c.heads, c.dim}, kc.options().dtype(dtype));
+        out[i] = fresh({tokens, c.heads, c.dim}, dtype, kc);
       } else {
         out[i] = tensor(a[8 + i], names[i]);
         if (out[i].sizes() != at::IntArrayRef({tokens, c.heads, c.dim}))
@@ -436,7 +443,7 @@ PyObject* decode8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     oa = attn_tensor{oa.ptr, oa.stride_s, 0, oa.stride_h};
     at::Tensor lse;
     if (a[12] == Py_None) {
-      lse = at::empty({batch, hq}, q.options().dtype(at::kFloat));
+      lse = fresh({batch, hq}, at::kFloat, q);
     } else {
       lse = tensor(a[12], "lse");
       if (!lse.is_cuda() || lse.get_device() != at.index || lse.scalar_type() != at::kFloat || lse.dim() != 2 ||
@@ -492,7 +499,7 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t most = share ? rows : rows * width;
     at::Tensor copies, counts;
     if (a[10] == Py_None) {
-      copies = at::empty({most, 2}, table.options());
+      copies = fresh({most, 2}, at::kInt, table);
     } else {
       copies = tensor(a[10], "copies");
       if (!copies.is_cuda() || copies.get_device() != index || copies.scalar_type() != at::kInt || copies.dim() != 2 ||
@@ -501,7 +508,7 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
                shape(copies), " on ", copies.device().str());
     }
     if (a[11] == Py_None) {
-      counts = at::empty({2}, table.options());
+      counts = fresh({2}, at::kInt, table);
     } else {
       ints(a[11], "counts", index, 2);
       counts = tensor(a[11], "counts");
