@@ -609,11 +609,12 @@ cudaError_t launch_append(const Append8Params& p, cudaStream_t stream) {
   const int64_t rows = p.tokens / seqs < p.cache.block.d ? (p.tokens + seqs - 1) / seqs : p.cache.block.d;
   g.share_log2 = 0;
   while (g.share_log2 < kMostShares && ((kHeld << 5 >> g.lanes_log2) << g.share_log2) < rows) ++g.share_log2;
-  // few blocks of tokens: several blocks share the heads of each, down to one for each warp
+  // few blocks of tokens: several blocks share the heads of each, down to one for each warp; many:
+  // a block of tokens is cut so that about four pieces come to each block
   const int64_t jobs = static_cast<int64_t>(p.h_q) + 2 * static_cast<int64_t>(p.h_k);
   const int at_once = kWarps >> g.share_log2;
   const int64_t fit = (jobs + at_once - 1) / at_once;
-  int64_t parts = 4 * most / units;
+  int64_t parts = units < most ? most / units : 4 * most / units;
   parts = parts < 1 ? 1 : (parts > fit ? fit : parts);
   g.parts = static_cast<int>(parts);
   const int64_t items = units * parts;
