@@ -39,6 +39,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kWeight = 16384.f;  // factor of the weights and of O until it is written
 constexpr int kKeys = 32;           // of a warp and tile
+constexpr int kUnitLog2 = 7, kUnit = 1 << kUnitLog2;  // keys of a unit of the line: half a tile
 constexpr float kLeast = 8.673617379884035e-19f, kMost = 1.152921504606847e18f;  // factors of V: 2^-60, 2^60
 
 template <int DP, int HN>
@@ -231,24 +232,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
   const uint32_t vp = static_cast<uint32_t>(p.cache.v.sb / 16), vslot = static_cast<uint32_t>(p.cache.v.ss / 16);
   const uint32_t fkp = static_cast<uint32_t>(p.ks[0]), fkb = static_cast<uint32_t>(p.ks[1]);
   const uint32_t fvp = static_cast<uint32_t>(p.vs[0]), fvb = static_cast<uint32_t>(p.vs[1]);
-  // this lane's key of the first tile: of tiles of 128 keys a warp has 16
-  const bool lane_on = lane < (4 << (p.tile_log2 - 5));
-  const int key0 = (warp << (p.tile_log2 - 3)) + lane;
   // The walk stands at the tile that is planned: it moves on when the next one is.
   uint32_t pend_page = 0, pend_within = 0;
   int flags = kBegin;
-  bool pend_live = false, first = true;
+  bool pend_live = false;
+  int units = 0;  // of the line that the planned tile takes: two, or the one that is left
   auto plan = [&]() {  // moves on and looks the tile up
     pend_live = false;
     if (left == 0) {
       flags = kNone;
       return;
     }
-    if (!first) {
+    if (units > 0) {
       flags &= kSecond;
-      if (ct != cnt - 1) {
-        ++ct;
-      } else {
+      ct += units;
+      if (ct == cnt) {
         ct = 0;
         flags = kBegin | kSecond;
         seg_from_start = true;
@@ -262,12 +260,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
         load_head();
       }
     }
-    first = false;
-    --left;
-    if (ct == cnt - 1) flags |= seg_from_start ? kEnd | kFull : kEnd;
+    units = left > 1 && ct + 1 < cnt ? 2 : 1;
+    left -= units;
+    if (ct + units == cnt) flags |= seg_from_start ? kEnd | kFull : kEnd;
     if (left == 0) flags |= kEnd;
-    const int j = cfirst + (ct << p.tile_log2) + key0;
-    pend_live = lane_on && j < cn;
+    // a warp has 32 keys of two units, 16 of one
+    const int j = cfirst + ct * kUnit + warp * (units * kUnit / kWarps) + lane;
+    pend_live = lane < units * kUnit / kWarps && j < cn;
     if (pend_live) {
       const uint32_t n = p.cache.page.div(static_cast<uint32_t>(j));
       pend_within = static_cast<uint32_t>(j) - n * p.cache.page.d;
@@ -505,10 +504,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
             for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
             const float mx = fmaxf(m[n][c], top);
-            const float f = mx == m[n][c] ? 1.f : ex2(m[n][c] - mx);
+            // (in halves: a step may be larger than fp32's exponents, where the sum starts at 2^60)
+            const float h = mx == m[n][c] ? 1.f : ex2(0.5f * (m[n][c] - mx)), f = h * h;
             m[n][c] = mx;
             base[n][c] = mx == -INFINITY ? 0.f : mx;
-            l[n][c] *= f;
+            l[n][c] = l[n][c] * h * h;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               o[k][n][c] *= f;
@@ -596,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float2 y = *reinterpret_cast<const float2*>(from + w * C::kWarpBytes);
-            const float f = ex2(s_max[w][row] - low);
+            const float h = ex2(0.5f * (s_max[w][row] - low)), f = h * h;
             x.x = fmaf(y.x, f, x.x);
             x.y = fmaf(y.y, f, x.y);
-            sum = fmaf(s_sum[w][row], f, sum);
+            sum = fmaf(s_sum[w][row] * h, h, sum);
           }
           if (whole) {
             const bool none = sum == 0.f;
@@ -612,10 +612,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
               p.lse[static_cast<int64_t>(b) * p.h_q + h0 + row] =
                   none ? INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
           } else {
-            *reinterpret_cast<float2*>(part + row * DP + col) = make_float2(x.x * (1.f / kWeight), x.y * (1.f / kWeight));
+            // the maximum without V's exponents, as the kernel that joins takes it: the sum lies in [1, 2)
+            const int e = sum > 0.f ? min(max(static_cast<int>(__float_as_uint(sum) >> 23) - 127, -126), 126) : 0;
+            const float down = __int_as_float((127 - e) << 23);
+            *reinterpret_cast<float2*>(part + row * DP + col) =
+                make_float2(x.x * (1.f / kWeight) * down, x.y * (1.f / kWeight) * down);
             if (col == 0) {
-              part[p.part_rows * DP + row] = top;
-              part[p.part_rows * DP + kMaxRows + row] = sum;
+              part[p.part_rows * DP + row] = top + static_cast<float>(e);
+              part[p.part_rows * DP + kMaxRows + row] = sum * down;
             }
           }
         }
@@ -632,7 +636,7 @@ cudaError_t launch_main(Decode8Params p, cudaStream_t stream) {
   using C = Cfg<DP, HN>;
   static std::atomic<unsigned long long> done{0};  // devices with the attribute set
   int runs;
-  cudaError_t e = shape_decode(p, 8, C::kBlocks, &runs);
+  cudaError_t e = shape_decode(p, kUnitLog2, C::kBlocks, &runs);
   if (e != cudaSuccess) return e;
   if (runs > 0) {
     int dev = 0;

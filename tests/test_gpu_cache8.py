@@ -268,6 +268,36 @@ def test_decode_with_factors_far_apart(dt, kind, exps):
     check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, d ** -0.5)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("low,high", [(0.0, 60), (-60, 60), (60, -60), (60, 0.0)])
+@pytest.mark.parametrize("n,cut", [(4096, 2048), (600, 320), (200, 16)])
+def test_decode_where_factors_change_along_the_sequence(kind, low, high, n, cut):
+    """The maximum that weights are taken from follows V's factors; the softmax's sum must not.  The
+    first keys, up to 2^20 times less probable, have one factor (0.0: none), the others another."""
+    d = 64
+    kc, vc, ks, vs, table = make_cache8(n, 1, 1, d, 16, 16, kind, 18, exps=(-6, -6))
+    rows = table[0].long()
+    for lo, hi, f in ((0, cut // 16, low), (cut // 16, len(rows), high)):
+        vs[rows[lo:hi]] = 2.0 ** f if f != 0.0 else 0.0
+    g = torch.Generator().manual_seed(5)
+    for shift in (0.0, -8.0, -20.0, 8.0):  # of the first keys' base-2 logits
+        first = (torch.arange(n) < cut).float()
+        want = torch.randn(n, generator=g) + shift * first
+        kc.view(torch.uint8).zero_()
+        page, at = rows[torch.arange(n) // 16], torch.arange(n) % 16
+        # a logit is code * factor * q: codes of 1 / 4 of a step, q makes them base-2 logits
+        code = (want * 4).round().clamp(-100, 100)
+        codes = kc.float()
+        codes[page, at, 0, 0] = code.cuda()
+        kc.view(torch.uint8).copy_(codes.to(kc.dtype).view(torch.uint8))
+        q = torch.zeros(1, 2, d, dtype=torch.bfloat16, device="cuda")
+        q[0, :, 0] = 16.0
+        scale = float(np.log(2.0))
+        o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints([n]), scale=scale)
+        ab.check_device_status()
+        check_decode8(o, lse, q, kc, vc, ks, vs, table, [n], scale)
+
+
 @pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -100])
 def test_decode_of_queries_far_from_one(size):
     lens, d = [300], 128
