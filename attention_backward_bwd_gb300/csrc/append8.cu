@@ -36,6 +36,9 @@ constexpr int kMostShares = 2; // log2 of the warps that share tokens
 constexpr int kLoads = 4;      // of a lane and of each of k and v, in a read-back
 constexpr float kLargest = 1.152921504606847e18f;    // 2^60
 
+// Chunks before which a lane looks whether there are more: the work of those between is mixed.
+__device__ constexpr bool looks(int i) { return i == 1 || i == 2 || i % 4 == 0; }
+
 // Where the other element of a pair is: kHalves in the lane n_freq / 8 further (n_freq a multiple
 // of 8), kPairs in the lane's own chunk, kMixed anywhere, read once more.
 enum RopeMode { kNoTurn = 0, kHalves = 1, kPairs = 2, kMixed = 3 };
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             }
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-              if (i >= left) break;
+              if (looks(i) && i >= left) break;
               if (MODE != kMixed) {
                 float v[8];
                 take(i, t0, v);
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
               uint32_t two = 0;
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i >= left) break;
+                if (looks(i) && i >= left) break;
                 two = most_of(most_of(most_of(most_of(two, raw[i].x, T()), raw[i].y, T()), raw[i].z, T()), raw[i].w, T());
               }
               const float2 y = Pack<T>::unpack(two);
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             } else {
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i >= left) break;
+                if (looks(i) && i >= left) break;
                 float v[8];
                 take(i, t0, v);
 #pragma unroll
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
               clean = false;
 #pragma unroll
               for (int i = 0; i < kHeld; ++i) {
-                if (i >= left) break;
+                if (looks(i) && i >= left) break;
                 float v[8];
                 take(i, t0, v);
 #pragma unroll
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
           auto put = [&](auto fits) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-              if (i >= left) break;
+              if (looks(i) && i >= left) break;
               float v[8];
               take(i, t0, v);
               if (i < stores)
