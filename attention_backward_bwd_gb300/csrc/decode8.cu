@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
       }
     }
 
-#pragma unroll
+#pragma unroll 1
     for (int sub = 0; sub < kSubs; ++sub) {
       if (sub > 0) {
         cp_wait<S - 2>();
