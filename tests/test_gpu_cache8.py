@@ -395,6 +395,40 @@ def test_decode_into_strided_outputs_on_a_stream_and_in_a_graph():
         check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_and_load_on_a_stream_and_in_a_graph(inter):
+    kind, page, hk, d = "int8", 16, 2, 64
+    kc, vc, ks, vs, table = make_cache8(80, 3, hk, d, page, 8, kind, 19)
+    q, k, v = (torch.randn(9, h, d).half().cuda() for h in (4, hk, hk))
+    n, cu, pos, inv = ints([3, 40, 7]), ints([0, 4, 5, 9]), ints(list(range(9))), torch.rand(32, device="cuda")
+    twin = [x.clone() for x in (kc, vc, ks, vs)]
+
+    def run(cache, stream=None):
+        got = ab.attn_cache_append8(k, v, *cache, table, n, cu, q=q, positions=pos, inv_freq=inv, interleaved=inter,
+                                    stream=stream)
+        return got, *ab.attn_cache_load8(*cache, table, n, cu, 9, dtype=torch.float16, stream=stream)
+
+    want = run(twin)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run((kc, vc, ks, vs), side)
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run((kc, vc, ks, vs))
+    for old in ([0, 9, 64], [5, 5, 5]):
+        n.copy_(ints(old))
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape))
+        graph.replay()
+        want = run(twin)
+        ab.check_device_status()
+        for x, y in zip((*got, kc, vc, ks, vs), (*want, *twin)):
+            assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("kind,dt,hf", [("e4m3", "bf16", False), ("int8", "fp16", True)])

@@ -146,9 +146,10 @@ def test_fork_reports_what_it_cannot_do():
     assert "no free page" in told() and got[4].tolist() == [0, 0] and got[0][2].tolist() == [*table[1, :2].tolist(), -1]
 
 
-def test_fork_of_strided_tables_in_a_graph():
+@pytest.mark.parametrize("pages", [200, 120000])  # one launch, a launch a step
+def test_fork_of_strided_tables_in_a_graph(pages):
     rng = np.random.default_rng(4)
-    lens, page, pages = rng.integers(1, 60, 8), 8, 200
+    lens, page = rng.integers(1, 60, 8), 8
     table, refs = pool(rng, lens, page, 9, pages)
     big = torch.full((8, 20), 55, dtype=torch.int32, device="cuda")
     t, n, r, who = big[:, 3:12], ints(lens), ints(refs), ints(list(range(8)))
@@ -222,6 +223,25 @@ def test_copy_reports_bad_pages():
     ab.attn_cache_copy(kc, vc, ints([[4, 5]]), stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(kc[5], kc[4])
+
+
+def test_calls_on_a_stream_of_their_own():
+    rng = np.random.default_rng(7)
+    for pages in (300, 120000):
+        lens, page = rng.integers(1, 60, 8), 8
+        table, refs = pool(rng, lens, page, 9, pages)
+        a = (ints(table), ints(lens), ints(refs))
+        parents, twin = rng.integers(0, 8, 8), [x.clone() for x in a]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = ab.attn_cache_fork(*a, page, parents=ints(parents), room=2, stream=side)
+        handle = ab.attn_cache_fork(*twin, page, room=0, stream=0)  # the default stream
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        ab.check_device_status()
+        check(table, lens, refs, page, parents, [2] * 8, True, got, None)
+        assert handle[4][0].item() == 0
 
 
 def test_copy_of_pages_behind_4_gib():
