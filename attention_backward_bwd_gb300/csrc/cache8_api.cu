@@ -292,8 +292,8 @@ int attn_cache_copy(const attn_paged_kv8* cache, int element_size, int h_k, int 
                 kv.page_size, h_k, head_dim);
   if (head_dim > 256 || head_dim % unit != 0)
     return fail(ATTN_ERR_SHAPE, "head_dim must be a multiple of %d of at most 256, got %d", unit, head_dim);
-  if (static_cast<int64_t>(kv.page_size) * h_k > INT32_MAX / (head_dim / unit))
-    return fail(ATTN_ERR_SHAPE, "a page must stay below 2^31 pieces of 16 bytes");
+  if (static_cast<int64_t>(kv.page_size) * h_k > (1 << 30) / (head_dim / unit))
+    return fail(ATTN_ERR_SHAPE, "a page must stay below 2^30 pieces of 16 bytes");
   if (num_pairs < 0) return fail(ATTN_ERR_SHAPE, "num_pairs must be >= 0, got %d", num_pairs);
   int rc;
   if ((rc = check_rows(&kv.k, "k cache", kv.num_pages, kv.page_size, h_k, unit))) return rc;

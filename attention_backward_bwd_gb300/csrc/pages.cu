@@ -402,9 +402,13 @@ __global__ void __launch_bounds__(kForkThreads) copy_refs_kernel(const int* from
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kFlight = 4;  // 16-byte pieces of a thread in flight
+// Copies of more than this pass the L2 by, with eight 16-byte pieces of a thread in flight; less is
+// left there, with four (4000 pages of 128 KB 168 us and, the other way, 185; 48 pages of 256 KB
+// 6.3 and 4.4).
+constexpr int64_t kPassing = 64 << 20;
 
 // A block takes a part of a page of k or of v, and with a page's first part its factors.
+template <int kFlight, bool kPass>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p, FastDiv run, FastDiv row, int parts) {
   const int n = p.count == nullptr ? p.num_pairs : min(max(*p.count, 0), p.num_pairs);
   const int64_t items = static_cast<int64_t>(n) * 2 * parts;
@@ -434,12 +438,15 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p, FastDi
       const int r = static_cast<int>(run.div(i)), c = i - r * p.chunks;
       const int r0 = static_cast<int>(row.div(r)), r1 = r - r0 * p.rows[1];
       off[k] = r0 * t.ss + r1 * t.sh + static_cast<int64_t>(c) * 16;
-      x[k] = __ldcs(reinterpret_cast<const uint4*>(from + off[k]));
+      const uint4* at = reinterpret_cast<const uint4*>(from + off[k]);
+      x[k] = kPass ? __ldcs(at) : *at;
     }
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
       if (i0 + k * kCopyThreads >= total) break;
-      __stcs(reinterpret_cast<uint4*>(to + off[k]), x[k]);
+      uint4* at = reinterpret_cast<uint4*>(to + off[k]);
+      if (kPass) __stcs(at, x[k]);
+      else *at = x[k];
     }
     if (part == 0 && p.k_scale != nullptr) {
       float* s = is_v ? p.v_scale : p.k_scale;
@@ -522,9 +529,13 @@ cudaError_t launch_copy(const CopyParams& p, cudaStream_t stream) {
   FastDiv run, row;
   run.set(static_cast<uint32_t>(p.chunks));
   row.set(static_cast<uint32_t>(p.rows[1]));
-  const int parts = ceil_div(p.rows[0] * p.rows[1] * p.chunks, kCopyThreads * kFlight);
+  const int64_t pieces = static_cast<int64_t>(p.rows[0]) * p.rows[1] * p.chunks;
+  const bool pass = pieces > kPassing / 64 / p.num_pairs;  // k and v, read and written
+  const int flight = pass ? 8 : 4, parts = static_cast<int>((pieces + kCopyThreads * flight - 1) / (kCopyThreads * flight));
   const int64_t items = static_cast<int64_t>(p.num_pairs) * 2 * parts, most = static_cast<int64_t>(num_sms()) * 8;
-  copy_kernel<<<static_cast<unsigned>(items < most ? items : most), kCopyThreads, 0, stream>>>(p, run, row, parts);
+  const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  if (pass) copy_kernel<8, true><<<grid, kCopyThreads, 0, stream>>>(p, run, row, parts);
+  else copy_kernel<4, false><<<grid, kCopyThreads, 0, stream>>>(p, run, row, parts);
   return cudaGetLastError();
 }
 

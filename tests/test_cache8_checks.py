@@ -132,7 +132,7 @@ CASES = [(f, kw, code) for f in (append, load, decode) for kw, code in BAD_CACHE
     (fork, dict(counts=A[4] + 16), ARG), (fork, dict(r2=A[1]), ARG), (fork, dict(ws=None), WS), (fork, dict(ws=A[10] + 4), WS),
     (fork, dict(size=64), WS),
     (copy, dict(c=None), NULL), (copy, dict(size=4), DTYPE), (copy, dict(d=72), SHAPE), (copy, dict(d=0), SHAPE),
-    (copy, dict(hk=0), SHAPE), (copy, dict(n=-1), SHAPE), (copy, dict(pairs=None), NULL), (copy, dict(pairs=P + 2), ALIGN),
+    (copy, dict(hk=0), SHAPE), (copy, dict(c=paged8(size=1 << 28, block=1 << 28)), SHAPE), (copy, dict(n=-1), SHAPE), (copy, dict(pairs=None), NULL), (copy, dict(pairs=P + 2), ALIGN),
     (copy, dict(count=P + 1), ALIGN), (copy, dict(c=paged8(fk=0)), ARG), (copy, dict(c=paged8(block=5)), SHAPE),
     (copy, dict(c=paged8(kh=72)), STRIDE), (copy, dict(c=paged8(vptr=0)), NULL), (copy, dict(c=paged8(st=(4, 0, 1))), STRIDE),
 ]
