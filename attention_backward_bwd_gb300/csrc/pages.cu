@@ -10,7 +10,7 @@
 // barrier parts the steps: bound by their chain, each some loads long.  Large ones (kLarge) take a
 // launch a step, with all of the GPU for the references and the rows: a reference is an atomic
 // operation, of which an SM issues one a cycle or so (512 rows of 1025 pages: 84 us in one cluster,
-// see launch_fork).
+// 23 in launches, of which the host's part is 11).
 // attn_cache_copy moves whole pages, 16 bytes a thread, several in flight: bound by the memory.
 #include <atomic>
 
@@ -28,7 +28,9 @@ constexpr int kEntries = 8;    // of a lane in flight
 constexpr int kChunk = 32 * kEntries;
 // Rows whose state is kept in shared memory: 12 bytes each, and 8 more for the prefix sums.
 constexpr int kRows = 8192;
-constexpr int64_t kLarge = 100000;  // entries and pages
+// Entries and pages from which every step has a launch of its own (the cluster and the launches:
+// 6600 11.0 and 11.9 us, 24900 14.7 and 12.4, 95700 37.2 and 14.3).
+constexpr int64_t kLarge = 16000;
 
 // Steps of a launch.
 enum { kRefs = 1, kList = 2, kWrite = 4, kAllSteps = 7 };
