@@ -159,11 +159,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
   // turns of a row: the last ones, up to a multiple of 4, turn by nothing
   const int nf = MODE == kNoTurn ? 0 : p.rot.n_freq, pitch = MODE == kNoTurn ? 4 : (nf + 3) / 4 * 4;
 
-  // fraction of a turn that one position adds at each frequency, times 2^64
-  for (int i = tid; i < nf; i += kThreads) {
-    const double x = static_cast<double>(p.rot.inv_freq[i]) * 0.15915494309189535;
-    turns[i] = static_cast<unsigned long long>((x - floor(x)) * 18446744073709551616.0);
-  }
+  const float inv_freq = tid < nf ? p.rot.inv_freq[tid] : 0.f;  // (at most 128)
   // ---- blocks of the sequences before this thread's
   const int per = (p.batch + kThreads - 1) / kThreads;
   int64_t mine = 0;
@@ -179,6 +175,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
     if (lane >= i) x += y;
   }
   if (lane == 31) s_sums[warp] = x;
+  if (tid < nf) {  // fraction of a turn that one position adds at each frequency, times 2^64
+    const double y = static_cast<double>(inv_freq) * 0.15915494309189535;
+    turns[tid] = static_cast<unsigned long long>((y - floor(y)) * 18446744073709551616.0);
+  }
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll
