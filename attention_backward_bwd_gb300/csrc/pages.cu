@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t cluster_blocks() {
 
 // Workspace of a fork: per row the pages and copies it needs and their prefix sums (beyond kRows
 // rows also the first row that takes it over, its parent and its length); per block its free
-// pages; the copies made, the pages needed and the free ones; then the list of free pages and,
+// pages; the pages needed and those granted; then the list of free pages and,
 // where the table is its own output, the old table.
 struct ForkWs {
   int *fresh, *copied, *who, *parent, *len, *fresh_before, *copied_before, *free_of, *sums, *list, *old;
@@ -155,12 +155,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
         for (int k = 0; k < kEntries; ++k)
           if (i0 + k * step < p.num_pages) p.refs_out[i0 + k * step] = x[k];
       }
-    if (STEPS & kRefs && at == 0) w.sums[0] = 0;
     if (few) __syncthreads();
     else sync();
     for (int b = b0; b < p.rows; b += bs)
       if (w.parent[b] >= 0) atomicMin(w.who + w.parent[b], b);
-    if (STEPS == kAllSteps) sync();  // the references are where they will be, too
+    // (one launch: the references are where they will be, too)
+    if (STEPS == kAllSteps && (copy_refs || !few)) sync();
     else __syncthreads();
   }
 
@@ -285,10 +285,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
 #pragma unroll
       for (int k = 0; k < kEntries; ++k) free_here += x[k] == 0;
     }
-    int total, wanted = 0;
+    int total, wanted = 0, copied0 = 0;
     const bool here = STEPS == kAllSteps && few;  // the prefix sums are each block's own
     if (here || rank == 0) {
-      int copied0 = 0;
       for (int r0 = 0; r0 < p.rows; r0 += kForkThreads) {
         const int b = r0 + tid;
         const int fresh = b < p.rows ? __ldcg(w.fresh + b) : 0, copied = b < p.rows ? __ldcg(w.copied + b) : 0;
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
         if (b < p.rows) w.copied_before[b] = copied0 + c;
         copied0 += total;
       }
-      if (!here && tid == 0) w.sums[1] = wanted;
+      if (rank == 0 && tid == 0) w.sums[1] = wanted;
     }
     block_prefix(free_here, s_sums, total);
     if (tid == 0) w.free_of[rank] = total;
@@ -331,9 +330,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
         }
       first += n;
     }
-    if (STEPS == kList && rank == 0 && tid == 0) {
+    if (rank == 0 && tid == 0) {
       w.sums[2] = granted;
-      p.counts[0] = 0;
+      p.counts[0] = granted == wanted ? copied0 : 0;  // where pages run out the rows count their copies
       p.counts[1] = all - granted;
     }
   }
@@ -342,6 +341,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
   if (STEPS & kWrite) {
     // ---- the new rows
     if (STEPS == kWrite) granted = __ldcg(w.sums + 2);
+    const bool run_out = __ldcg(w.sums + 2) < __ldcg(w.sums + 1);
     for (int64_t item = at >> 5; item < items; item += step >> 5) {
       const int b = static_cast<int>(item / chunks), i0 = static_cast<int>(item - static_cast<int64_t>(b) * chunks) * kChunk;
       const Row r = row_of(b, false);
@@ -386,15 +386,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
       made = __reduce_add_sync(0xffffffffu, made);
       if (lane == 0) {
         if (i0 == 0) p.seqlens_out[b] = r.n;
-        if (made > 0) atomicAdd(STEPS == kWrite ? p.counts : w.sums, made);
+        if (run_out && made > 0) atomicAdd(p.counts, made);
       }
-    }
-  }
-  if (STEPS == kAllSteps) {
-    sync();
-    if (at == 0) {
-      p.counts[0] = __ldcg(w.sums);
-      p.counts[1] = all - granted;
     }
   }
 }
