@@ -395,6 +395,59 @@ def test_decode_into_strided_outputs_on_a_stream_and_in_a_graph():
         check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("d", [32, 48, 160, 176, 208, 224, 240])
+def test_other_head_dims(d):
+    # a prompt and single tokens into blocks of 8, and attention over them
+    dt, kind, page, hk = torch.float16, "e4m3" if d % 32 else "int8", 24, 2
+    kc, vc, ks, vs, table = make_cache8(300, 2, hk, d, page, 8, kind, 20)
+    want, fac, tab = numbers(vc), f64(vs), table.cpu().numpy()
+    lens = [0, 5]
+    for new in ([250, 3], [1, 1], [1, 1]):
+        cu = [0, new[0], sum(new)]
+        q, k, v = (torch.randn(cu[2], h, d).to(dt).cuda() for h in (3 * hk, hk, hk))
+        pos, inv = ints(list(range(cu[2]))), torch.rand(d // 2, device="cuda")
+        got = ab.attn_cache_append8(k, v, kc, vc, ks, vs, table, ints(lens), ints(cu), q=q, positions=pos, inv_freq=inv)
+        ab.check_device_status()
+        for b in range(2):
+            c8.append(want, fac, tab[b], page, lens[b], f64(v)[cu[b]:cu[b + 1]], kind)
+        assert np.array_equal(numbers(vc), want) and np.array_equal(f64(vs), fac)
+        rq = co.rope(f64(q), [list(range(cu[2]))], inv.cpu().numpy(), (d // 2,))
+        assert (np.abs(f64(got) - rq) <= HALF_STEP[dt] * np.abs(rq) + 2.0 ** -19 * 2 * np.abs(f64(q)).max()).all()
+        lens = [a + b for a, b in zip(lens, new)]
+        last = got[[cu[1] - 1, cu[2] - 1]]
+        o, lse = ab.attn_decode8(last, kc, vc, ks, vs, table, ints(lens))
+        ab.check_device_status()
+        check_decode8(o, lse, last, kc, vc, ks, vs, table, lens, d ** -0.5)
+
+
+def test_many_sequences():
+    # more of them than a block has threads, some without keys
+    batch, hk, d, page = 700, 2, 64, 16
+    rng = np.random.default_rng(21)
+    lens = rng.integers(0, 60, batch)
+    kc, vc, ks, vs, table = make_cache8(64, batch, hk, d, page, 16, "int8", 21)
+    want, fac, tab = numbers(vc), f64(vs), table.cpu().numpy()
+    new = rng.integers(0, 4, batch)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    k, v = torch.randn(2, int(cu[-1]), hk, d).half().cuda()
+    ab.attn_cache_append8(k, v, kc, vc, ks, vs, table, ints(lens), ints(cu))
+    ab.check_device_status()
+    for b in range(batch):
+        c8.append(want, fac, tab[b], page, int(lens[b]), f64(v)[cu[b]:cu[b + 1]], "int8")
+    assert np.array_equal(numbers(vc), want) and np.array_equal(f64(vs), fac)
+    gk, gv = ab.attn_cache_load8(kc, vc, ks, vs, table, ints(lens), ints(cu), int(cu[-1]), dtype=torch.float16)
+    ab.check_device_status()
+    for b in range(0, batch, 7):
+        j = range(int(lens[b]), int(lens[b] + new[b]))
+        assert torch.equal(gv[cu[b]:cu[b + 1]].cpu(), torch.from_numpy(slots_of(vc, vs, table, b, j)).half())
+        assert torch.equal(gk[cu[b]:cu[b + 1]].cpu(), torch.from_numpy(slots_of(kc, ks, table, b, j)).half())
+    lens = [int(x) for x in lens + new]
+    q = torch.randn(batch, 4, d).bfloat16().cuda()
+    o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints(lens))
+    ab.check_device_status()
+    check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, d ** -0.5)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_append_and_load_on_a_stream_and_in_a_graph(inter):
     kind, page, hk, d = "int8", 16, 2, 64
