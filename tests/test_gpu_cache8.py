@@ -249,6 +249,19 @@ def test_decode(case):
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("group", [2, 8, 11, 16])
+@pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
+def test_decode_every_width_and_group(kind, group, d):
+    lens = [777, 0, 130, 2500]
+    kc, vc, ks, vs, table = make_cache8(2500, 4, 2, d, 32, 16, kind, 22, heads_first=d == 96)
+    q = torch.randn(4, 2 * group, d, generator=torch.Generator().manual_seed(d)).bfloat16().cuda()
+    for window, cap in ((-1, 0.0), (300, 25.0)):
+        o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints(lens), window=(window, 0), softcap=cap)
+        ab.check_device_status()
+        check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, d ** -0.5, window, cap)
+
+
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 @pytest.mark.parametrize("exps", [(-40, 30), (-60, -50), (50, 60)])
