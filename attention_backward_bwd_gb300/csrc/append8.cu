@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
             was = was > 0.f ? fminf(was, kLargest) : 0.f;
             float now = factor_of<INT8>(top);
-            if (factor != nullptr && now > was && was > 0.f) {
-              const float ratio = was / now;
+            if (factor != nullptr && now > was && old > 0) {
+              const float ratio = was / now;  // (0 where they stood for zeros)
               const int per_row = p.head_dim / 16;
               for (int i = lane + 32 * member; i < old * per_row; i += 32 << g.share_log2) {
                 const int r = i / per_row;
