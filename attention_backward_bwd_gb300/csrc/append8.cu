@@ -65,7 +65,7 @@ __device__ __forceinline__ float factor_of(float top) {
   return __int_as_float((min(max(e, -60), 60) + 127) << 23);
 }
 
-// The codes of x inv.  kClean: all x are finite and none is beyond the largest code.
+// The codes of x inv.  kClean: of int8, all x are finite and none is beyond the largest code.
 template <bool INT8, bool kClean = false>
 __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float inv) {
   if (INT8) {
@@ -80,6 +80,26 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, fl
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// A result y that was rounded to 24 bits, given what is left of it (only the sign counts): the number
+// with an odd last bit next to it.  That rounds on to the few bits of a code or a 16-bit type, and at
+// their ties, as the exact result does.
+__device__ __forceinline__ float odd_of(float y, float left) {
+  const uint32_t u = __float_as_uint(y);
+  if (!(left < 0.f || left > 0.f) || y == 0.f) return y;
+  return __uint_as_float(((u ^ __float_as_uint(left)) >> 31) == 0 ? u | 1u : (u - 1u) | 1u);
+}
+__device__ __forceinline__ float times(float x, float f) {
+  const float y = x * f;
+  return odd_of(y, fmaf(x, f, -y));
+}
+// x / f, given 1 / f: the quotient is put right by what is left, so that it is next to the exact one.
+__device__ __forceinline__ float over(float x, float f, float inv) {
+  const float y = x * inv;
+  if (!(fabsf(y) < INFINITY)) return y;
+  const float z = fmaf(fmaf(-y, f, x), inv, y);
+  return odd_of(z, fmaf(-z, f, x));
 }
 
 template <bool INT8>
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
         factor = (is_v ? p.cache.v_scale : p.cache.k_scale) + page * st[0] + blk * st[1] + head * st[2];
         if (old > 0) was = *factor;
       }
-      float top = 0.f, inv = 0.f;
+      float top = 0.f, now = 0.f, inv = 0.f;
       bool clean = true;  // all are finite
       char* to = nullptr;
       int64_t step = 0;
@@ -466,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
             const TensorArg& pages = is_v ? p.cache.pages.v : p.cache.pages.k;
             to = static_cast<char*>(const_cast<void*>(pages.ptr)) + page * pages.sb + within * pages.ss + head * pages.sh;
             was = was > 0.f ? fminf(was, kLargest) : 0.f;
-            float now = factor_of<INT8>(top);
+            now = factor_of<INT8>(top);
             if (factor != nullptr && now > was && old > 0) {
               const float ratio = was / now;  // (0 where they stood for zeros)
               const int per_row = p.head_dim / 16;
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const float4 y = value4<INT8>(w[k]);
-                  w[k] = code4<INT8>(y.x, y.y, y.z, y.w, ratio);
+                  w[k] = code4<INT8>(times(y.x, ratio), times(y.y, ratio), times(y.z, ratio), times(y.w, ratio), 1.f);
                 }
                 *at16 = codes;
               }
@@ -493,19 +513,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append8_kernel(Append8Param
           // ---- codes
           char* out = to + t0 * (step >> (5 - g.lanes_log2));
           const int stores = factor != nullptr ? rows : 0;
+          // x / s is a product where s is a power of two, which an earlier factor need not be
+          const bool power = (__float_as_uint(now) & 0x7fffffu) == 0;
           auto put = [&](auto fits) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
               if (looks(i) && i >= left) break;
               float v[8];
               take(i, t0, v);
+              if (!fits.value && !power)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = over(v[k], now, inv);
+              const float mul = !fits.value && !power ? 1.f : inv;
               if (i < stores)
-                *reinterpret_cast<uint2*>(out) = make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], inv),
-                                                            code4<INT8, fits.value>(v[4], v[5], v[6], v[7], inv));
+                *reinterpret_cast<uint2*>(out) = make_uint2(code4<INT8, fits.value>(v[0], v[1], v[2], v[3], mul),
+                                                            code4<INT8, fits.value>(v[4], v[5], v[6], v[7], mul));
               out += step;
             }
           };
-          if (INT8 && clean) put(std::true_type());
+          if (power && (!INT8 || clean)) put(std::true_type());
           else put(std::false_type());
         }
       }

@@ -48,3 +48,82 @@ def test_append_behind_a_factor_of_zero(kind, d, page, block, old, new):
     v[:, 0] *= 64.0  # the other head's factor grows
     assert (numbers(kc) != 0).any() and (numbers(vc) != 0).any()
     appended(kc, vc, ks, vs, table, page, old, cu, k, v, kind)
+
+
+def borders(kind):
+    """Numbers half way between neighbouring codes."""
+    if kind == "int8":
+        return np.arange(0.5, 127)
+    v = c8.e4m3_values()
+    return (v[1:] + v[:-1])[40:] / 2
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_append_takes_the_nearest_code_behind_any_factor(kind, dt):
+    """x next to the middle of two codes of a factor that is no power of two: that middle is missed by
+    less than 2^-24 of it, where x times the factor's reciprocal lies on the other side or on it."""
+    batch, heads, d, page = 64, 8, 16, 2
+    kc, vc, ks, vs, table = make_cache8(2, batch, heads, d, page, 2, kind, 32)
+    rng = np.random.default_rng(4)
+    mids = borders(kind)
+    mid = rng.choice(mids[mids <= c8.TOP[kind] / 2], (batch, heads))  # so that the factor stays
+    x = torch.from_numpy(rng.uniform(1.0, 2.0, (batch, heads))).to(DT[dt])
+    factor = (f64(x) / mid).astype(np.float32)
+    # the reciprocal's way: it rounds off another code than the nearest for some
+    near = c8.code(f64(x) / factor.astype(np.float64), kind)
+    twice = c8.code((x.float().numpy() * (np.float32(1.0) / factor)).astype(np.float64), kind)
+    assert (near != twice).sum() > 20
+    for s in (ks, vs):
+        s[table[:, 0].long(), 0] = torch.from_numpy(factor).cuda()
+    k, v = torch.zeros(2, batch, heads, d, dtype=DT[dt])
+    k[:, :, 3], v[:, :, 12] = x, -x
+    v[::2, :, 5] = float("inf")  # (its code is the largest one)
+    want = [(numbers(c), f64(s)) for c, s in ((kc, ks), (vc, vs))]
+    ab.attn_cache_append8(k.cuda(), v.cuda(), kc, vc, ks, vs, table, ints([1] * batch))
+    ab.check_device_status()
+    rows = table[:, 0].long().cpu().numpy()
+    for (codes, fac), at, sign, got, got_s in zip(want, (3, 12), (1, -1), (kc, vc), (ks, vs)):
+        codes[rows, 1] = 0
+        codes[rows, 1, :, at] = sign * near
+        if at == 12:
+            codes[rows[::2], 1, :, 5] = c8.TOP[kind]
+        assert np.array_equal(f64(got_s), fac)
+        assert np.array_equal(numbers(got), codes)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_append_rounds_earlier_codes_of_any_factor_to_the_nearest(kind):
+    # code * factor / 2^e next to the middle of two codes
+    batch, heads, d, page = 64, 8, 16, 2
+    kc, vc, ks, vs, table = make_cache8(2, batch, heads, d, page, 2, kind, 33)
+    rng = np.random.default_rng(5)
+    low = borders(kind)
+    mid = rng.choice(low[low < c8.TOP[kind] / 8], (batch, heads))
+    code = c8.code(rng.uniform(0.6, 0.95, (batch, heads)) * c8.TOP[kind], kind)
+    factor = (mid / code).astype(np.float32)  # below 1 / 4, and the new factor is 1
+    product = code * factor.astype(np.float64)
+    assert (c8.code(product, kind) != c8.code((code.astype(np.float32) * factor).astype(np.float64), kind)).sum() > 20
+    rows = table[:, 0].long()
+    for c, s in ((kc, ks), (vc, vs)):
+        n = c.float()
+        n[rows, 0] = 0.0
+        n[rows, 0, :, 7] = torch.from_numpy(code).float().cuda()
+        c.view(torch.uint8).copy_(n.to(c.dtype).view(torch.uint8))
+        s[rows, 0] = torch.from_numpy(factor).cuda()
+    x = torch.zeros(batch, heads, d).half()
+    x[:, :, 0] = c8.TOP[kind]
+    appended(kc, vc, ks, vs, table, page, [1] * batch, list(range(batch + 1)), x.cuda(), -x.cuda(), kind)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_append_of_prompts_behind_any_factors(kind):
+    old, new, d, page, block = [5, 0, 70, 130], [90, 33, 1, 200], 96, 128, 32
+    kc, vc, ks, vs, table = make_cache8(330, 4, 3, d, page, block, kind, 34)
+    g = torch.Generator().manual_seed(6)
+    for s in (ks, vs):
+        s.mul_((1.0 + torch.rand(s.shape, generator=g)).cuda())
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    k, v = torch.randn(2, cu[-1], 3, d, generator=g).half().cuda()
+    v *= 20.0
+    appended(kc, vc, ks, vs, table, page, old, cu, k, v, kind)
