@@ -587,6 +587,7 @@ __global__ void __launch_bounds__(kThreads) load8_kernel(Load8Params p, FastDiv 
     for (int i0 = lane; i0 < chunks; i0 += 32 * kLoads) {
       uint2 codes[kLoads][2];
       float s[kLoads][2];
+      bool twice = false;  // a factor is no power of two: fp32 may round its products, and the type once more
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const int i = i0 + 32 * k, head = static_cast<int>(per_row.div(i)), c = i - head * static_cast<int>(per_row.d);
@@ -610,8 +611,23 @@ __global__ void __launch_bounds__(kThreads) load8_kernel(Load8Params p, FastDiv 
           *reinterpret_cast<uint4*>(to[kind] + head * (kind ? p.v.sh : p.k.sh) + c * 8) =
               make_uint4(Pack<T>::two(x.x * f, x.y * f), Pack<T>::two(x.z * f, x.w * f), Pack<T>::two(y.x * f, y.y * f),
                          Pack<T>::two(y.z * f, y.w * f));
+          twice = twice || (__float_as_uint(f) & 0x7fffffu) != 0;
         }
       }
+      // (done again here: in place it takes registers, 64 -> 70, and time of all factors, 46.1 -> 46.9 us for 41800 tokens)
+      if (!twice) continue;
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind)
+#pragma unroll 1
+        for (int i = i0; i < min(chunks, i0 + 32 * kLoads); i += 32) {
+          const int head = static_cast<int>(per_row.div(i)), c = i - head * static_cast<int>(per_row.d);
+          const uint2 z = *reinterpret_cast<const uint2*>(rows[kind] + head * (kind ? p.cache.pages.v.sh : p.cache.pages.k.sh) + c * 8);
+          const float f = scales[kind][head * (kind ? p.cache.vs[2] : p.cache.ks[2])];
+          const float4 x = value4<INT8>(z.x), y = value4<INT8>(z.y);
+          *reinterpret_cast<uint4*>(to[kind] + head * (kind ? p.v.sh : p.k.sh) + c * 8) =
+              make_uint4(Pack<T>::two(times(x.x, f), times(x.y, f)), Pack<T>::two(times(x.z, f), times(x.w, f)),
+                         Pack<T>::two(times(y.x, f), times(y.y, f)), Pack<T>::two(times(y.z, f), times(y.w, f)));
+        }
     }
   }
 }

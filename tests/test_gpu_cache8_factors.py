@@ -127,3 +127,41 @@ def test_append_of_prompts_behind_any_factors(kind):
     k, v = torch.randn(2, cu[-1], 3, d, generator=g).half().cuda()
     v *= 20.0
     appended(kc, vc, ks, vs, table, page, old, cu, k, v, kind)
+
+
+def rounded(x, dt):
+    """x (64 bits) rounded once to `dt`, ties to even; within the type's normal range."""
+    bits = 11 if dt == "fp16" else 8
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 2.0 ** bits), e - bits)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("heads,d", [(8, 128), (1, 16)])
+def test_load_rounds_once_behind_any_factor(kind, dt, heads, d):
+    """code * factor next to the middle of two numbers of the type, which its rounding to fp32 makes a tie."""
+    pages, page = 64, 32
+    kc, vc, ks, vs, table = make_cache8(pages * page, 1, heads, d, page, 1, kind, 35, spare=0)
+    rng = np.random.default_rng(7)
+    bits = 11 if dt == "fp16" else 8
+    # a factor for each slot and head, and codes of which one in it makes such a product
+    code = c8.code(rng.uniform(0.6, 0.95, (pages, page, heads)) * c8.TOP[kind], kind)
+    mid = (2.0 ** bits / 2 + rng.integers(0, 2 ** (bits - 1), code.shape) + 0.5) / 2.0 ** bits
+    factor = (mid / code).astype(np.float32)
+    once = rounded(code * factor.astype(np.float64), dt)
+    twice = rounded((code.astype(np.float32) * factor).astype(np.float64), dt)
+    assert (once != twice).sum() > 50
+    for c, s in ((kc, ks), (vc, vs)):
+        n = c.float()
+        n[..., 3] = torch.from_numpy(code).float().cuda()
+        c.view(torch.uint8).copy_(n.to(c.dtype).view(torch.uint8))
+        s.copy_(torch.from_numpy(factor).cuda())
+    got = ab.attn_cache_load8(kc, vc, ks, vs, table, ints([0]), ints([0, pages * page]), pages * page, dtype=DT[dt])
+    ab.check_device_status()
+    rows = table[0].long().cpu().numpy()
+    for x, c in zip(got, (kc, vc)):
+        want = rounded(numbers(c) * factor.astype(np.float64)[..., None], dt)[rows].reshape(-1, heads, d)
+        small = np.abs(want) < 2.0 ** -14  # fp16's steps below: rounded at 2^-24
+        assert np.array_equal(f64(x)[~small], want[~small])
+        assert (np.abs(f64(x) - want)[small] <= 2.0 ** -24).all()
