@@ -196,8 +196,9 @@ cudaError_t launch_evict(const EvictParams& p, int dtype, cudaStream_t stream);
 // Geometry of a decode with tiles of 1 << tile_log2 keys: how the groups are cut into head
 // tiles, the lines, their runs (0: no keys) and whether segments are taken whole.
 cudaError_t shape_decode(DecodeParams& p, int tile_log2, int blocks_per_sm, int* runs);
-// Joins the partials that a decode's `runs` blocks left (not after whole segments).
-cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, cudaStream_t stream);
+// Joins the partials that a decode's `runs` blocks left (not after whole segments).  far: values
+// may differ by more than fp32's exponents hold beside their weights.
+cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, bool far, cudaStream_t stream);
 
 // ---- checks of arguments (cache_api.cu)
 

@@ -639,7 +639,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 // there are more segments than blocks of the first kernel (`blocks`), its segment is the
 // one that starts in the run of such a block and is cut at its end, if there is one; else
 // (by_segment) it is counted off.
-template <typename T>
+//
+// FAR: partials whose values are 2^+-60 apart beside their weights (V's factors).  Where a weight is
+// below fp32's normal range its values may still count: they are scaled by its root twice, which w
+// holds below 0 for them.
+template <typename T, bool FAR>
 __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks, int by_segment, int rows_per,
                                                      int dp) {
   __shared__ int s_sums[kJoin / 32];
@@ -734,8 +738,9 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks,
     for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float base = top == -INFINITY ? 0.f : top;
     for (int i = lane; i < nc; i += 32) {
-      w[i] = ex2(w[i] - base);
-      sum += w[i] * (i == lane ? sums : part(i)[part_m + kMaxRows + row]);
+      const float d = w[i] - base, f = ex2(d);
+      w[i] = FAR && d < -126.f ? -ex2(0.5f * d) : f;
+      sum += f * (i == lane ? sums : part(i)[part_m + kMaxRows + row]);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -748,7 +753,11 @@ __global__ void __launch_bounds__(kJoin) join_kernel(DecodeParams p, int blocks,
 #pragma unroll
           for (int k = 0; k < kAhead; ++k)
             if (i0 + k * shares < nc) {
-              const float f = w[i0 + k * shares];
+              float f = w[i0 + k * shares];
+              if (FAR && f < 0.f) {
+                f = -f;
+                x[c][k] = make_float4(x[c][k].x * f, x[c][k].y * f, x[c][k].z * f, x[c][k].w * f);
+              }
               acc[c].x += f * x[c][k].x;
               acc[c].y += f * x[c][k].y;
               acc[c].z += f * x[c][k].z;
@@ -887,7 +896,7 @@ cudaError_t launch_t(DecodeParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (p.whole) return cudaSuccess;
-  e = launch_join(p, Pack<T>::kIsBf16 ? ATTN_BF16 : ATTN_FP16, r, stream);
+  e = launch_join(p, Pack<T>::kIsBf16 ? ATTN_BF16 : ATTN_FP16, r, false, stream);
   if (e != cudaSuccess || p.w_in == nullptr || p.max_seqlen == 0) return e;
   // 16 blocks fit an SM
   const int64_t bg = static_cast<int64_t>(p.batch) * p.h_k, fit = (16 * static_cast<int64_t>(num_sms()) + bg - 1) / bg;
@@ -935,7 +944,7 @@ cudaError_t shape_decode(DecodeParams& p, int tile_log2, int blocks_per_sm, int*
   return cudaSuccess;
 }
 
-cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, cudaStream_t stream) {
+cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, bool far, cudaStream_t stream) {
   cudaLaunchAttribute early;  // starts while the kernel before it drains, and waits for it
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -951,8 +960,9 @@ cudaError_t launch_join(const DecodeParams& p, int dtype, int runs, cudaStream_t
   cfg.attrs = &early;
   cfg.numAttrs = runs > 0 ? 1 : 0;
   const int dp = pad_dim(p.head_dim);
-  return dtype == ATTN_BF16 ? cudaLaunchKernelEx(&cfg, join_kernel<__nv_bfloat16>, p, runs, by_segment, rows_per, dp)
-                            : cudaLaunchKernelEx(&cfg, join_kernel<__half>, p, runs, by_segment, rows_per, dp);
+  auto* kernel = dtype == ATTN_BF16 ? (far ? join_kernel<__nv_bfloat16, true> : join_kernel<__nv_bfloat16, false>)
+                                    : (far ? join_kernel<__half, true> : join_kernel<__half, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, p, runs, by_segment, rows_per, dp);
 }
 
 DecodeWs decode_ws(int batch, int h_q, int h_k, int head_dim, int max_seqlen, bool weights) {

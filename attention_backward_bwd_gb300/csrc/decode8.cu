@@ -35,7 +35,8 @@
 // fp16 numbers, its rounded value and the rounded remainder, times 2^14, so that it is right to
 // 2^-22 of itself or 2^-38 of the largest.  V's factors are kept within 2^+-60, so that the
 // 2^(s - M) of the sum, up to 2^60, have room in fp32; where M steps by more than fp32's exponents
-// they are scaled in halves, and partials leave with a sum in [1, 2).  All sums are fp32.
+// they are scaled in halves, and partials leave with a sum in [1, 2).  Their maximum is that of the
+// sum alone, so the join scales a far partial's O in halves, too.  All sums are fp32.
 #include <atomic>
 
 #include "decode.cuh"
@@ -659,7 +660,7 @@ cudaError_t launch_main(Decode8Params p, cudaStream_t stream) {
     decode8_kernel<DP, HN, INT8><<<runs, kThreads, C::kSmem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return p.whole ? cudaSuccess : launch_join(p, p.bf16 ? ATTN_BF16 : ATTN_FP16, runs, stream);
+  return p.whole ? cudaSuccess : launch_join(p, p.bf16 ? ATTN_BF16 : ATTN_FP16, runs, true, stream);
 }
 
 template <int DP>

@@ -165,3 +165,52 @@ def test_load_rounds_once_behind_any_factor(kind, dt, heads, d):
         small = np.abs(want) < 2.0 ** -14  # fp16's steps below: rounded at 2^-24
         assert np.array_equal(f64(x)[~small], want[~small])
         assert (np.abs(f64(x) - want)[small] <= 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("gap", [120, 128, 136, 144])
+@pytest.mark.parametrize("n,group", [(4096, 2), (30000, 1), (700, 16)])
+def test_decode_of_improbable_keys_whose_values_are_large(kind, gap, n, group):
+    """Most keys are 2^-gap times as probable as one of them and have values up to 2^120 times as large,
+    in other blocks' parts of the sequence: they make up O where the gap is small enough, and are as
+    good as nothing beside it where it is not."""
+    d = 64
+    kc, vc, ks, vs, table = make_cache8(n, 1, 1, d, 16, 16, kind, 36, exps=(0, 0))
+    for c in (kc, vc):
+        c.view(torch.uint8).zero_()
+    rows = table[0].long()
+    vs.fill_(2.0 ** 60)
+    vs[rows[(n - 1) // 16]] = 2.0 ** -60
+    at = (rows[torch.arange(n) // 16], torch.arange(n) % 16)
+    k, v = kc.float(), vc.float()
+    # base-2 logits are sums of two codes; the last block's keys but one take no part
+    k[at[0], at[1], 0, 0] = -104.0
+    k[at[0], at[1], 0, 1] = 104.0 - gap
+    last = torch.arange((n - 1) // 16 * 16, n)
+    k[at[0][last], at[1][last], 0, 0] = -112.0
+    k[at[0][last], at[1][last], 0, 1] = -112.0
+    k[at[0][n - 1], at[1][n - 1], 0, :2] = 0.0
+    g = torch.Generator().manual_seed(8)
+    v[at[0], at[1], 0] = torch.randint(1, 9, (n, d), generator=g).float().cuda()
+    for c, x in ((kc, k), (vc, v)):
+        c.view(torch.uint8).copy_(x.to(c.dtype).view(torch.uint8))
+    q = torch.zeros(1, group, d, dtype=torch.bfloat16, device="cuda")
+    q[..., :2] = 1.0
+    scale = float(np.log(2.0))
+    o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints([n]), scale=scale)
+    ab.check_device_status()
+    check_decode8(o, lse, q, kc, vc, ks, vs, table, [n], scale)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_decode_behind_factors_that_are_no_powers_of_two(kind):
+    lens, d = [900, 0, 77, 3000], 128
+    kc, vc, ks, vs, table = make_cache8(3000, 4, 2, d, 48, 12, kind, 37)
+    g = torch.Generator().manual_seed(9)
+    for s in (ks, vs):
+        s.mul_((1.0 + torch.rand(s.shape, generator=g)).cuda())
+    for dt, group in (("fp16", 4), ("bf16", 12)):
+        q = torch.randn(4, 2 * group, d, generator=g).to(DT[dt]).cuda()
+        o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, ints(lens))
+        ab.check_device_status()
+        check_decode8(o, lse, q, kc, vc, ks, vs, table, lens, d ** -0.5)
