@@ -28,8 +28,8 @@
 // from 285 us: 32 keys looked up at once, the maximum compared by vote and moved only where it
 // grows, weights without a second exponent, O added up in one round (in eight it cost 3 us a segment).
 //
-// Numbers.  q enters as fp16: bf16 rows are divided by the power of two of their largest element,
-// which is exact down to 2^-17 of it and off by 2^-25 of it below.  The weight of a code in O is
+// Numbers.  q enters as fp16: bf16 rows are scaled by a power of two, their largest element to
+// [2^15, 2^16), which is exact down to 2^-32 of it and off by 2^-40 of it below.  The weight of a code in O is
 // p_j vs_j, and the running maximum M is that of s_j log2(e) + floor(log2 vs_j), so that the weight
 // 2^(s - M) vs stays below 2 whatever the factors of the blocks are.  It enters the product as two
 // fp16 numbers, its rounded value and the rounded remainder, times 2^14, so that it is right to
@@ -399,10 +399,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
                              max((x.y & 0x7fffu) << 16, x.y & 0x7fff0000u)));
         }
         float mul = 1.f;
-        if (p.bf16) {  // divided by the power of two of the row's largest element
+        if (p.bf16) {  // the row's largest element to [2^15, 2^16): of bf16 at most 65280, which fp16 holds
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = min(max(static_cast<int>(top >> 23) - 127, -126), 126);
+          const int e = max(static_cast<int>(top >> 23) - 127 - 15, -126);
           const float down = __int_as_float((127 - e) << 23);
           mul = __int_as_float((127 + e) << 23);
 #pragma unroll
