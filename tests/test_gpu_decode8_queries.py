@@ -37,7 +37,9 @@ def test_decode_of_one_large_element_that_no_key_meets(kind, exp, group):
     ref = co.decode(f64(q[0]), k, v, scale)
     most = np.repeat(np.abs(k).sum(2).max(0), group)
     logit = (d + 4) * 2.0 ** -22 * ref["mag"] + 2.0 ** -20 + 2.0 ** -40 * scale * np.abs(f64(q[0])).max(1) * most
-    assert logit.max() < 2.0 ** -9  # the bound tells something
+    # (q's part is at most 2^-40 x 1.5 x 2^24 x 0.25 sum |k|, of sums near 500 0.003: beside logits that lost
+    # elements of size 1 it tells)
+    assert logit.max() < 2.0 ** -7
     steps = (n / 64 + 16) * 2.0 ** -23
     half = HALF_STEP[q.dtype]
     bound = half * np.abs(ref["o"]) + ref["absv"] * (2 * logit + 2.0 ** -19 + steps + 2.0 ** -22)[:, None] * (1 + half) + \
