@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, HN>::kBlocks) decode8_kernel
 #pragma unroll
           for (int n = 0; n < HN; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              y[gr][n][i * 2 + c] = (s[n][0][i * 2 + c] + s[n][1][i * 2 + c]) * (f.x * qscale[n][c]);
+            for (int c = 0; c < 2; ++c)  // (ks times q's scale may be beyond fp32, beside a sum of 0)
+              y[gr][n][i * 2 + c] = (s[n][0][i * 2 + c] + s[n][1][i * 2 + c]) * f.x * qscale[n][c];
         }
       }
       if (p.softcap > 0.f) {

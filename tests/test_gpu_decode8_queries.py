@@ -46,3 +46,24 @@ def test_decode_of_one_large_element_that_no_key_meets(kind, exp, group):
         2 * SMALLEST[q.dtype]
     assert (np.abs(f64(lse[0]) - ref["lse"]) <= logit + 2.0 ** -20 + steps + np.abs(ref["lse"]) * 2.0 ** -22).all()
     assert (np.abs(f64(o[0]) - ref["o"]) <= bound).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_decode_of_large_queries_over_large_factors_of_zeros(kind, softcap):
+    # q's size times the factor is beyond fp32, but the codes that it meets are 0: all keys are alike
+    n, d = 300, 64
+    kc, vc, ks, vs, table = make_cache8(n, 1, 1, d, 16, 16, kind, 52)
+    codes = kc.float()
+    codes[..., 5] = 0.0
+    kc.view(torch.uint8).copy_(codes.to(kc.dtype).view(torch.uint8))
+    ks.fill_(2.0 ** 60)
+    q = torch.zeros(1, 2, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = 2.0 ** 100
+    o, lse = ab.attn_decode8(q, kc, vc, ks, vs, table, torch.tensor([n], dtype=torch.int32, device="cuda"), softcap=softcap)
+    ab.check_device_status()
+    v = slots_of(vc, vs, table, 0, range(n))
+    want, half = v.mean(0), HALF_STEP[q.dtype]
+    bound = half * np.abs(want) + np.abs(v).mean(0) * 2.0 ** -17  # exponentials 2^-20, sums of 300 keys 21 steps of 2^-23
+    assert (np.abs(f64(o[0]) - want) <= bound).all()
+    assert np.abs(f64(lse[0]) - np.log(n)).max() <= 2.0 ** -17
