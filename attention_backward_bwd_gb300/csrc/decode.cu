@@ -127,7 +127,7 @@ __host__ __device__ constexpr int perm(int row) {
 // memory, so a read behind it in program order waits until it has been issued.
 template <int DP>
 __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t* valid, uint32_t dst,
-                                          int idx, const DecodeParams& p, uint64_t policy) {
+                                          int idx, const DecodeParams& p) {
   constexpr int kLanes = DP == 64 ? 8 : (DP <= 128 ? 16 : 32), kStep = kCopy / kLanes;
   constexpr int kTile = Cfg<DP, false>::kTile, kIter = kTile / kStep, kPitch = Cfg<DP, false>::kPitch;
   const int c = idx % kLanes, r0 = idx / kLanes;
@@ -147,8 +147,8 @@ __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t*
       for (int i = 0; i < 8; ++i) a[i] = rows[(i0 + i) * kStep];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        cp_async16(at(i0 + i), a[i].x + c * 16, policy);
-        cp_async16(at(i0 + i) + kTile * kPitch, a[i].y + c * 16, policy);
+        cp_async16(at(i0 + i), a[i].x + c * 16);
+        cp_async16(at(i0 + i) + kTile * kPitch, a[i].y + c * 16);
       }
     }
   } else {
@@ -158,8 +158,8 @@ __device__ __forceinline__ void copy_rows(const longlong2* rows, const uint32_t*
       const bool ok = a.x != 0;
       const long long k = ok ? a.x + c * 16 : reinterpret_cast<long long>(p.cache.k.ptr);
       const long long v = ok ? a.y + c * 16 : reinterpret_cast<long long>(p.cache.v.ptr);
-      cp_async16_or_zero(at(i), k, ok, policy);
-      cp_async16_or_zero(at(i) + kTile * kPitch, v, ok, policy);
+      cp_async16_or_zero(at(i), k, ok);
+      cp_async16_or_zero(at(i) + kTile * kPitch, v, ok);
     }
   }
 }
@@ -329,9 +329,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
       load_head();
     };
-    // Keys and values are read once, unless a group has several head tiles: they leave the
-    // L2 first, so that logits and partials stay for the second kernel.
-    const uint64_t policy = p.head_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     auto store_plan = [&](int tile) {
       TileDesc& d = desc[tile % kSlots];
 #pragma unroll
@@ -357,8 +354,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     auto fetch = [&](int tile) {  // issues the copies of one tile, if there is one
       const TileDesc& d = desc[tile % kSlots];
       if (!(d.flags & kNone))
-        copy_rows<DP>(rows + (tile & 1) * kTile, d.valid, ring_u + (tile % S) * C::kStageBytes, key, p,
-                             policy);
+        copy_rows<DP>(rows + (tile & 1) * kTile, d.valid, ring_u + (tile % S) * C::kStageBytes, key, p);
       cp_commit();
     };
     // the first copies leave as soon as their rows are known

@@ -78,24 +78,17 @@ __device__ __forceinline__ int scan_tiles(const DecodeParams& p, bool tell, int*
   return before + x - mine;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, long long src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "l"(policy)
-               : "memory");
+// (Without an L2 cache policy: three variants of these kernels whose copies had one, all gone, ended
+// with an illegal instruction.  What caused it was not found.)
+__device__ __forceinline__ void cp_async16(uint32_t dst, long long src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 16 bytes, or 16 zeros.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0), "l"(policy)
-               : "memory");
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

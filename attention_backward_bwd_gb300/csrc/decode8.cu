@@ -90,15 +90,6 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int k) {
   return (row ^ ((k & kMask) << 4)) + (k & ~(kMask | 1)) * 16;
 }
 
-// (Without a cache policy: with a uniform warp index the compiler keeps the policy in a uniform
-// register, and such a copy ends as an illegal instruction.)
-__device__ __forceinline__ void cp_async16(uint32_t dst, long long src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes, or 16 zeros.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, long long src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const float* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
