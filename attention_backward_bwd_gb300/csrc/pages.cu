@@ -5,12 +5,13 @@
 // references that go and come and what each row needs; prefix sums over the rows and the number of
 // free pages in each block's part of the pool; the list of the lowest free pages; the new rows.
 // Who goes on with which row is worked out by every block for itself, in shared memory.  Which page
-// a row gets follows from its place alone, so that the result does not depend on timing.  A warp
-// takes kChunk entries of a row.  Small tables and pools are one launch of one cluster, whose
-// barrier parts the steps: bound by their chain, each some loads long.  Large ones (kLarge) take a
-// launch a step, with all of the GPU for the references and the rows: a reference is an atomic
-// operation, of which an SM issues one a cycle or so (512 rows of 1025 pages: 84 us in one cluster,
-// 23 in launches, of which the host's part is 11).
+// a row gets follows from its place alone, so that the result does not depend on timing.  A row that
+// goes on and would write a page that others hold too (the settled references say so) gives up its
+// pages from there on; they lose their references in the last step, after the free pages were listed,
+// since the copies still read them.  A warp takes kChunk entries of a row.  Small tables and pools are
+// one launch of one cluster, whose barrier parts the steps: bound by their chain, each some loads long.
+// Large ones (kLarge) take a launch a step, with all of the GPU for the references and the rows (512
+// rows of 1025 pages: 84 us in one cluster, 23 in launches).
 // attn_cache_copy moves whole pages, 16 bytes a thread, several in flight: bound by the memory.
 #include <atomic>
 
@@ -46,13 +47,15 @@ __device__ __forceinline__ uint32_t cluster_blocks() {
   return r;
 }
 
-// Workspace of a fork: per row the pages and copies it needs and their prefix sums (beyond kRows
-// rows also the first row that takes it over, its parent and its length); per block its free
-// pages; the pages needed and those granted; then the list of free pages and,
+// Workspace of a fork: per row the pages and copies it needs, their prefix sums (the pages' below 0
+// where the row gives pages up) and what it holds of pages that it would write (kNoneHeld, one page's
+// number, kSomeHeld); beyond kRows rows also the first row that takes it over, its parent and its
+// length; per block its free pages; the pages needed and those granted; then the list of free pages and,
 // where the table is its own output, the old table.
 struct ForkWs {
-  int *fresh, *copied, *who, *parent, *len, *fresh_before, *copied_before, *free_of, *sums, *list, *old;
+  int *fresh, *copied, *who, *parent, *len, *fresh_before, *copied_before, *held, *free_of, *sums, *list, *old;
 };
+enum { kNoneHeld = -1, kSomeHeld = -2 };
 __host__ __device__ inline ForkWs fork_layout(int* ws, int64_t rows, int64_t list) {
   ForkWs w;
   w.fresh = ws;
@@ -62,7 +65,8 @@ __host__ __device__ inline ForkWs fork_layout(int* ws, int64_t rows, int64_t lis
   w.len = w.parent + rows;
   w.fresh_before = w.len + rows;
   w.copied_before = w.fresh_before + rows;
-  w.free_of = w.copied_before + rows;
+  w.held = w.copied_before + rows;
+  w.free_of = w.held + rows;
   w.sums = w.free_of + kCluster;
   w.list = w.sums + 8;
   w.old = w.list + list;
@@ -97,6 +101,7 @@ struct Row {
   int parent, n;      // -1: none; its length
   int full, used, need;  // entries of full pages, of pages with slots, with the room
   bool heir;          // goes on with its parent's pages
+  bool gives;         // but not with those from `full` on, which others hold
 };
 
 template <int STEPS>
@@ -164,11 +169,11 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
     else __syncthreads();
   }
 
-  auto row_of = [&](int b, bool tell) {
+  auto shape_of = [&](int b, int parent, int n, bool tell) {
     Row r;
-    r.parent = w.parent[b];
-    r.n = r.parent < 0 ? 0 : w.len[r.parent];
-    r.heir = r.parent >= 0 && w.who[r.parent] == b;
+    r.parent = parent;
+    r.n = n;
+    r.heir = r.gives = false;
     r.full = r.n / p.page_size;
     r.used = r.full + (r.n % p.page_size != 0 ? 1 : 0);
     const int room = r.parent < 0 ? 0 : (p.room == nullptr ? p.room_all : p.room[b]);
@@ -180,6 +185,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
     r.need = static_cast<int>((slots + p.page_size - 1) / p.page_size);
     return r;
   };
+  auto row_of = [&](int b, bool tell) {
+    const int parent = w.parent[b];
+    Row r = shape_of(b, parent, parent < 0 ? 0 : w.len[parent], tell);
+    r.heir = parent >= 0 && w.who[parent] == b;
+    return r;
+  };
   // Entry i of a row: its page, whether that is the parent's shared one, one to be copied, missing.
   struct Entry {
     int page;
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
   auto entry_of = [&](const Row& r, int page, int i) {
     Entry e{-1, false, false, false, false};
     if (r.parent < 0 || i >= p.max_pages) return e;
-    if (r.heir) {
+    if (r.heir && (!r.gives || i < r.full)) {
       e.page = valid(page) ? page : -1;
       e.fresh = e.page < 0 && i >= r.used && i < r.need;
     } else if (i < r.used) {
@@ -201,8 +212,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
     }
     return e;
   };
-  // Where a row's missing entries start (and end: at max(used, need)).
-  auto lack_from = [&](const Row& r) { return r.heir ? r.used : (p.share ? r.full : 0); };
+  // Where a row's missing entries start (and end: at max(used, need)), and those that it may give up.
+  auto lack_from = [&](const Row& r) { return r.heir || p.share ? r.full : 0; };
   // Entries i0 + 32 k + lane below `end`, as they are.
   auto load = [&](const int* row, int i0, int end, int (&page)[kEntries]) {
 #pragma unroll
@@ -211,9 +222,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
       page[k] = i < end ? __ldcg(row + i) : -1;
     }
   };
-  // Missing entries and copies of [from, end), by a warp.
-  auto count = [&](const Row& r, const int* old, int from, int end, int& fresh, int& copied) {
+  // Missing entries and copies of [from, end), by a warp; of an heir also what it holds there.
+  auto count = [&](const Row& r, const int* old, int from, int end, int& fresh, int& copied, int& held) {
     fresh = copied = 0;
+    int pages = 0, most = kNoneHeld;
     for (int i0 = from; i0 < end; i0 += kChunk) {
       int page[kEntries];
       load(old, i0, end, page);
@@ -223,10 +235,13 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
           const Entry e = entry_of(r, page[k], i0 + 32 * k + lane);
           fresh += e.fresh;
           copied += e.copied;
+          pages += e.page >= 0;
+          most = max(most, e.page);
         }
     }
     fresh = __reduce_add_sync(0xffffffffu, fresh);
     copied = __reduce_add_sync(0xffffffffu, copied);
+    held = __reduce_add_sync(0xffffffffu, pages) > 1 ? static_cast<int>(kSomeHeld) : __reduce_max_sync(0xffffffffu, most);
   };
   const int chunks = (p.max_pages + kChunk - 1) / kChunk;
   const int64_t items = static_cast<int64_t>(p.rows) * chunks;
@@ -259,11 +274,12 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
           }
         }
       if (i0 == 0) {
-        int fresh, copied;
-        count(r, old, lack_from(r), max(r.used, r.need), fresh, copied);
+        int fresh, copied, held;
+        count(r, old, lack_from(r), max(r.used, r.need), fresh, copied, held);
         if (lane == 0) {
           w.fresh[b] = fresh;
           w.copied[b] = copied;
+          w.held[b] = r.heir ? held : static_cast<int>(kNoneHeld);
           // pages of slots that cannot be copied: what is neither copied nor the room's
           if (r.parent >= 0 && !r.heir && copied < r.used - lack_from(r)) report(p.status, kBadPage);
         }
@@ -277,6 +293,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
     // ---- free pages of each block's part; prefix sums over the rows
     const int page0 = static_cast<int>(static_cast<int64_t>(p.num_pages) * rank / blocks);
     const int page1 = static_cast<int>(static_cast<int64_t>(p.num_pages) * (rank + 1) / blocks);
+    const bool here = STEPS == kAllSteps && few;  // the prefix sums are each block's own
+    int fresh = 0, copied = 0, held = kNoneHeld;
+    auto ask = [&](int b) {
+      fresh = b < p.rows ? __ldcg(w.fresh + b) : 0;
+      copied = b < p.rows ? __ldcg(w.copied + b) : 0;
+      held = b < p.rows ? __ldcg(w.held + b) : static_cast<int>(kNoneHeld);
+    };
+    if (here || rank == 0) ask(tid);  // (on their way while the counts are read)
     int free_here = 0;
     for (int i0 = page0 + tid; i0 < page1; i0 += kForkThreads * kEntries) {
       int x[kEntries];
@@ -286,13 +310,27 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
       for (int k = 0; k < kEntries; ++k) free_here += x[k] == 0;
     }
     int total, wanted = 0, copied0 = 0;
-    const bool here = STEPS == kAllSteps && few;  // the prefix sums are each block's own
     if (here || rank == 0) {
       for (int r0 = 0; r0 < p.rows; r0 += kForkThreads) {
         const int b = r0 + tid;
-        const int fresh = b < p.rows ? __ldcg(w.fresh + b) : 0, copied = b < p.rows ? __ldcg(w.copied + b) : 0;
+        if (r0 > 0) ask(b);
+        bool gives = held >= 0 && __ldcg(p.refs_out + held) > 1;
+        if (held != kNoneHeld && (gives || held == kSomeHeld)) {
+          int s = p.parents == nullptr ? b : p.parents[b];
+          s = s >= p.rows ? b : s;
+          const Row r = shape_of(b, s, STEPS == kAllSteps ? w.len[s] : __ldcg(saved_len + s), false);
+          const int* old = p.table + s * p.table_stride;
+          for (int i = r.full; i < max(r.used, r.need) && !gives; ++i) {
+            const int page = __ldcg(old + i);
+            gives = valid(page) && __ldcg(p.refs_out + page) > 1;
+          }
+          if (gives) {  // its partly full page is copied, the room's are new
+            copied = r.used > r.full && valid(__ldcg(old + r.full)) ? 1 : 0;
+            fresh = copied + max(r.need - r.used, 0);
+          }
+        }
         const int f = block_prefix(fresh, s_sums, total);
-        if (b < p.rows) w.fresh_before[b] = wanted + f;
+        if (b < p.rows) w.fresh_before[b] = gives ? ~(wanted + f) : wanted + f;
         wanted += total;
         const int c = block_prefix(copied, s_sums, total);
         if (b < p.rows) w.copied_before[b] = copied0 + c;
@@ -344,16 +382,17 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
     const bool run_out = __ldcg(w.sums + 2) < __ldcg(w.sums + 1);
     for (int64_t item = at >> 5; item < items; item += step >> 5) {
       const int b = static_cast<int>(item / chunks), i0 = static_cast<int>(item - static_cast<int64_t>(b) * chunks) * kChunk;
-      const Row r = row_of(b, false);
+      Row r = row_of(b, false);
+      r.gives = w.fresh_before[b] < 0;
       const int from = r.parent < 0 ? b : r.parent;
       const int* old = in_place ? w.old + static_cast<int64_t>(from) * p.max_pages : p.table + from * p.table_stride;
       int* out = p.table_out + b * p.out_stride;
       int page[kEntries];
       load(old, i0, r.heir ? p.max_pages : r.used, page);  // entries that the parent has a say in
-      int fresh0 = w.fresh_before[b], copied0 = w.copied_before[b], made = 0;
+      int fresh0 = r.gives ? ~w.fresh_before[b] : w.fresh_before[b], copied0 = w.copied_before[b], made = 0, freed = 0;
       if (i0 > lack_from(r) && i0 < max(r.used, r.need)) {
-        int fresh, copied;
-        count(r, old, lack_from(r), i0, fresh, copied);
+        int fresh, copied, held;
+        count(r, old, lack_from(r), i0, fresh, copied, held);
         fresh0 += fresh;
         copied0 += copied;
       }
@@ -381,12 +420,17 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkParams p, ForkWs
           fresh0 += __popc(fresh);
           copied0 += __popc(copied);
         }
-        if (i < p.max_pages) out[i] = now;
+        if (i < p.max_pages) {
+          out[i] = now;
+          if (r.gives && i >= r.full && valid(page[k])) freed += atomicSub(p.refs_out + page[k], 1) == 1;
+        }
       }
       made = __reduce_add_sync(0xffffffffu, made);
+      if (r.gives) freed = __reduce_add_sync(0xffffffffu, freed);
       if (lane == 0) {
         if (i0 == 0) p.seqlens_out[b] = r.n;
         if (run_out && made > 0) atomicAdd(p.counts, made);
+        if (freed > 0) atomicAdd(p.counts + 1, freed);
       }
     }
   }
@@ -460,7 +504,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p, FastDi
 size_t fork_ws(int rows, int max_pages, int num_pages) {
   const int64_t entries = static_cast<int64_t>(rows) * max_pages;
   const int64_t list = entries < num_pages ? entries : num_pages;
-  return align256((7 * static_cast<int64_t>(rows) + kCluster + 8 + list + entries) * sizeof(int));
+  return align256((8 * static_cast<int64_t>(rows) + kCluster + 8 + list + entries) * sizeof(int));
 }
 
 namespace {

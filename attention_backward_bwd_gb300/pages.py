@@ -29,7 +29,9 @@ def attn_cache_fork(block_table, seqlens, refs, page_size: int, parents=None, ro
     none, the row is freed).  The first row of a parent goes on with its pages; the others share the
     full ones and get a fresh page for the rest (``share=False``: for all), listed in ``copies``
     (int32 [B, 2], or [B * pages a sequence, 2] without sharing: source, fresh page).  Then every
-    row gets fresh pages for ``room`` more slots (an int, or int32 [B]).  Fresh pages are the lowest
+    row gets fresh pages for ``room`` more slots (an int, or int32 [B]).  A row that goes on gets
+    copies and fresh pages as well in place of pages that it would write and others hold: after
+    ``seqlens`` was lowered (rejected tokens) call this before the next append.  Fresh pages are the lowest
     unreferenced ones; ``counts`` (int32 [2]): the copies listed, the pages still free.  Run
     ``attn_cache_copy(..., copies, counts)`` for every cache of the table before the next append.
     """

@@ -81,16 +81,22 @@ int attn_decode8(const attn_tensor* q, const attn_tensor* o, float* lse, int dty
  * none.  Row b of the new table is made from row parents[b] of the old one (parents NULL: b
  * itself), of length n = seqlens[parents[b]]; a negative parent frees the row (all entries -1,
  * length 0).
- *   - The first row (lowest b) of a parent goes on with all its pages, also those beyond n.
+ *   - The first row (lowest b) of a parent goes on with all its pages, also those beyond n.  If, once
+ *     all rows have let go and shared, others hold one of those that it is to write (the partly full
+ *     one, the room's; so after seqlens was lowered into a shared page), it gives up its pages from
+ *     there on (references - 1): the partly full one is copied to a fresh page, the room's are fresh.
+ *     Pages given up are not among the fresh ones of the same call.
  *   - Every other row shares the full pages (references + 1) and gets a fresh page for one that
  *     is partly full; with share == 0 it gets a fresh page for each.  (source, fresh page) is
  *     written to copies, in the order of rows and entries, for attn_cache_copy.
  *   - Entries of slots [n, n + room[b]) that name no page get a fresh one (room NULL: room_all).
  *     Room beyond max_pages * page_size is left out and reported.
  *   - Pages of rows that no row goes on with lose a reference.
- * Fresh pages are the lowest ones without references after that, in the order of rows and entries;
- * where they run out, entries become -1, are not copied, and are reported.  counts[0] becomes the
- * number of copies, counts[1] that of the pages still free.  copies: pairs, room for rows of
+ * So no slot of [n, n + room), nor any of a partly full page, lies in a page that others hold as well;
+ * after seqlens was lowered a fork (parents NULL) has to run before the next append.
+ * Fresh pages are the lowest ones without references then, in the order of rows and entries; where they
+ * run out, entries become -1, are not copied, and are reported.  counts[0] becomes the
+ * number of copies, counts[1] that of the pages without references.  copies: pairs, room for rows of
  * them (share == 0: rows * max_pages); further ones are left as they were.  A parent >= rows is
  * reported and taken for b, a bad length for 0, a shared entry without a page stays without one
  * (reported).  Outputs may be the inputs themselves (the same pointer and stride), other overlaps

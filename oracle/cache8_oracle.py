@@ -76,7 +76,7 @@ def fork(table, lens, refs, page, parents, room, share=True):
     rows, width = table.shape
     refs = refs.copy()
     new = np.full_like(table, -1)
-    heir, out_len, want, made = {}, [0] * rows, [], []
+    heir, out_len, want, made, gone = {}, [0] * rows, [], [], []
     for b in range(rows):
         if parents[b] >= 0:
             heir.setdefault(int(parents[b]), b)
@@ -87,22 +87,25 @@ def fork(table, lens, refs, page, parents, room, share=True):
                     refs[e] -= 1
     for b in range(rows):
         s = int(parents[b])
+        if s >= 0 and heir[s] != b and share:
+            for e in table[s, :lens[s] // page]:
+                refs[e] += 1
+    for b in range(rows):
+        s = int(parents[b])
         if s < 0:
             continue
         n = out_len[b] = int(lens[s])
-        used, need = math.ceil(n / page), min(width, math.ceil((n + room[b]) / page))
+        full, used, need = n // page, math.ceil(n / page), min(width, math.ceil((n + room[b]) / page))
+        own = width if heir[s] == b else full if share else 0  # entries that are the parent's
+        if heir[s] == b and any(e >= 0 and refs[e] > 1 for e in table[s, full:max(used, need)]):
+            own = full  # others hold what this row would write
+            gone += [e for e in table[s, full:] if e >= 0]
         for i in range(width):
-            if heir[s] == b:
+            if i < own:
                 new[b, i] = table[s, i]
-                if i >= used and i < need and table[s, i] < 0:
-                    want.append((b, i, -1))
-            elif i < used:
-                if share and (i + 1) * page <= n:
-                    new[b, i] = table[s, i]
-                    refs[table[s, i]] += 1
-                else:
-                    want.append((b, i, table[s, i]))
-            elif i < need:
+            if i >= own and i < used:
+                want.append((b, i, table[s, i]))
+            elif i >= used and i < need and new[b, i] < 0:
                 want.append((b, i, -1))
     free = [p for p in range(len(refs)) if refs[p] == 0]
     missing = len(want) > len(free)
@@ -111,4 +114,6 @@ def fork(table, lens, refs, page, parents, room, share=True):
         refs[p] = 1
         if src >= 0:
             made.append((src, p))
+    for e in gone:  # free from the next call on
+        refs[e] -= 1
     return new, np.array(out_len), refs, made, int((refs == 0).sum()), missing
