@@ -33,6 +33,12 @@ constexpr unsigned int kNoPage = 16u;     // no free page left for a fork
 // Longest sequence of a decode or an eviction.  Their kernels count slots in 32 bits and step past
 // the last one by up to 8 * 512 slots (evict.cu: a head's threads) or a tile.
 constexpr int kMaxLength = INT32_MAX - 8191;
+// Tokens of a call on the 8-bit cache, slots of one of its blocks (a block's codes are counted in 32
+// bits, 16 of them at once), entries and pages of a fork: a grid's step (append8.cu: 8 blocks of 8 warps
+// an SM; pages.cu: 2 of 512 threads, times 8 entries) past the last stays below 2^31.
+constexpr int kMaxTokens = INT32_MAX - 65535;
+constexpr int kMaxBlock = 1 << 26;
+constexpr int kMaxEntries = INT32_MAX - (1 << 20);
 
 struct PagedArg {
   TensorArg k, v;  // sb: page, ss: slot, sh: head

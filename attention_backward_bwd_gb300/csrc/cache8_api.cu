@@ -37,6 +37,7 @@ int check_cache8(const attn_paged_kv8* c, int batch, int h_k, int head_dim, Cach
   if (rc) return rc;
   if (c->block <= 0 || c->kv.page_size % c->block != 0)
     return fail(ATTN_ERR_SHAPE, "block (%d) must be positive and divide page_size (%d)", c->block, c->kv.page_size);
+  if (c->block > kMaxBlock) return fail(ATTN_ERR_SHAPE, "block must be at most 2^26, got %d", c->block);
   out->ks[0] = c->k_scale_page;
   out->ks[1] = c->k_scale_block;
   out->ks[2] = c->k_scale_head;
@@ -80,7 +81,8 @@ int attn_cache_append8(const attn_tensor* q, const attn_tensor* oq, const attn_t
   if (rc) return rc;
   if (static_cast<int64_t>(h_q) + 2 * static_cast<int64_t>(h_k) > INT32_MAX / 2)
     return fail(ATTN_ERR_SHAPE, "h_q + 2 h_k must stay below 2^30");
-  if (tokens < 0) return fail(ATTN_ERR_SHAPE, "tokens must be >= 0, got %d", tokens);
+  if (tokens < 0 || tokens > kMaxTokens)
+    return fail(ATTN_ERR_SHAPE, "tokens must lie in [0, 2^31 - 65536], got %d", tokens);
   if (cu_seqlens == nullptr && tokens != batch)
     return fail(ATTN_ERR_ARG, "without cu_seqlens there is one token a sequence: got %d tokens, %d "
                 "sequences", tokens, batch);
@@ -123,7 +125,8 @@ int attn_cache_load8(const attn_tensor* k, const attn_tensor* v, int dtype, int 
   clear_error();
   int rc = check_heads(dtype, batch, h_k, h_k, head_dim);
   if (rc) return rc;
-  if (tokens < 0) return fail(ATTN_ERR_SHAPE, "tokens must be >= 0, got %d", tokens);
+  if (tokens < 0 || tokens > kMaxTokens)
+    return fail(ATTN_ERR_SHAPE, "tokens must lie in [0, 2^31 - 65536], got %d", tokens);
   if (static_cast<int64_t>(h_k) * head_dim > INT32_MAX) return fail(ATTN_ERR_SHAPE, "h_k * head_dim must stay below 2^31");
   Load8Params p;
   std::memset(&p, 0, sizeof(p));
@@ -201,7 +204,9 @@ int attn_decode8(const attn_tensor* q, const attn_tensor* o, float* lse, int dty
 }
 
 size_t attn_cache_fork_workspace_size(int rows, int max_pages, int num_pages) {
-  if (rows <= 0 || max_pages <= 0 || num_pages <= 0 || static_cast<int64_t>(rows) * max_pages > INT32_MAX) return 0;
+  if (rows <= 0 || max_pages <= 0 || num_pages <= 0 || static_cast<int64_t>(rows) * max_pages > kMaxEntries ||
+      num_pages > kMaxEntries)
+    return 0;
   return fork_ws(rows, max_pages, num_pages);
 }
 
@@ -217,7 +222,8 @@ int attn_cache_fork(const int* block_table, int64_t table_stride, int* table_out
   if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX)
     return fail(ATTN_ERR_SHAPE, "max_pages * page_size must stay below 2^31");
   const int64_t entries = static_cast<int64_t>(rows) * max_pages;
-  if (entries > INT32_MAX) return fail(ATTN_ERR_SHAPE, "rows * max_pages must stay below 2^31");
+  if (entries > kMaxEntries || num_pages > kMaxEntries)
+    return fail(ATTN_ERR_SHAPE, "rows * max_pages and num_pages must stay below 2^31 - 2^20");
   for (const void* ptr : {static_cast<const void*>(block_table), static_cast<const void*>(table_out),
                           static_cast<const void*>(seqlens), static_cast<const void*>(seqlens_out),
                           static_cast<const void*>(refs), static_cast<const void*>(refs_out),

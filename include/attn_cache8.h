@@ -21,7 +21,8 @@ extern "C" {
  * (page_size is a multiple of it) has a factor for each head: slot j of a page holds for head h
  * the values code * k_scale[page * k_scale_page + (j / block) * k_scale_block + h * k_scale_head],
  * and v alike.  Factors are 0 or lie in [2^-60, 2^60] (attn_decode8 takes a factor of v beyond that
- * for the nearest bound); the append makes powers of two.
+ * for the nearest bound); the append makes powers of two.  A block has at most 2^26 slots, a call
+ * at most 2^31 - 65536 tokens.
  * attn_cache_evict moves single slots between blocks and does not take such a cache.
  */
 enum { ATTN_E4M3 = 0, ATTN_INT8 = 1 };
@@ -100,9 +101,9 @@ int attn_decode8(const attn_tensor* q, const attn_tensor* o, float* lse, int dty
  * them (share == 0: rows * max_pages); further ones are left as they were.  A parent >= rows is
  * reported and taken for b, a bad length for 0, a shared entry without a page stays without one
  * (reported).  Outputs may be the inputs themselves (the same pointer and stride), other overlaps
- * are not allowed.  workspace: attn_cache_fork_workspace_size bytes, 256-byte aligned, not shared
- * by calls that may overlap.  The copies have to run (attn_cache_copy, for every cache of the
- * table) before anything is appended.
+ * are not allowed.  rows * max_pages and num_pages stay below 2^31 - 2^20.  workspace:
+ * attn_cache_fork_workspace_size bytes, 256-byte aligned, not shared by calls that may overlap.  The
+ * copies have to run (attn_cache_copy, for every cache of the table) before anything is appended.
  */
 size_t attn_cache_fork_workspace_size(int rows, int max_pages, int num_pages);
 int attn_cache_fork(const int* block_table, int64_t table_stride, int* table_out,
