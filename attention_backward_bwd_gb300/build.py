@@ -35,15 +35,33 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
+def _newer(than: str) -> bool:
+    """Whether the file is missing or older than a source."""
+    if not os.path.exists(than):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
+    t = os.path.getmtime(than)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps += [os.path.join(HERE, "..", "include", f)
              for f in os.listdir(os.path.join(HERE, "..", "include"))]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch() -> str:
+    """The torch that _native.so is bound to ("": there is none with CUDA)."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return f"{torch.__version__} {os.path.dirname(torch.__file__)} {sys.version}" if torch.version.cuda else ""
+
+
+def _built_for() -> str:
+    try:
+        with open(os.path.join(BUILD, "native.torch")) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def _native() -> None:
@@ -63,19 +81,23 @@ def _native() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for native.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, NATIVE)
+    with open(os.path.join(BUILD, "native.torch"), "w") as f:
+        f.write(_torch())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
-    """Compile and link if anything changed; returns the library path."""
-    if not force and not _stale():
-        return LIB
+    """Compile and link what changed; returns the library path.
+
+    The library is linked whatever becomes of _native.so, which a torch without CUDA cannot have."""
+    against = _torch()
+    module = against != "" and (force or _newer(NATIVE) or _built_for() != against)
+    library = force or _newer(LIB)
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_v else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-I", CSRC, "-c", src, "-o", obj]
+        cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-I", CSRC, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
@@ -84,15 +106,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        native = ex.submit(_native)
-        objs = list(ex.map(compile_one, sources()))
-        native.result()
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        native = ex.submit(_native) if module else None
+        if library:
+            objs = list(ex.map(compile_one, sources()))
+            tmp = LIB + ".tmp"
+            cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+        if native is not None:
+            native.result()
     return LIB
 
 

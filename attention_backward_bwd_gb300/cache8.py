@@ -31,7 +31,7 @@ def native():
         from .build import NATIVE
         if not os.path.exists(NATIVE):
             raise ImportError(f"{NATIVE} is missing: build it with `python -c 'import __graft_entry__ as g; "
-                              f"g.build()'`.  There is no fallback implementation.")
+                              f"g.build()'`, with a torch that has CUDA.  There is no fallback implementation.")
         from . import _native as module
         module.bind(AttnError, *(ctypes.cast(getattr(library, n), ctypes.c_void_p).value for n in _ENTRIES))
         _native = module
