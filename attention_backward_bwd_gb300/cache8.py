@@ -40,8 +40,13 @@ def native():
 
 def _on(stream, tensor):
     """(stream handle, stream) of an explicit ``stream``: what a call allocates belongs to it."""
-    side = _side(stream, tensor.device.index) if tensor.is_cuda else None
+    side = _side(stream, tensor.device.index) if isinstance(tensor, torch.Tensor) and tensor.is_cuda else None
     return (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)), side
+
+
+def _is(tensor, dims):
+    """Whether sizes can be taken from it (the call refuses what is none, as without ``stream``)."""
+    return isinstance(tensor, torch.Tensor) and tensor.dim() == dims
 
 
 def attn_cache_append8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens=None, q=None,
@@ -55,7 +60,7 @@ def attn_cache_append8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, se
     whose codes are rounded again where it grows."""
     if stream is not None:
         stream, side = _on(stream, k)
-        if q is not None and out_q is None:
+        if _is(q, 3) and out_q is None:
             out_q = _new(side, torch.empty_like, q)
     return native().append8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, cu_seqlens, q, positions,
                             inv_freq, sections, interleaved, out_q, stream)
@@ -75,9 +80,10 @@ def attn_cache_load8(k_cache, v_cache, k_scale, v_scale, block_table, starts, cu
         raise AttnError(-1, f"dtype must be float16 or bfloat16, got {dtype}")
     if stream is not None:
         stream, side = _on(stream, k_cache)
-        like = (max(0, tokens), *k_cache.shape[2:])
-        out_k, out_v = (_new(side, torch.empty, like, dtype=dtype, device=k_cache.device) if x is None else x
-                        for x in (out_k, out_v))
+        if _is(k_cache, 4):
+            like = (max(0, tokens), *k_cache.shape[2:])
+            out_k, out_v = (_new(side, torch.empty, like, dtype=dtype, device=k_cache.device) if x is None else x
+                            for x in (out_k, out_v))
     return native().load8(k_cache, v_cache, k_scale, v_scale, block_table, starts, cu_seqlens, tokens, out_k, out_v,
                           code, stream)
 
@@ -91,11 +97,12 @@ def attn_decode8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens, ma
     least ``decode_workspace_size(...)`` bytes."""
     if stream is not None:
         stream, side = _on(stream, q)
-        if out is None:
+        fits = _is(q, 3) and _is(k_cache, 4) and _is(block_table, 2)
+        if out is None and fits:
             out = _new(side, torch.empty_like, q)
-        if lse is None:
+        if lse is None and fits:
             lse = _new(side, torch.empty, q.shape[:2], dtype=torch.float32, device=q.device)
-        if workspace is None:
+        if workspace is None and fits:
             most = block_table.shape[1] * k_cache.shape[1] if max_seqlen is None else max_seqlen
             need = decode_workspace_size(*q.shape[:2], k_cache.shape[2], q.shape[2], most)
             workspace = _new(side, torch.empty, max(need, 256), dtype=torch.uint8, device=q.device)

@@ -10,7 +10,7 @@ import functools
 import torch
 
 from .binding import _new, lib
-from .cache8 import _on, native
+from .cache8 import _is, _on, native
 
 
 @functools.lru_cache(maxsize=256)
@@ -37,14 +37,15 @@ def attn_cache_fork(block_table, seqlens, refs, page_size: int, parents=None, ro
     """
     if stream is not None:
         stream, side = _on(stream, block_table)
-        rows, width = block_table.shape
-        make = functools.partial(_new, side, torch.empty, device=block_table.device)
-        if copies is None:
-            copies = make((rows if share else rows * width, 2), dtype=torch.int32)
-        if counts is None:
-            counts = make(2, dtype=torch.int32)
-        if workspace is None:
-            workspace = make(max(fork_workspace_size(rows, width, refs.shape[0]), 256), dtype=torch.uint8)
+        if _is(block_table, 2) and _is(refs, 1):
+            rows, width = block_table.shape
+            make = functools.partial(_new, side, torch.empty, device=block_table.device)
+            if copies is None:
+                copies = make((rows if share else rows * width, 2), dtype=torch.int32)
+            if counts is None:
+                counts = make(2, dtype=torch.int32)
+            if workspace is None:
+                workspace = make(max(fork_workspace_size(rows, width, refs.shape[0]), 256), dtype=torch.uint8)
     return native().fork(block_table, seqlens, refs, page_size, parents, room, share, table_out, seqlens_out, refs_out,
                          copies, counts, workspace, stream)
 
