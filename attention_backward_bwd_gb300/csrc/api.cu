@@ -505,7 +505,7 @@ int attn_check_device_status(attn_stream_t stream) {
     return fail(ATTN_ERR_ARG, "device-side check of a serving call:%s%s%s%s%s",
                 (v[2] & kBadPage) ? " a block_table entry names no page;" : "",
                 (v[2] & kBadLength) ? " a length or slot of seqlens is out of range;" : "",
-                (v[2] & kBadOffsets) ? " cu_seqlens of an append" : "",
+                (v[2] & kBadOffsets) ? " cu_seqlens of an append or a read-back;" : "",
                 (v[2] & kBadParent) ? " a parent of a fork is out of range;" : "",
                 (v[2] & kNoPage) ? " no free page is left" : "");
   return fail(ATTN_ERR_DEVICE_TIMEOUT, "a bounded device wait gave up (site 0x%08x)", v[0]);

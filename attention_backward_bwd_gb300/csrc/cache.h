@@ -26,7 +26,7 @@ struct FastDiv {
 // Bits of the device status word of these operators (status_word()[2]).
 constexpr unsigned int kBadLength = 1u;   // seqlens / slots out of range
 constexpr unsigned int kBadPage = 2u;     // block_table entry outside [0, num_pages)
-constexpr unsigned int kBadOffsets = 4u;  // cu_seqlens of an append
+constexpr unsigned int kBadOffsets = 4u;  // cu_seqlens of an append or a read-back
 constexpr unsigned int kBadParent = 8u;   // parents of a fork
 constexpr unsigned int kNoPage = 16u;     // no free page left for a fork
 
