@@ -13,9 +13,9 @@
 // the turns of the tokens, and the rows stay in registers as they came: they are turned once for
 // their largest value and once more when they are rounded, so that k and v are read once.
 // Warps share the tokens of a row of heads where they are more; what is beyond that, too, is read a
-// second time, from the L2.  It is bound by its instructions: of 17400 tokens of 16 + 16 heads of 96
-// (84 us for a floor of 39) issue slots are busy for 54 % of the time, with 16 warps an SM, which is
-// what 128 registers leave.  (Eight chunks a lane and three blocks an SM: 110 us; rows behind the last
+// second time, from the L2.  Of 19014 tokens of 16 + 16 heads of 96 (85 us for a floor of 43) issue slots
+// are busy for 58 % of the time, which leaves latencies that 16 warps an SM do not cover, as many as
+// 128 registers leave.  (Eight chunks a lane and three blocks an SM: 110 us; rows behind the last
 // one read again in place of zeros: 93; a row of heads for every warp of every block, without the loop
 // over heads: 157.)
 // Read-back.  A warp takes a token: 8 codes a lane, 16 bytes out, so that a warp's stores are whole

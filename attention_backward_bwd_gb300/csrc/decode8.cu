@@ -22,7 +22,7 @@
 // of which a tile takes two where it can: a look-up for 32 keys costs what one for 16 does (with
 // tiles of 128 keys throughout 64 sequences up to 16384 keys took 243 us where 210 with 256).
 //
-// Measured: 64 sequences of 4096 to 16384 keys, 32 query heads on 8 of 128, e4m3 202 to 209 us, 95 to
+// Measured: 64 sequences of 4096 to 16384 keys, 32 query heads on 8 of 128, e4m3 202 to 210 us, 95 to
 // 98 % of the copy bandwidth; one of 131071 keys in int8 53 us (75 %) and e4m3 50.  Beside the bytes there
 // are about 8.5 us of first reads (lengths, table, rows) and of the join.  What it was made faster by,
 // from 285 us: 32 keys looked up at once, the maximum compared by vote and moved only where it

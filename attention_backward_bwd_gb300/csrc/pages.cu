@@ -11,7 +11,7 @@
 // since the copies still read them.  A warp takes kChunk entries of a row.  Small tables and pools are
 // one launch of one cluster, whose barrier parts the steps: bound by their chain, each some loads long.
 // Large ones (kLarge) take a launch a step, with all of the GPU for the references and the rows (512
-// rows of 1025 pages: 84 us in one cluster, 23 in launches).
+// rows of 1001 pages, 770000 entries and pages: 85 us in one cluster, 19 in launches).
 // attn_cache_copy moves whole pages, 16 bytes a thread, several in flight: bound by the memory.
 #include <atomic>
 
@@ -30,7 +30,7 @@ constexpr int kChunk = 32 * kEntries;
 // Rows whose state is kept in shared memory: 12 bytes each, and 8 more for the prefix sums.
 constexpr int kRows = 8192;
 // Entries and pages from which every step has a launch of its own (the cluster and the launches:
-// 6600 11.0 and 11.9 us, 24900 14.7 and 12.4, 95700 37.2 and 14.3).
+// 6600 10.7 and 12.6 us, 23300 15.4 and 13.0, 132000 26.5 and 14.4).
 constexpr int64_t kLarge = 16000;
 
 // Steps of a launch.
@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kForkThreads) copy_refs_kernel(const int* from
 }
 
 constexpr int kCopyThreads = 256;
-// Copies of more than this pass the L2 by, with eight 16-byte pieces of a thread in flight; less is
-// left there, with four (4000 pages of 128 KB 168 us and, the other way, 185; 48 pages of 256 KB
+// Copies of more than this are marked to leave the L2 first, with eight 16-byte pieces of a thread in
+// flight; less stays there, with four (4000 pages of 128 KB 168 us and, the other way, 185; 48 pages of 256 KB
 // 6.3 and 4.4).
 constexpr int64_t kPassing = 64 << 20;
 

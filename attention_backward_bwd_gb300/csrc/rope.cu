@@ -26,7 +26,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;   // row groups of a warp in flight
 // Blocks resident on an SM: halves hold two chunks a row group and eight turns, 128
 // registers; pairs and copies less (16384 tokens of 40 heads of 128, halves: 54.6 us with
-// two blocks, 60.1 with three; pairs, 17400 appended tokens of 32 heads: 84.1 and 79.1).
+// two blocks, 60.1 with three; pairs, 19014 appended tokens of 32 heads: 84.1 and 79.1).
 template <int MODE>
 constexpr int kBlocks = MODE == 1 ? 3 : 2;
 
