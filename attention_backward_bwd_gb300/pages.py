@@ -34,7 +34,8 @@ def attn_cache_fork(block_table, seqlens, refs, page_size: int, parents=None, ro
     ``seqlens`` was lowered (rejected tokens) call this before the next append.  Fresh pages are the lowest
     unreferenced ones; ``counts`` (int32 [2]): the copies listed, the pages still free.  Run
     ``attn_cache_copy(..., copies, counts)`` for every cache of the table before the next append.
-    attn_cache_evict writes pages that rows share: fork what is to be evicted with ``share=False``.
+    attn_cache_evict writes pages that rows share: fork what is to be evicted with ``share=False`` from
+    the start.
     """
     if stream is not None:
         stream, side = _on(stream, block_table)

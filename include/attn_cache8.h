@@ -104,8 +104,9 @@ int attn_decode8(const attn_tensor* q, const attn_tensor* o, float* lse, int dty
  * are not allowed.  rows * max_pages and num_pages stay below 2^31 - 2^20.  workspace:
  * attn_cache_fork_workspace_size bytes, 256-byte aligned, not shared by calls that may overlap.  The
  * copies have to run (attn_cache_copy, for every cache of the table) before anything is appended.
- * attn_cache_evict moves slots within all pages of a sequence, also those that others share: fork
- * with share == 0 what is to be evicted.  Per-slot state (weights, slot positions) is the caller's to
+ * attn_cache_evict moves slots within all pages of a sequence, also those that others share: rows that
+ * are to be evicted are forked with share == 0 from the start (a row that goes on keeps the full pages
+ * that it shares already, whatever share is).  Per-slot state (weights, slot positions) is the caller's to
  * reorder.
  */
 size_t attn_cache_fork_workspace_size(int rows, int max_pages, int num_pages);
